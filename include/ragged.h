@@ -66,6 +66,8 @@ typedef enum ragged_dtype {
 /* Bits of the per-device status word (ragged_get_device_status). */
 #define RAGGED_DEV_BAD_SEQLENS 0x1u /* cu_seqlens decreasing, or a length > max_seqlen */
 #define RAGGED_DEV_TIMEOUT 0x2u     /* a bounded device-side wait gave up              */
+#define RAGGED_DEV_BAD_BUCKETS 0x4u /* a bucket outside the bias table                 */
+#define RAGGED_DEV_CAPACITY 0x8u    /* more rows to write than the output holds        */
 
 /* Largest L_full accepted by pack/unpack and max_seqlen by attention. */
 #define RAGGED_MAX_TOKENS 16384
@@ -370,6 +372,150 @@ RAGGED_API ragged_status ragged_pipeline_graph_create(const void *dense_qkv, con
                                                       ragged_pipeline_graph **graph_out);
 RAGGED_API ragged_status ragged_pipeline_graph_launch(ragged_pipeline_graph *graph, void *stream, uint32_t flags);
 RAGGED_API ragged_status ragged_pipeline_graph_destroy(ragged_pipeline_graph *graph);
+
+/*
+ * Attention with a learned relative position bias, its gradients, and the
+ * attention weight that every token collects.
+ *
+ * ragged_bias_attn describes one problem.  Sequence b has the query rows
+ * cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 and the key / value rows
+ * cu_seqlens_k[b] .. ; query head h reads key / value head h / (H / Hkv).
+ * With integer positions p of the tokens and D = max_distance:
+ *
+ *     s[i, j] = scale q_i . k_j + table[buckets[clamp(p_j - p_i, -D, D) + D], h]
+ *     out_i   = sum_j exp(s[i, j] - lse_i) v_j,   lse_i = log sum_j exp(s[i, j])
+ *
+ * Positions belong to the tokens, so tokens that survive pruning or eviction
+ * keep their bias: pos is what ragged_pack's src_idx (modulo L_full) or
+ * ragged_evict's pos_out gives.  A query row whose sequence has no keys, or
+ * whose scores are all -inf, gets out = 0 and lse = -inf, and passes no
+ * gradient.  Rows past the last sequence are neither read nor written.
+ *
+ *   q                device; element (t, h, c) at q[t * q_tok_stride + h *
+ *                    q_head_stride + c].  16-byte aligned, as are both strides
+ *                    (q_head_stride is not used when H is 1).
+ *   k, v             device; the same with kv_tok_stride, kv_head_stride and
+ *                    Hkv heads.  v is not used by ragged_attn_weight.
+ *   cu_seqlens_q, cu_seqlens_k   device int32 [B + 1], non-decreasing.  The
+ *                    same array for self-attention.
+ *   max_seqlen_q, max_seqlen_k   host-side bounds on the lengths, 1 ..
+ *                    RAGGED_MAX_TOKENS; a sequence longer than its bound is
+ *                    skipped and RAGGED_DEV_BAD_SEQLENS is set.
+ *   B                0 .. 65535 sequences;  H 1 .. 65534, a multiple of Hkv;
+ *                    head_dim 64;  scale positive and finite.
+ *   dtype            RAGGED_F16 or RAGGED_BF16: q, k, v, out, the gradients,
+ *                    table and dtable.  Scores, softmax and sums are fp32.
+ *   table            device [num_buckets, H], contiguous; 1 <= num_buckets <= 64.
+ *   buckets          device int32 [2 * max_distance + 1], 0 <= max_distance
+ *                    <= 1024 (ragged_rel_buckets gives one).  An entry outside
+ *                    [0, num_buckets) sets RAGGED_DEV_BAD_BUCKETS; its pairs
+ *                    get no bias and pass no gradient to the table.
+ *   pos_q, pos_k     device int32 per row (any order, magnitudes up to 2^30),
+ *                    or NULL: key j of a sequence is at position j, and its
+ *                    queries are the last ones: query i at i + L_k - L_q.
+ *   lse              device float; lse[h * lse_stride + t].  Written by
+ *                    ragged_attn_bias_fwd, read by the others.  lse_stride is
+ *                    at least the number of query rows (cu_seqlens_q[B]).
+ */
+typedef struct ragged_bias_attn {
+    const void *q, *k, *v;
+    int64_t q_tok_stride, q_head_stride, kv_tok_stride, kv_head_stride;
+    const int32_t *cu_seqlens_q, *cu_seqlens_k;
+    int64_t B, max_seqlen_q, max_seqlen_k, H, Hkv, head_dim;
+    const void *table;
+    const int32_t *buckets;
+    int64_t num_buckets, max_distance;
+    const int32_t *pos_q, *pos_k;
+    float *lse;
+    int64_t lse_stride;
+    float scale;
+    ragged_dtype dtype;
+} ragged_bias_attn;
+
+/*
+ * ragged_rel_buckets - buckets of the relative distances -D .. D on the host.
+ * n = num_buckets (half of it for each direction when bidirectional; then the
+ * upper half holds the keys after the query).  Distances below n / 2 have a
+ * bucket each; the others share n - n / 2 buckets spaced by the logarithm up
+ * to D: e + floor(log(d / e) / log(D / e) * (n - e)) with e = n / 2, decided
+ * in whole numbers, and distances from D on the last one (min(d, n - 1) where
+ * D <= e leaves no room for a logarithm).  Not bidirectional:
+ * keys after the query count as distance 0.  host_out: 2 * max_distance + 1
+ * values in host memory.
+ */
+RAGGED_API ragged_status ragged_rel_buckets(int64_t num_buckets, int64_t max_distance, int32_t bidirectional,
+                                            int32_t *host_out);
+
+/*
+ * ragged_attn_bias_fwd - writes out (element (t, h, c) at out[t *
+ * out_tok_stride + h * 64 + c], out_tok_stride >= H * 64, 16-byte aligned) and
+ * lse.  workspace: device scratch of the size that
+ * ragged_attn_bias_fwd_workspace reports (0: may be NULL), 16-byte aligned, of
+ * this call alone until its work has finished; nothing in it is kept.
+ */
+RAGGED_API ragged_status ragged_attn_bias_fwd_workspace(const ragged_bias_attn *problem, int64_t *bytes);
+RAGGED_API ragged_status ragged_attn_bias_fwd(const ragged_bias_attn *problem, void *out, int64_t out_tok_stride,
+                                              void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * ragged_attn_bias_bwd - gradients of q, k, v and table from dout, with out
+ * and lse as ragged_attn_bias_fwd wrote them:
+ *     P = exp(s - lse),  dS = P (dout v^T - rowsum(dout out)),
+ *     dq = scale dS k,  dk = scale dS^T q,  dv = P^T dout,
+ *     dtable[n, h] = sum of dS over the pairs of head h in bucket n
+ * (dk and dv summed over the query heads of their head; dtable over the whole
+ * batch).  Every sum is taken in a fixed order.  dq, dk and dv have strides of
+ * their own (dk and dv share theirs) and cover the rows of the sequences only;
+ * dtable is [num_buckets, H], contiguous.  workspace as above.
+ */
+RAGGED_API ragged_status ragged_attn_bias_bwd_workspace(const ragged_bias_attn *problem, int64_t *bytes);
+RAGGED_API ragged_status ragged_attn_bias_bwd(const ragged_bias_attn *problem, const void *out, int64_t out_tok_stride,
+                                              const void *dout, int64_t dout_tok_stride, void *dq,
+                                              int64_t dq_tok_stride, int64_t dq_head_stride, void *dk, void *dv,
+                                              int64_t dkv_tok_stride, int64_t dkv_head_stride, void *dtable,
+                                              void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * ragged_attn_weight - the attention weight that every token collects:
+ *     weight[h, j] = prev[h, j] + sum_i exp(s[i, j] - lse_i)
+ * over the queries of its sequence, with lse as ragged_attn_bias_fwd wrote it.
+ * weight and prev: device float, element [h * weight_stride + key row]; prev
+ * may be NULL (0) or weight itself.  weight_stride is at least the number of
+ * key rows.
+ */
+RAGGED_API ragged_status ragged_attn_weight(const ragged_bias_attn *problem, const float *prev, float *weight,
+                                            int64_t weight_stride, void *stream);
+
+/*
+ * ragged_evict - keeps the tokens with the largest attention weight and packs
+ * them, from a ragged buffer to a ragged buffer.  Sequence b (L_b rows) keeps
+ * m_b = clamp(budget[b], 0, L_b) of them, in their order: first its first
+ * `sinks` and last `recents` tokens, then those with the largest total over
+ * the heads, fp32(sum_h weight[h, t]) summed in fp64.  Ties go to the lower
+ * index; NaN ranks below every number.
+ *
+ *   rows          device rows of row_bytes (a multiple of 16), 16-byte aligned;
+ *                 or NULL with rows_out NULL: only the selection.
+ *   weight        device float [H, weight_stride], as ragged_attn_weight writes.
+ *   cu_seqlens    device int32 [B + 1], 0 <= B <= 65535;  1 <= max_seqlen <=
+ *                 RAGGED_MAX_TOKENS bounds every L_b (a longer sequence keeps
+ *                 nothing and sets RAGGED_DEV_BAD_SEQLENS).
+ *   budget        device int32 [B].
+ *   pos           device int32 per row or NULL (a token's place in its sequence).
+ *   capacity      rows that the outputs hold; kept rows past it are not written
+ *                 and set RAGGED_DEV_CAPACITY.
+ *   rows_out      kept row o is input row src_idx[o];
+ *   cu_out        int32 [B + 1]: cu_out[b+1] = cu_out[b] + m_b;
+ *   src_idx       int32 [capacity];
+ *   weight_out    float [H, weight_out_stride >= capacity] or NULL;
+ *   pos_out       int32 [capacity] or NULL.
+ * Outputs must not overlap inputs.  Rows past cu_out[B] are not written.
+ */
+RAGGED_API ragged_status ragged_evict(const void *rows, int64_t row_bytes, const float *weight, int64_t weight_stride,
+                                      int64_t H, const int32_t *cu_seqlens, int64_t B, int64_t max_seqlen,
+                                      const int32_t *budget, int64_t sinks, int64_t recents, const int32_t *pos,
+                                      int64_t capacity, void *rows_out, int32_t *cu_out, int32_t *src_idx,
+                                      float *weight_out, int64_t weight_out_stride, int32_t *pos_out, void *stream);
 
 /*
  * ragged_get_device_status - read and clear the status word of the current

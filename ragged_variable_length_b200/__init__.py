@@ -13,6 +13,11 @@ Entry points (same names as the C ABI):
   ragged_pipeline    pack -> attend -> CLS in one host call
   ragged_mask_l2     Threshold-l2 keep mask from token feature norms
   ragged_pack_topk   top-k keep selection by score fused into pack
+  ragged_attn_bias_fwd   attention with a learned relative position bias, and
+  ragged_attn_bias_bwd   its gradients (q, k, v and the bias table)
+  ragged_attn_weight  the attention weight that every token collects
+  ragged_evict       keep the tokens with the largest weight, ragged to ragged
+  ragged_rel_buckets  buckets of the relative distances for the bias table
   ragged_pipeline_noalloc  the two-launch pipeline with its packed q/k/v in a
                      fixed library array, for callers that cannot allocate
 ``Pipeline`` keeps the buffers and the marshalled arguments of one shape so
@@ -37,6 +42,8 @@ RAGGED_ERR_CUDA = 3
 RAGGED_ERR_DEVICE = 4
 RAGGED_DEV_BAD_SEQLENS = 0x1
 RAGGED_DEV_TIMEOUT = 0x2
+RAGGED_DEV_BAD_BUCKETS = 0x4
+RAGGED_DEV_CAPACITY = 0x8
 RAGGED_MAX_TOKENS = 16384
 RAGGED_NOALLOC_SCRATCH_BYTES = 16 << 20
 RAGGED_PIPELINE_AUTO = 0
@@ -57,13 +64,27 @@ EXPORTS = ("ragged_pack", "ragged_attn_fwd", "ragged_unpack_cls", "ragged_unpack
            "ragged_pipeline", "ragged_get_device_status", "ragged_status_string",
            "ragged_last_error", "ragged_abi_version", "ragged_set_attn_kernel",
            "ragged_mask_l2", "ragged_pack_topk", "ragged_pipeline_noalloc", "ragged_pipeline_graph_create",
-           "ragged_pipeline_graph_launch", "ragged_pipeline_graph_destroy")
+           "ragged_pipeline_graph_launch", "ragged_pipeline_graph_destroy",
+           "ragged_rel_buckets", "ragged_attn_bias_fwd_workspace", "ragged_attn_bias_fwd",
+           "ragged_attn_bias_bwd_workspace", "ragged_attn_bias_bwd", "ragged_attn_weight", "ragged_evict")
 
 
 class RaggedError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{message} (status {status})")
         self.status = status
+
+
+class BiasAttn(ctypes.Structure):
+    """struct ragged_bias_attn of include/ragged.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v")] +
+                [(n, ctypes.c_int64) for n in ("q_tok_stride", "q_head_stride", "kv_tok_stride", "kv_head_stride")] +
+                [(n, ctypes.c_void_p) for n in ("cu_seqlens_q", "cu_seqlens_k")] +
+                [(n, ctypes.c_int64) for n in ("B", "max_seqlen_q", "max_seqlen_k", "H", "Hkv", "head_dim")] +
+                [(n, ctypes.c_void_p) for n in ("table", "buckets")] +
+                [(n, ctypes.c_int64) for n in ("num_buckets", "max_distance")] +
+                [(n, ctypes.c_void_p) for n in ("pos_q", "pos_k", "lse")] +
+                [("lse_stride", ctypes.c_int64), ("scale", ctypes.c_float), ("dtype", ctypes.c_int)])
 
 
 _lib = None
@@ -92,6 +113,17 @@ def load(path: Optional[str] = None):
     lib.ragged_pipeline_graph_launch.argtypes = [vp, vp, ctypes.c_uint32]
     lib.ragged_pipeline_graph_destroy.argtypes = [vp]
     lib.ragged_get_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
+    problem, size = ctypes.POINTER(BiasAttn), ctypes.POINTER(i64)
+    lib.ragged_rel_buckets.argtypes = [i64, i64, i32, vp]
+    lib.ragged_attn_bias_fwd_workspace.argtypes = [problem, size]
+    lib.ragged_attn_bias_fwd.argtypes = [problem, vp, i64, vp, i64, vp]
+    lib.ragged_attn_bias_bwd_workspace.argtypes = [problem, size]
+    lib.ragged_attn_bias_bwd.argtypes = [problem, vp, i64, vp, i64, vp, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp]
+    lib.ragged_attn_weight.argtypes = [problem, vp, vp, i64, vp]
+    lib.ragged_evict.argtypes = [vp, i64, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp]
+    for name in ("ragged_rel_buckets", "ragged_attn_bias_fwd_workspace", "ragged_attn_bias_fwd",
+                 "ragged_attn_bias_bwd_workspace", "ragged_attn_bias_bwd", "ragged_attn_weight", "ragged_evict"):
+        getattr(lib, name).restype = ctypes.c_int
     for name in ("ragged_pack", "ragged_attn_fwd", "ragged_unpack_cls", "ragged_unpack",
                  "ragged_pipeline", "ragged_get_device_status", "ragged_pipeline_noalloc",
                  "ragged_pipeline_graph_create", "ragged_pipeline_graph_launch", "ragged_pipeline_graph_destroy"):
@@ -309,6 +341,233 @@ def ragged_get_device_status(stream=None) -> int:
     val = ctypes.c_uint32(0)
     _check(load().ragged_get_device_status(ctypes.byref(val), _stream(stream)))
     return int(val.value)
+
+
+def ragged_rel_buckets(num_buckets: int, max_distance: int, bidirectional: bool = True, device="cuda") -> torch.Tensor:
+    """Bucket of every relative distance -max_distance .. max_distance (key position
+    minus query position): int32 [2 * max_distance + 1] for the ``buckets`` argument below."""
+    out = torch.empty(max(1, 2 * int(max_distance) + 1), dtype=torch.int32)
+    _check(load().ragged_rel_buckets(int(num_buckets), int(max_distance), int(bidirectional), out.data_ptr()))
+    return out.to(device)
+
+
+def _on_stream(stream):
+    """Context in which tensors are allocated for, and work goes to, `stream`."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _same_device(*tensors) -> None:
+    """One device for all, and the current one: the library launches there."""
+    index = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"a tensor is on {t.device}, not on the current CUDA device {index}")
+
+
+def _int32(t: Optional[torch.Tensor], n: Optional[int], what: str) -> None:
+    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or
+                          (n is not None and t.shape[0] != n)):
+        raise ValueError(f"{what} must be contiguous int32" + ("" if n is None else f" [{n}]"))
+
+
+def _bias_problem(q, k, v, cu_q, cu_k, max_q, max_k, table, buckets, pos_q, pos_k, scale, lse) -> BiasAttn:
+    """The checked problem of the three attention operators with a position bias (v: k where it is not read)."""
+    (Tq, H, d), (Tk, Hkv, dk) = q.shape, k.shape
+    dt = q.dtype
+    qs, ks = q.stride(), k.stride()
+    if v.shape != k.shape or dk != d or k.dtype != dt or v.dtype != dt or table.dtype != dt:
+        raise ValueError("q [Tq, H, d], k and v [Tk, Hkv, d] and table must have one dtype and head_dim")
+    if qs[2] != 1 or ks[2] != 1 or v.stride() != ks:
+        raise ValueError("q, k and v need a unit innermost stride, and k and v the same strides")
+    if table.dim() != 2 or table.shape[1] != H or not table.is_contiguous():
+        raise ValueError("table must be contiguous [num_buckets, H]")
+    if cu_q.shape != cu_k.shape:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must have the same length")
+    _int32(cu_q, None, "cu_seqlens_q")
+    _int32(cu_k, None, "cu_seqlens_k")
+    _int32(buckets, None, "buckets")
+    if buckets.shape[0] % 2 == 0:
+        raise ValueError("buckets must have an odd length, 2 * max_distance + 1")
+    if pos_q is not None:
+        _int32(pos_q, Tq, "pos_q")
+    if pos_k is not None:
+        _int32(pos_k, Tk, "pos_k")
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (H, Tq) or (Tq > 1 and lse.stride(1) != 1):
+        raise ValueError("lse must be float32 [H, Tq] with unit innermost stride")
+    _same_device(q, k, v, cu_q, cu_k, table, buckets, pos_q, pos_k, lse)
+    some = cu_q.data_ptr()   # stands for the address of a tensor without elements, which is never read
+    return BiasAttn(q.data_ptr() or some, k.data_ptr() or some, v.data_ptr() or some, qs[0], qs[1], ks[0], ks[1],
+                    some, cu_k.data_ptr(), cu_q.shape[0] - 1, max_q, max_k, H, Hkv, d, table.data_ptr(),
+                    buckets.data_ptr(), table.shape[0], buckets.shape[0] // 2, _ptr(pos_q), _ptr(pos_k),
+                    lse.data_ptr() or some, lse.stride(0) if Tq else 0, d ** -0.5 if scale is None else scale,
+                    _dtype_code(q))
+
+
+def _workspace(sizer, problem, like: torch.Tensor):
+    """Scratch of one call from torch's allocator: (tensor or None, address, bytes)."""
+    n = ctypes.c_int64(0)
+    _check(sizer(problem, n))
+    if n.value == 0:
+        return None, None, 0
+    t = torch.empty(n.value, dtype=torch.uint8, device=like.device)
+    return t, t.data_ptr(), n.value
+
+
+def _heads(t: torch.Tensor, like: torch.Tensor, what: str) -> None:
+    if t.shape != like.shape or t.dtype != like.dtype or t.stride(2) != 1:
+        raise ValueError(f"{what} must have the shape and dtype of its input and a unit innermost stride")
+
+
+def _rows_of_heads(t: torch.Tensor, like: torch.Tensor, what: str) -> None:
+    _heads(t, like, what)
+    if t.shape[1] > 1 and t.stride(1) != t.shape[2]:
+        raise ValueError(f"{what} must be [T, H, head_dim] with contiguous heads")
+
+
+def ragged_attn_bias_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                         cu_seqlens_k: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int, table: torch.Tensor,
+                         buckets: torch.Tensor, pos_q: Optional[torch.Tensor] = None,
+                         pos_k: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                         out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None):
+    """Attention of ragged queries q [Tq, H, 64] over ragged keys and values [Tk, Hkv, 64] with the
+    learned bias table [num_buckets, H] (bucket of the clamped relative position) -> (out [Tq, H, 64],
+    lse float32 [H, Tq]).  f16 / bf16.  For self-attention pass the same cu_seqlens and positions twice;
+    without positions a sequence's queries are its last tokens (one new token against a cache)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return ragged_attn_bias_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table,
+                                        buckets, pos_q, pos_k, scale, out, lse)
+    Tq, H, d = q.shape
+    if out is None:
+        out = torch.empty((Tq, H, d), dtype=q.dtype, device=q.device)
+    else:
+        _rows_of_heads(out, q, "out")
+        _same_device(out)
+    if lse is None:
+        lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
+    p = _bias_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table, buckets, pos_q, pos_k,
+                      scale, lse)
+    lib = load()
+    ws, addr, size = _workspace(lib.ragged_attn_bias_fwd_workspace, p, q)
+    _check(lib.ragged_attn_bias_fwd(p, out.data_ptr() or p.cu_seqlens_q, out.stride(0) if Tq else H * d, addr, size,
+                                    _stream(None)))
+    return out, lse
+
+
+def ragged_attn_bias_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                         lse: torch.Tensor, cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor, max_seqlen_q: int,
+                         max_seqlen_k: int, table: torch.Tensor, buckets: torch.Tensor,
+                         pos_q: Optional[torch.Tensor] = None, pos_k: Optional[torch.Tensor] = None,
+                         scale: Optional[float] = None, dq: Optional[torch.Tensor] = None,
+                         dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
+                         dtable: Optional[torch.Tensor] = None, stream=None):
+    """Gradients (dq, dk, dv, dtable) of ragged_attn_bias_fwd from dout [Tq, H, 64], with its out and lse.
+    dq, dk and dv may be strided views (the slices of one fused gradient); rows past the last sequence
+    are left as they were."""
+    if stream is not None:
+        with _on_stream(stream):
+            return ragged_attn_bias_bwd(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                                        max_seqlen_k, table, buckets, pos_q, pos_k, scale, dq, dk, dv, dtable)
+    Tq, H, d = q.shape
+    _rows_of_heads(out, q, "out")
+    if dout.shape != q.shape or dout.dtype != q.dtype:
+        raise ValueError("dout must have the shape and dtype of out")
+    if dout.stride(2) != 1 or (H > 1 and dout.stride(1) != d) or (Tq > 1 and dout.stride(0) < H * d):
+        dout = dout.contiguous()   # a broadcast or transposed gradient
+    dq = torch.empty((Tq, H, d), dtype=q.dtype, device=q.device) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
+    dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
+    dtable = torch.empty(table.shape, dtype=table.dtype, device=table.device) if dtable is None else dtable
+    _heads(dq, q, "dq")
+    _heads(dk, k, "dk")
+    _heads(dv, v, "dv")
+    if dk.shape[0] and dk.stride() != dv.stride():
+        raise ValueError("dk and dv must have the same strides")
+    if dtable.shape != table.shape or dtable.dtype != table.dtype or not dtable.is_contiguous():
+        raise ValueError("dtable must be contiguous with the shape and dtype of table")
+    _same_device(dout, out, dq, dk, dv, dtable)
+    p = _bias_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table, buckets, pos_q, pos_k,
+                      scale, lse)
+    lib = load()
+    ws, addr, size = _workspace(lib.ragged_attn_bias_bwd_workspace, p, q)
+    some = p.cu_seqlens_q
+    _check(lib.ragged_attn_bias_bwd(p, out.data_ptr() or some, out.stride(0) if Tq > 1 else H * d,
+                                    dout.data_ptr() or some, dout.stride(0) if Tq > 1 else H * d,
+                                    dq.data_ptr() or some, dq.stride(0), dq.stride(1), dk.data_ptr() or some,
+                                    dv.data_ptr() or some, dk.stride(0), dk.stride(1), dtable.data_ptr(), addr, size,
+                                    _stream(None)))
+    return dq, dk, dv, dtable
+
+
+def ragged_attn_weight(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                       cu_seqlens_k: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int, table: torch.Tensor,
+                       buckets: torch.Tensor, pos_q: Optional[torch.Tensor] = None,
+                       pos_k: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                       prev: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """Attention weight that every token collects: weight[h, j] = prev[h, j] + sum_i exp(s[i, j] - lse_i),
+    float32 [H, Tk], with the lse of ragged_attn_bias_fwd.  weight=prev adds in place."""
+    if stream is not None:
+        with _on_stream(stream):
+            return ragged_attn_weight(q, k, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table,
+                                      buckets, pos_q, pos_k, scale, prev, weight)
+    H, Tk = q.shape[1], k.shape[0]
+    if weight is None:
+        weight = torch.empty((H, Tk), dtype=torch.float32, device=k.device)
+    ws = weight.stride(0) if H > 1 else Tk
+    for t, what in ((weight, "weight"), (prev, "prev")):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (H, Tk) or (Tk > 1 and t.stride(1) != 1) or
+                              (H > 1 and t.stride(0) != ws)):
+            raise ValueError(f"{what} must be float32 [H, Tk] with unit innermost stride, prev as weight")
+    _same_device(weight, prev)
+    p = _bias_problem(q, k, k, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table, buckets, pos_q, pos_k,
+                      scale, lse)
+    _check(load().ragged_attn_weight(p, _ptr(prev) or None, weight.data_ptr() or p.cu_seqlens_q, ws, _stream(None)))
+    return weight
+
+
+def ragged_evict(rows: Optional[torch.Tensor], weight: torch.Tensor, cu_seqlens: torch.Tensor, max_seqlen: int,
+                 budget: torch.Tensor, sinks: int = 1, recents: int = 0, pos: Optional[torch.Tensor] = None,
+                 total: Optional[int] = None, stream=None):
+    """Keeps budget[b] tokens of every sequence: the first `sinks`, the last `recents`, then those with the
+    largest weight [H, T] summed over the heads (ties: the lower index), in their order
+    -> (rows_out, cu_out, src_idx, weight_out, pos_out).
+
+    rows [T, ...] contiguous with a multiple of 16 bytes per token, or None.  The outputs have `total` rows
+    (default T); rows past cu_out[B] are not written, and kept rows past `total` are dropped and flagged.
+    src_idx is the input row of every kept one, pos_out its position (pos, or its place in the sequence)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return ragged_evict(rows, weight, cu_seqlens, max_seqlen, budget, sinks, recents, pos, total)
+    H, T = weight.shape
+    B = cu_seqlens.shape[0] - 1
+    if weight.dtype != torch.float32 or (T > 1 and weight.stride(1) != 1):
+        raise ValueError("weight must be float32 [H, T] with unit innermost stride")
+    if rows is not None and (rows.shape[0] != T or not rows.is_contiguous()):
+        raise ValueError("rows must be contiguous [T, ...]")
+    _int32(cu_seqlens, None, "cu_seqlens")
+    _int32(budget, B, "budget")
+    if pos is not None:
+        _int32(pos, T, "pos")
+    _same_device(rows, weight, cu_seqlens, budget, pos)
+    n = T if total is None else int(total)
+    dev = weight.device
+    rows_out = None if rows is None else torch.empty((n,) + tuple(rows.shape[1:]), dtype=rows.dtype, device=dev)
+    ints = torch.empty(2 * n + B + 1, dtype=torch.int32, device=dev)
+    cu_out, src_idx, pos_out = ints[:B + 1], ints[B + 1:B + 1 + n], ints[B + 1 + n:]
+    weight_out = torch.empty((H, n), dtype=torch.float32, device=dev)
+    copy = rows is not None and n > 0 and T > 0
+    row_bytes = rows.stride(0) * rows.element_size() if copy else 0
+    some = cu_seqlens.data_ptr()
+    _check(load().ragged_evict(rows.data_ptr() if copy else None, row_bytes, weight.data_ptr() or some,
+                               weight.stride(0) if H > 1 else 0, H, some, B, int(max_seqlen), budget.data_ptr() or some,
+                               int(sinks), int(recents), _ptr(pos) or None, n, rows_out.data_ptr() if copy else None,
+                               cu_out.data_ptr(), src_idx.data_ptr() if n else None,
+                               weight_out.data_ptr() if n else None, n, pos_out.data_ptr() if n else None,
+                               _stream(None)))
+    return rows_out, cu_out, src_idx, weight_out, pos_out
 
 
 class _PipelineArgs(ctypes.Structure):

@@ -1,0 +1,316 @@
+// Host side of the operators with a learned relative position bias and of the
+// eviction (declared in ragged.h).  Included by ragged_api.cu, whose argument
+// helpers (fail, cuda_check, aligned16, ensure_smem) it uses.
+#pragma once
+
+#include "bias_simple.cuh"
+#include "evict.cuh"
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+ragged_status check_stride16(int64_t elements, const char* what) {
+    if (elements <= 0 || elements % 8)
+        return fail(RAGGED_ERR_INVALID_ARG, "%s = %lld must be a positive multiple of 16 bytes", what, (long long)elements);
+    return RAGGED_OK;
+}
+
+// Argument checks shared by the three operators; fills the kernels' view.
+ragged_status check_bias_problem(const ragged_bias_attn* a, bool need_v, ragged::bias::Problem* p) {
+    if (a == nullptr) return fail(RAGGED_ERR_INVALID_ARG, "the problem is NULL");
+    if (a->B < 0) return fail(RAGGED_ERR_INVALID_ARG, "B = %lld is negative", (long long)a->B);
+    if (a->B > 65535) return fail(RAGGED_ERR_UNSUPPORTED, "B = %lld exceeds 65535", (long long)a->B);
+    if (a->dtype != RAGGED_F16 && a->dtype != RAGGED_BF16 && a->dtype != RAGGED_F32)
+        return fail(RAGGED_ERR_INVALID_ARG, "unknown dtype %d", (int)a->dtype);
+    if (a->dtype == RAGGED_F32) return fail(RAGGED_ERR_UNSUPPORTED, "the attention with a position bias takes f16 and bf16");
+    if (a->head_dim != 64)
+        return fail(RAGGED_ERR_UNSUPPORTED, "head_dim = %lld (only 64 is implemented)", (long long)a->head_dim);
+    if (a->H < 1 || a->H > 65534) return fail(RAGGED_ERR_INVALID_ARG, "H = %lld outside [1, 65534]", (long long)a->H);
+    if (a->Hkv < 1 || a->H % a->Hkv)
+        return fail(RAGGED_ERR_INVALID_ARG, "H = %lld is not a multiple of Hkv = %lld", (long long)a->H, (long long)a->Hkv);
+    const int64_t longest[2] = {a->max_seqlen_q, a->max_seqlen_k};
+    for (int64_t n : longest)
+        if (n < 1 || n > RAGGED_MAX_TOKENS)
+            return fail(RAGGED_ERR_INVALID_ARG, "max_seqlen = %lld outside [1, %d]", (long long)n, RAGGED_MAX_TOKENS);
+    if (!(a->scale > 0.f) || a->scale > 3.0e38f)
+        return fail(RAGGED_ERR_INVALID_ARG, "scale must be a positive finite number");
+    if (a->num_buckets < 1 || a->num_buckets > ragged::bias::kMaxBuckets)
+        return fail(RAGGED_ERR_UNSUPPORTED, "num_buckets = %lld outside [1, %d]", (long long)a->num_buckets,
+                    ragged::bias::kMaxBuckets);
+    if (a->max_distance < 0 || a->max_distance > ragged::bias::kMaxDistance)
+        return fail(RAGGED_ERR_UNSUPPORTED, "max_distance = %lld outside [0, %d]", (long long)a->max_distance,
+                    ragged::bias::kMaxDistance);
+    if (a->B > 0) {
+        if (!a->q || !a->k || (need_v && !a->v) || !a->cu_seqlens_q || !a->cu_seqlens_k || !a->table || !a->buckets || !a->lse)
+            return fail(RAGGED_ERR_INVALID_ARG, "q, k, v, cu_seqlens, table, buckets and lse must not be NULL");
+        if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v))
+            return fail(RAGGED_ERR_INVALID_ARG, "q, k and v must be 16-byte aligned");
+        if (!aligned4(a->cu_seqlens_q) || !aligned4(a->cu_seqlens_k) || !aligned4(a->pos_q) || !aligned4(a->pos_k) ||
+            !aligned4(a->buckets) || !aligned4(a->lse))
+            return fail(RAGGED_ERR_INVALID_ARG, "cu_seqlens, positions, buckets and lse must be 4-byte aligned");
+        if (reinterpret_cast<uintptr_t>(a->table) & 1u)
+            return fail(RAGGED_ERR_INVALID_ARG, "table must be 2-byte aligned");
+        ragged_status st = check_stride16(a->q_tok_stride, "q_tok_stride");
+        if (st == RAGGED_OK) st = check_stride16(a->kv_tok_stride, "kv_tok_stride");
+        if (st == RAGGED_OK && a->H > 1) st = check_stride16(a->q_head_stride, "q_head_stride");
+        if (st == RAGGED_OK && a->Hkv > 1) st = check_stride16(a->kv_head_stride, "kv_head_stride");
+        if (st != RAGGED_OK) return st;
+        if (a->lse_stride < 0) return fail(RAGGED_ERR_INVALID_ARG, "lse_stride is negative");
+    }
+    *p = ragged::bias::Problem{
+        static_cast<const uint16_t*>(a->q), static_cast<const uint16_t*>(a->k), static_cast<const uint16_t*>(a->v),
+        a->q_tok_stride, a->H > 1 ? a->q_head_stride : 0, a->kv_tok_stride, a->Hkv > 1 ? a->kv_head_stride : 0,
+        a->cu_seqlens_q, a->cu_seqlens_k, a->pos_q, a->pos_k, static_cast<const uint16_t*>(a->table), a->buckets,
+        a->lse, a->lse_stride, static_cast<int>(a->B), static_cast<int>(a->max_seqlen_q), static_cast<int>(a->max_seqlen_k),
+        static_cast<int>(a->H), static_cast<int>(a->Hkv), static_cast<int>(a->H / a->Hkv),
+        static_cast<int>(a->num_buckets), static_cast<int>(a->max_distance), a->scale, a->scale * ragged::bias::kLog2e};
+    return RAGGED_OK;
+}
+
+int64_t tiles128(int64_t n) { return (n + ragged::bias::kQTile - 1) / ragged::bias::kQTile; }
+
+// Workspace of the backward pass: delta [H, lse_stride] floats, then the
+// partial sums of the table's gradient [B, H, query tiles, num_buckets].
+int64_t bwd_delta_floats(const ragged_bias_attn* a) { return (a->H * a->lse_stride + 3) & ~int64_t(3); }
+int64_t bwd_workspace(const ragged_bias_attn* a) {
+    return 4 * (bwd_delta_floats(a) + a->B * a->H * tiles128(a->max_seqlen_q) * a->num_buckets);
+}
+int64_t fwd_workspace(const ragged_bias_attn*) { return 0; }
+
+ragged_status check_workspace(const void* ws, int64_t have, int64_t need) {
+    if (need > 0 && (ws == nullptr || have < need))
+        return fail(RAGGED_ERR_INVALID_ARG, "the workspace holds %lld bytes, %lld are needed", (long long)(ws ? have : 0),
+                    (long long)need);
+    if (need > 0 && !aligned16(ws)) return fail(RAGGED_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
+    return RAGGED_OK;
+}
+
+template <typename T>
+ragged_status launch_bias_fwd(const ragged::bias::Problem& p, uint16_t* out, int64_t out_tok, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>(tiles128(p.max_q)), static_cast<unsigned>(p.H), static_cast<unsigned>(p.B));
+    ragged::bias::bias_fwd_simple<T><<<grid, 128, 0, s>>>(p, out, out_tok);
+    return cuda_check(cudaGetLastError(), "attention (position bias) launch");
+}
+
+template <typename T>
+ragged_status launch_bias_bwd(const ragged::bias::Problem& p, const ragged::bias::BwdArgs& a, cudaStream_t s) {
+    const dim3 gq(static_cast<unsigned>(a.q_tiles), static_cast<unsigned>(p.H), static_cast<unsigned>(p.B));
+    ragged::bias::bias_bwd_q_simple<T><<<gq, 128, 0, s>>>(p, a);
+    ragged_status st = cuda_check(cudaGetLastError(), "query gradient launch");
+    if (st != RAGGED_OK) return st;
+    const dim3 gk(static_cast<unsigned>(tiles128(p.max_k)), static_cast<unsigned>(p.Hkv), static_cast<unsigned>(p.B));
+    ragged::bias::bias_bwd_kv_simple<T><<<gk, 128, 0, s>>>(p, a);
+    st = cuda_check(cudaGetLastError(), "key and value gradient launch");
+    if (st != RAGGED_OK) return st;
+    const dim3 gt(static_cast<unsigned>(p.num_buckets), static_cast<unsigned>(p.H));
+    ragged::bias::bias_bwd_table<T><<<gt, 256, 0, s>>>(p, a);
+    return cuda_check(cudaGetLastError(), "table gradient launch");
+}
+
+template <typename T>
+ragged_status launch_bias_weight(const ragged::bias::Problem& p, const float* prev, float* weight, int64_t stride,
+                                 cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>(tiles128(p.max_k)), static_cast<unsigned>(p.H), static_cast<unsigned>(p.B));
+    ragged::bias::bias_weight_simple<T><<<grid, 128, 0, s>>>(p, prev, weight, stride);
+    return cuda_check(cudaGetLastError(), "attention weight launch");
+}
+
+DeviceFlags g_evict_smem;
+
+// x^a * y^b >= u^c * v^d in whole numbers (up to 64 factors below 2^16 each).
+struct BigUint {
+    uint32_t w[72] = {1};
+    int n = 1;
+    void times(uint32_t f) {
+        uint64_t carry = 0;
+        for (int i = 0; i < n; ++i) {
+            carry += static_cast<uint64_t>(w[i]) * f;
+            w[i] = static_cast<uint32_t>(carry);
+            carry >>= 32;
+        }
+        if (carry) w[n++] = static_cast<uint32_t>(carry);
+    }
+    bool at_least(const BigUint& o) const {
+        if (n != o.n) return n > o.n;
+        for (int i = n - 1; i >= 0; --i)
+            if (w[i] != o.w[i]) return w[i] > o.w[i];
+        return true;
+    }
+};
+
+}  // namespace
+
+extern "C" {
+
+ragged_status ragged_rel_buckets(int64_t num_buckets, int64_t max_distance, int32_t bidirectional, int32_t* host_out) {
+    if (num_buckets < 1 || num_buckets > ragged::bias::kMaxBuckets)
+        return fail(RAGGED_ERR_UNSUPPORTED, "num_buckets = %lld outside [1, %d]", (long long)num_buckets,
+                    ragged::bias::kMaxBuckets);
+    if (max_distance < 0 || max_distance > ragged::bias::kMaxDistance)
+        return fail(RAGGED_ERR_UNSUPPORTED, "max_distance = %lld outside [0, %d]", (long long)max_distance,
+                    ragged::bias::kMaxDistance);
+    if (bidirectional && num_buckets % 2)
+        return fail(RAGGED_ERR_INVALID_ARG, "num_buckets = %lld must be even for both directions", (long long)num_buckets);
+    if (host_out == nullptr) return fail(RAGGED_ERR_INVALID_ARG, "host_out is NULL");
+    const int n = static_cast<int>(bidirectional ? num_buckets / 2 : num_buckets), D = static_cast<int>(max_distance);
+    const int exact = n / 2, m = n - exact;
+    for (int delta = -D; delta <= D; ++delta) {
+        const int d = bidirectional ? (delta < 0 ? -delta : delta) : (delta < 0 ? -delta : 0);
+        int b;
+        if (n == 1) {
+            b = 0;
+        } else if (d < exact) {
+            b = d;
+        } else if (exact >= D) {   // no room for a logarithmic part
+            b = d < n - 1 ? d : n - 1;
+        } else {
+            // exact + the largest k <= m with (D / exact)^k <= (d / exact)^m
+            int k = 0;
+            while (k < m) {
+                BigUint lhs, rhs;
+                for (int i = 0; i <= k; ++i) lhs.times(static_cast<uint32_t>(D));
+                for (int i = 0; i < m; ++i) lhs.times(static_cast<uint32_t>(exact));
+                for (int i = 0; i < m; ++i) rhs.times(static_cast<uint32_t>(d));
+                for (int i = 0; i <= k; ++i) rhs.times(static_cast<uint32_t>(exact));
+                if (!rhs.at_least(lhs)) break;
+                ++k;
+            }
+            b = exact + k < n - 1 ? exact + k : n - 1;
+        }
+        host_out[delta + D] = b + (bidirectional && delta > 0 ? n : 0);
+    }
+    return RAGGED_OK;
+}
+
+ragged_status ragged_attn_bias_fwd_workspace(const ragged_bias_attn* a, int64_t* bytes) {
+    ragged::bias::Problem p;
+    if (bytes == nullptr) return fail(RAGGED_ERR_INVALID_ARG, "bytes is NULL");
+    ragged_status st = check_bias_problem(a, true, &p);
+    if (st != RAGGED_OK) return st;
+    *bytes = fwd_workspace(a);
+    return RAGGED_OK;
+}
+
+ragged_status ragged_attn_bias_fwd(const ragged_bias_attn* a, void* out, int64_t out_tok_stride, void* workspace,
+                                   int64_t workspace_bytes, void* stream) {
+    ragged::bias::Problem p;
+    ragged_status st = check_bias_problem(a, true, &p);
+    if (st != RAGGED_OK || a->B == 0) return st;
+    if (out == nullptr) return fail(RAGGED_ERR_INVALID_ARG, "out must not be NULL");
+    if (!aligned16(out)) return fail(RAGGED_ERR_INVALID_ARG, "out must be 16-byte aligned");
+    if (out_tok_stride < a->H * 64 || out_tok_stride % 8)
+        return fail(RAGGED_ERR_INVALID_ARG, "out_tok_stride must be >= H * head_dim and a multiple of 16 bytes");
+    st = check_workspace(workspace, workspace_bytes, fwd_workspace(a));
+    if (st != RAGGED_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return a->dtype == RAGGED_F16 ? launch_bias_fwd<__half>(p, static_cast<uint16_t*>(out), out_tok_stride, s)
+                                  : launch_bias_fwd<__nv_bfloat16>(p, static_cast<uint16_t*>(out), out_tok_stride, s);
+}
+
+ragged_status ragged_attn_bias_bwd_workspace(const ragged_bias_attn* a, int64_t* bytes) {
+    ragged::bias::Problem p;
+    if (bytes == nullptr) return fail(RAGGED_ERR_INVALID_ARG, "bytes is NULL");
+    ragged_status st = check_bias_problem(a, true, &p);
+    if (st != RAGGED_OK) return st;
+    *bytes = bwd_workspace(a);
+    return RAGGED_OK;
+}
+
+ragged_status ragged_attn_bias_bwd(const ragged_bias_attn* a, const void* out, int64_t out_tok_stride, const void* dout,
+                                   int64_t dout_tok_stride, void* dq, int64_t dq_tok_stride, int64_t dq_head_stride,
+                                   void* dk, void* dv, int64_t dkv_tok_stride, int64_t dkv_head_stride, void* dtable,
+                                   void* workspace, int64_t workspace_bytes, void* stream) {
+    ragged::bias::Problem p;
+    ragged_status st = check_bias_problem(a, true, &p);
+    if (st != RAGGED_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtable == nullptr || (reinterpret_cast<uintptr_t>(dtable) & 1u))
+        return fail(RAGGED_ERR_INVALID_ARG, "dtable must be a 2-byte aligned device pointer");
+    if (a->B == 0)
+        return cuda_check(cudaMemsetAsync(dtable, 0, static_cast<size_t>(a->num_buckets * a->H * 2), s), "cudaMemsetAsync");
+    if (!out || !dout || !dq || !dk || !dv)
+        return fail(RAGGED_ERR_INVALID_ARG, "out, dout, dq, dk and dv must not be NULL");
+    if (!aligned16(out) || !aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+        return fail(RAGGED_ERR_INVALID_ARG, "out, dout, dq, dk and dv must be 16-byte aligned");
+    if (out_tok_stride < a->H * 64 || out_tok_stride % 8 || dout_tok_stride < a->H * 64 || dout_tok_stride % 8)
+        return fail(RAGGED_ERR_INVALID_ARG, "out_tok_stride and dout_tok_stride must be >= H * head_dim and multiples of 16 bytes");
+    st = check_stride16(dq_tok_stride, "dq_tok_stride");
+    if (st == RAGGED_OK) st = check_stride16(dkv_tok_stride, "dkv_tok_stride");
+    if (st == RAGGED_OK && a->H > 1) st = check_stride16(dq_head_stride, "dq_head_stride");
+    if (st == RAGGED_OK && a->Hkv > 1) st = check_stride16(dkv_head_stride, "dkv_head_stride");
+    if (st == RAGGED_OK) st = check_workspace(workspace, workspace_bytes, bwd_workspace(a));
+    if (st != RAGGED_OK) return st;
+    float* ws = static_cast<float*>(workspace);
+    ragged::bias::BwdArgs g{static_cast<const uint16_t*>(out), static_cast<const uint16_t*>(dout), out_tok_stride,
+                            dout_tok_stride, static_cast<uint16_t*>(dq), static_cast<uint16_t*>(dk),
+                            static_cast<uint16_t*>(dv), dq_tok_stride, a->H > 1 ? dq_head_stride : 0, dkv_tok_stride,
+                            a->Hkv > 1 ? dkv_head_stride : 0, ws, ws + bwd_delta_floats(a),
+                            static_cast<uint16_t*>(dtable), static_cast<int>(tiles128(a->max_seqlen_q))};
+    return a->dtype == RAGGED_F16 ? launch_bias_bwd<__half>(p, g, s) : launch_bias_bwd<__nv_bfloat16>(p, g, s);
+}
+
+ragged_status ragged_attn_weight(const ragged_bias_attn* a, const float* prev, float* weight, int64_t weight_stride,
+                                 void* stream) {
+    ragged::bias::Problem p;
+    ragged_status st = check_bias_problem(a, false, &p);
+    if (st != RAGGED_OK || a->B == 0) return st;
+    if (weight == nullptr || !aligned4(weight) || !aligned4(prev))
+        return fail(RAGGED_ERR_INVALID_ARG, "weight must not be NULL; weight and prev must be 4-byte aligned");
+    if (weight_stride < 0) return fail(RAGGED_ERR_INVALID_ARG, "weight_stride is negative");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return a->dtype == RAGGED_F16 ? launch_bias_weight<__half>(p, prev, weight, weight_stride, s)
+                                  : launch_bias_weight<__nv_bfloat16>(p, prev, weight, weight_stride, s);
+}
+
+ragged_status ragged_evict(const void* rows, int64_t row_bytes, const float* weight, int64_t weight_stride, int64_t H,
+                           const int32_t* cu_seqlens, int64_t B, int64_t max_seqlen, const int32_t* budget, int64_t sinks,
+                           int64_t recents, const int32_t* pos, int64_t capacity, void* rows_out, int32_t* cu_out,
+                           int32_t* src_idx, float* weight_out, int64_t weight_out_stride, int32_t* pos_out, void* stream) {
+    if (B < 0) return fail(RAGGED_ERR_INVALID_ARG, "B = %lld is negative", (long long)B);
+    if (B > 65535) return fail(RAGGED_ERR_UNSUPPORTED, "B = %lld exceeds 65535", (long long)B);
+    if (H < 1 || H > 65534) return fail(RAGGED_ERR_INVALID_ARG, "H = %lld outside [1, 65534]", (long long)H);
+    if (max_seqlen < 1 || max_seqlen > RAGGED_MAX_TOKENS)
+        return fail(RAGGED_ERR_INVALID_ARG, "max_seqlen = %lld outside [1, %d]", (long long)max_seqlen, RAGGED_MAX_TOKENS);
+    if (sinks < 0 || recents < 0 || sinks > RAGGED_MAX_TOKENS || recents > RAGGED_MAX_TOKENS)
+        return fail(RAGGED_ERR_INVALID_ARG, "sinks and recents must lie in [0, %d]", RAGGED_MAX_TOKENS);
+    if (capacity < 0 || capacity >= (int64_t(1) << 31))
+        return fail(RAGGED_ERR_INVALID_ARG, "capacity = %lld outside [0, 2^31)", (long long)capacity);
+    if (cu_out == nullptr || !aligned4(cu_out)) return fail(RAGGED_ERR_INVALID_ARG, "cu_out must be a 4-byte aligned device pointer");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (B == 0) return cuda_check(cudaMemsetAsync(cu_out, 0, sizeof(int32_t), s), "cudaMemsetAsync");
+    if (!weight || !cu_seqlens || !budget || (capacity > 0 && !src_idx))
+        return fail(RAGGED_ERR_INVALID_ARG, "weight, cu_seqlens, budget and src_idx must not be NULL");
+    if ((rows == nullptr) != (rows_out == nullptr))
+        return fail(RAGGED_ERR_INVALID_ARG, "rows and rows_out must both be given or both be NULL");
+    if (rows != nullptr) {
+        if (row_bytes <= 0 || row_bytes % 16 || row_bytes / 16 >= (int64_t(1) << 31))
+            return fail(RAGGED_ERR_INVALID_ARG, "row_bytes = %lld must be a positive multiple of 16", (long long)row_bytes);
+        if (!aligned16(rows) || !aligned16(rows_out))
+            return fail(RAGGED_ERR_INVALID_ARG, "rows and rows_out must be 16-byte aligned");
+        if (rows == rows_out) return fail(RAGGED_ERR_INVALID_ARG, "rows_out must not be rows");
+    }
+    if (!aligned4(weight) || !aligned4(cu_seqlens) || !aligned4(budget) || !aligned4(pos) || !aligned4(src_idx) ||
+        !aligned4(weight_out) || !aligned4(pos_out))
+        return fail(RAGGED_ERR_INVALID_ARG, "weights, cu_seqlens, budget, positions and src_idx must be 4-byte aligned");
+    if (weight_out == weight || cu_out == cu_seqlens || (pos != nullptr && pos_out == pos))
+        return fail(RAGGED_ERR_INVALID_ARG, "the outputs must not be the inputs");
+    if (weight_stride < 0 || weight_out_stride < 0 || (weight_out != nullptr && H > 1 && weight_out_stride < capacity))
+        return fail(RAGGED_ERR_INVALID_ARG, "weight strides are too small");
+    ragged::evict::Args a{weight, weight_stride, cu_seqlens, budget, pos, static_cast<int>(B), static_cast<int>(H),
+                          static_cast<int>(max_seqlen), static_cast<int>(sinks), static_cast<int>(recents), capacity,
+                          cu_out, src_idx, pos_out, weight_out, weight_out_stride, static_cast<const uint4*>(rows),
+                          static_cast<uint4*>(rows_out), static_cast<uint32_t>(rows ? row_bytes / 16 : 0)};
+    ragged_status st = ensure_smem(ragged::evict::select_kernel, RAGGED_MAX_TOKENS * 4, g_evict_smem);
+    if (st != RAGGED_OK) return st;
+    ragged::evict::select_kernel<<<static_cast<unsigned>(B), ragged::evict::kThreads, static_cast<size_t>(max_seqlen) * 4, s>>>(a);
+    st = cuda_check(cudaGetLastError(), "evict selection launch");
+    if (st != RAGGED_OK || capacity == 0 || (rows == nullptr && weight_out == nullptr)) return st;
+    const int64_t warps = ragged::evict::kCopyThreads / 32;
+    const int64_t blocks = std::min<int64_t>((capacity + warps - 1) / warps, 16LL * sm_count());
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(weight_out ? 1 + H : 1));
+    ragged::evict::copy_kernel<<<grid, ragged::evict::kCopyThreads, 0, s>>>(a);
+    return cuda_check(cudaGetLastError(), "evict copy launch");
+}
+
+}  // extern "C"

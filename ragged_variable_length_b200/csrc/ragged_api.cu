@@ -786,3 +786,5 @@ ragged_status ragged_pipeline_graph_destroy(ragged_pipeline_graph* graph) {
 }
 
 }  // extern "C"
+
+#include "bias_api.cuh"
