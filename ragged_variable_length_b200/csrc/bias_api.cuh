@@ -3,7 +3,7 @@
 // helpers (fail, cuda_check, aligned16, ensure_smem) it uses.
 #pragma once
 
-#include "bias_simple.cuh"
+#include "bias_bwd.cuh"
 #include "evict.cuh"
 
 namespace {
@@ -70,13 +70,26 @@ ragged_status check_bias_problem(const ragged_bias_attn* a, bool need_v, ragged:
 
 int64_t tiles128(int64_t n) { return (n + ragged::bias::kQTile - 1) / ragged::bias::kQTile; }
 
-// Workspace of the backward pass: delta [H, lse_stride] floats, then the
-// partial sums of the table's gradient [B, H, query tiles, num_buckets].
+// Workspace of the backward pass: delta [H, lse_stride] floats, an exponent per
+// (sequence, head, query tile), then the tiles' sums for the table's gradient
+// [B, H, query tiles, num_buckets].
 int64_t bwd_delta_floats(const ragged_bias_attn* a) { return (a->H * a->lse_stride + 3) & ~int64_t(3); }
+int64_t bwd_items(const ragged_bias_attn* a) { return a->B * a->H * tiles128(a->max_seqlen_q); }
 int64_t bwd_workspace(const ragged_bias_attn* a) {
-    return 4 * (bwd_delta_floats(a) + a->B * a->H * tiles128(a->max_seqlen_q) * a->num_buckets);
+    return 4 * (bwd_delta_floats(a) + bwd_items(a) * (1 + a->num_buckets));
 }
 int64_t fwd_workspace(const ragged_bias_attn*) { return 0; }
+
+// Positions that the query-gradient kernel's expanded table covers: what two
+// CTAs per SM leave room for next to the gradient's sums, unless that is too
+// little to be of use (many buckets, or a far-reaching map): then one CTA.
+constexpr int kTwoPerSm = (228 * 1024) / 2 - 1024 - 2048;   // less the reserved and the static part
+constexpr int bwd_q_span(int D, int num_buckets) {
+    const int entries = (kTwoPerSm - ragged::bias::bwd_q_fixed_bytes(num_buckets) - 32) / 6;
+    const int span = (entries - 1 - ragged::bias::kVecPad) / 2 - D;
+    return span < 256 ? ragged::bias::kSpan : span < ragged::bias::kSpan ? span : ragged::bias::kSpan;
+}
+constexpr int kBwdQSmemMax = ragged::bias::bwd_q_smem_bytes(ragged::bias::kMaxDistance, ragged::bias::kMaxBuckets, ragged::bias::kSpan);
 
 ragged_status check_workspace(const void* ws, int64_t have, int64_t need) {
     if (need > 0 && (ws == nullptr || have < need))
@@ -86,33 +99,47 @@ ragged_status check_workspace(const void* ws, int64_t have, int64_t need) {
     return RAGGED_OK;
 }
 
+DeviceFlags g_bias_fwd_smem[2], g_bias_bwd_q_smem[2], g_bias_bwd_kv_smem[2], g_bias_weight_smem[2];
+template <typename T>
+constexpr int kTypeSlot = std::is_same<T, __half>::value ? 0 : 1;
+
+dim3 bias_grid(int64_t tiles, int heads, int B) {
+    return dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(heads), static_cast<unsigned>(B));
+}
+
 template <typename T>
 ragged_status launch_bias_fwd(const ragged::bias::Problem& p, uint16_t* out, int64_t out_tok, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(tiles128(p.max_q)), static_cast<unsigned>(p.H), static_cast<unsigned>(p.B));
-    ragged::bias::bias_fwd_simple<T><<<grid, 128, 0, s>>>(p, out, out_tok);
+    using namespace ragged::bias;
+    ragged_status st = ensure_smem(bias_fwd_kernel<T>, fwd_smem_bytes(kMaxDistance), g_bias_fwd_smem[kTypeSlot<T>]);
+    if (st != RAGGED_OK) return st;
+    bias_fwd_kernel<T><<<bias_grid(tiles128(p.max_q), p.H, p.B), kThreads, fwd_smem_bytes(p.D), s>>>(p, out, out_tok);
     return cuda_check(cudaGetLastError(), "attention (position bias) launch");
 }
 
 template <typename T>
-ragged_status launch_bias_bwd(const ragged::bias::Problem& p, const ragged::bias::BwdArgs& a, cudaStream_t s) {
-    const dim3 gq(static_cast<unsigned>(a.q_tiles), static_cast<unsigned>(p.H), static_cast<unsigned>(p.B));
-    ragged::bias::bias_bwd_q_simple<T><<<gq, 128, 0, s>>>(p, a);
-    ragged_status st = cuda_check(cudaGetLastError(), "query gradient launch");
+ragged_status launch_bias_bwd(const ragged::bias::Problem& p, ragged::bias::BwdArgs a, cudaStream_t s) {
+    using namespace ragged::bias;
+    ragged_status st = ensure_smem(bias_bwd_q_kernel<T>, kBwdQSmemMax, g_bias_bwd_q_smem[kTypeSlot<T>]);
+    if (st == RAGGED_OK) st = ensure_smem(bias_bwd_kv_kernel<T>, bwd_kv_smem_bytes(kMaxDistance), g_bias_bwd_kv_smem[kTypeSlot<T>]);
     if (st != RAGGED_OK) return st;
-    const dim3 gk(static_cast<unsigned>(tiles128(p.max_k)), static_cast<unsigned>(p.Hkv), static_cast<unsigned>(p.B));
-    ragged::bias::bias_bwd_kv_simple<T><<<gk, 128, 0, s>>>(p, a);
+    a.span = bwd_q_span(p.D, p.num_buckets);
+    bias_bwd_q_kernel<T><<<bias_grid(a.q_tiles, p.H, p.B), kThreads, bwd_q_smem_bytes(p.D, p.num_buckets, a.span), s>>>(p, a);
+    st = cuda_check(cudaGetLastError(), "query gradient launch");
+    if (st != RAGGED_OK) return st;
+    bias_bwd_kv_kernel<T><<<bias_grid(tiles128(p.max_k), p.Hkv, p.B), kThreads, bwd_kv_smem_bytes(p.D), s>>>(p, a);
     st = cuda_check(cudaGetLastError(), "key and value gradient launch");
     if (st != RAGGED_OK) return st;
-    const dim3 gt(static_cast<unsigned>(p.num_buckets), static_cast<unsigned>(p.H));
-    ragged::bias::bias_bwd_table<T><<<gt, 256, 0, s>>>(p, a);
+    bias_bwd_table_kernel<T><<<bias_grid(p.num_buckets, p.H, 1), 256, 0, s>>>(p, a);
     return cuda_check(cudaGetLastError(), "table gradient launch");
 }
 
 template <typename T>
 ragged_status launch_bias_weight(const ragged::bias::Problem& p, const float* prev, float* weight, int64_t stride,
                                  cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(tiles128(p.max_k)), static_cast<unsigned>(p.H), static_cast<unsigned>(p.B));
-    ragged::bias::bias_weight_simple<T><<<grid, 128, 0, s>>>(p, prev, weight, stride);
+    using namespace ragged::bias;
+    ragged_status st = ensure_smem(bias_weight_kernel<T>, weight_smem_bytes(kMaxDistance), g_bias_weight_smem[kTypeSlot<T>]);
+    if (st != RAGGED_OK) return st;
+    bias_weight_kernel<T><<<bias_grid(tiles128(p.max_k), p.H, p.B), kThreads, weight_smem_bytes(p.D), s>>>(p, prev, weight, stride);
     return cuda_check(cudaGetLastError(), "attention weight launch");
 }
 
@@ -245,8 +272,10 @@ ragged_status ragged_attn_bias_bwd(const ragged_bias_attn* a, const void* out, i
     ragged::bias::BwdArgs g{static_cast<const uint16_t*>(out), static_cast<const uint16_t*>(dout), out_tok_stride,
                             dout_tok_stride, static_cast<uint16_t*>(dq), static_cast<uint16_t*>(dk),
                             static_cast<uint16_t*>(dv), dq_tok_stride, a->H > 1 ? dq_head_stride : 0, dkv_tok_stride,
-                            a->Hkv > 1 ? dkv_head_stride : 0, ws, ws + bwd_delta_floats(a),
-                            static_cast<uint16_t*>(dtable), static_cast<int>(tiles128(a->max_seqlen_q))};
+                            a->Hkv > 1 ? dkv_head_stride : 0, ws,
+                            reinterpret_cast<int*>(ws + bwd_delta_floats(a)),
+                            ws + bwd_delta_floats(a) + bwd_items(a), static_cast<uint16_t*>(dtable),
+                            static_cast<int>(tiles128(a->max_seqlen_q)), 0};
     return a->dtype == RAGGED_F16 ? launch_bias_bwd<__half>(p, g, s) : launch_bias_bwd<__nv_bfloat16>(p, g, s);
 }
 
