@@ -366,52 +366,65 @@ def _same_device(*tensors) -> None:
             raise ValueError(f"a tensor is on {t.device}, not on the current CUDA device {index}")
 
 
-def _int32(t: Optional[torch.Tensor], n: Optional[int], what: str) -> None:
-    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or
-                          (n is not None and t.shape[0] != n)):
-        raise ValueError(f"{what} must be contiguous int32" + ("" if n is None else f" [{n}]"))
+_i32 = torch.int32
+
+
+def _int32(t: torch.Tensor, n: int, what: str) -> None:
+    if t.dtype is not _i32 or t.dim() != 1 or not t.is_contiguous() or (n >= 0 and t.shape[0] != n):
+        raise ValueError(f"{what} must be contiguous int32" + (f" [{n}]" if n >= 0 else ""))
 
 
 def _bias_problem(q, k, v, cu_q, cu_k, max_q, max_k, table, buckets, pos_q, pos_k, scale, lse) -> BiasAttn:
     """The checked problem of the three attention operators with a position bias (v: k where it is not read)."""
-    (Tq, H, d), (Tk, Hkv, dk) = q.shape, k.shape
+    Tq, H, d = q.shape
+    shape = k.shape
     dt = q.dtype
-    qs, ks = q.stride(), k.stride()
-    if v.shape != k.shape or dk != d or k.dtype != dt or v.dtype != dt or table.dtype != dt:
+    q_tok, q_head, q_one = q.stride()
+    ks = k.stride()
+    if v.shape != shape or shape[2] != d or k.dtype is not dt or v.dtype is not dt or table.dtype is not dt:
         raise ValueError("q [Tq, H, d], k and v [Tk, Hkv, d] and table must have one dtype and head_dim")
-    if qs[2] != 1 or ks[2] != 1 or v.stride() != ks:
+    if q_one != 1 or ks[2] != 1 or v.stride() != ks:
         raise ValueError("q, k and v need a unit innermost stride, and k and v the same strides")
-    if table.dim() != 2 or table.shape[1] != H or not table.is_contiguous():
+    nb, heads = table.shape
+    if heads != H or not table.is_contiguous():
         raise ValueError("table must be contiguous [num_buckets, H]")
-    if cu_q.shape != cu_k.shape:
-        raise ValueError("cu_seqlens_q and cu_seqlens_k must have the same length")
-    _int32(cu_q, None, "cu_seqlens_q")
-    _int32(cu_k, None, "cu_seqlens_k")
-    _int32(buckets, None, "buckets")
-    if buckets.shape[0] % 2 == 0:
+    _int32(cu_q, -1, "cu_seqlens_q")
+    B = cu_q.shape[0] - 1
+    if cu_k is not cu_q:
+        _int32(cu_k, B + 1, "cu_seqlens_k")
+    _int32(buckets, -1, "buckets")
+    entries = buckets.shape[0]
+    if entries % 2 == 0:
         raise ValueError("buckets must have an odd length, 2 * max_distance + 1")
     if pos_q is not None:
         _int32(pos_q, Tq, "pos_q")
     if pos_k is not None:
-        _int32(pos_k, Tk, "pos_k")
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (H, Tq) or (Tq > 1 and lse.stride(1) != 1):
+        _int32(pos_k, shape[0], "pos_k")
+    if lse.dtype is not torch.float32 or lse.shape != (H, Tq) or (Tq > 1 and lse.stride(1) != 1):
         raise ValueError("lse must be float32 [H, Tq] with unit innermost stride")
     _same_device(q, k, v, cu_q, cu_k, table, buckets, pos_q, pos_k, lse)
     some = cu_q.data_ptr()   # stands for the address of a tensor without elements, which is never read
-    return BiasAttn(q.data_ptr() or some, k.data_ptr() or some, v.data_ptr() or some, qs[0], qs[1], ks[0], ks[1],
-                    some, cu_k.data_ptr(), cu_q.shape[0] - 1, max_q, max_k, H, Hkv, d, table.data_ptr(),
-                    buckets.data_ptr(), table.shape[0], buckets.shape[0] // 2, _ptr(pos_q), _ptr(pos_k),
-                    lse.data_ptr() or some, lse.stride(0) if Tq else 0, d ** -0.5 if scale is None else scale,
-                    _dtype_code(q))
+    return BiasAttn(q.data_ptr() or some, k.data_ptr() or some, v.data_ptr() or some, q_tok, q_head, ks[0], ks[1],
+                    some, cu_k.data_ptr(), B, max_q, max_k, H, shape[1], d, table.data_ptr(), buckets.data_ptr(), nb,
+                    entries // 2, None if pos_q is None else pos_q.data_ptr(),
+                    None if pos_k is None else pos_k.data_ptr(), lse.data_ptr() or some,
+                    lse.stride(0) if Tq else 0, d ** -0.5 if scale is None else scale, _dtype_code(q))
+
+
+def _current_stream() -> int:
+    """Handle of torch's current stream (without the Stream object around it)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _workspace(sizer, problem, like: torch.Tensor):
     """Scratch of one call from torch's allocator: (tensor or None, address, bytes)."""
     n = ctypes.c_int64(0)
-    _check(sizer(problem, n))
+    status = sizer(problem, n)
+    if status:
+        _check(status)
     if n.value == 0:
         return None, None, 0
-    t = torch.empty(n.value, dtype=torch.uint8, device=like.device)
+    t = like.new_empty(n.value, dtype=torch.uint8)
     return t, t.data_ptr(), n.value
 
 
@@ -441,18 +454,20 @@ def ragged_attn_bias_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_s
                                         buckets, pos_q, pos_k, scale, out, lse)
     Tq, H, d = q.shape
     if out is None:
-        out = torch.empty((Tq, H, d), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _rows_of_heads(out, q, "out")
         _same_device(out)
     if lse is None:
-        lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((H, Tq), dtype=torch.float32)
     p = _bias_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table, buckets, pos_q, pos_k,
                       scale, lse)
     lib = load()
     ws, addr, size = _workspace(lib.ragged_attn_bias_fwd_workspace, p, q)
-    _check(lib.ragged_attn_bias_fwd(p, out.data_ptr() or p.cu_seqlens_q, out.stride(0) if Tq else H * d, addr, size,
-                                    _stream(None)))
+    status = lib.ragged_attn_bias_fwd(p, out.data_ptr() or p.cu_seqlens_q, out.stride(0) if Tq > 1 else H * d, addr, size,
+                                      _current_stream())
+    if status:
+        _check(status)
     return out, lse
 
 
@@ -476,16 +491,24 @@ def ragged_attn_bias_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v
         raise ValueError("dout must have the shape and dtype of out")
     if dout.stride(2) != 1 or (H > 1 and dout.stride(1) != d) or (Tq > 1 and dout.stride(0) < H * d):
         dout = dout.contiguous()   # a broadcast or transposed gradient
-    dq = torch.empty((Tq, H, d), dtype=q.dtype, device=q.device) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
-    dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
-    dtable = torch.empty(table.shape, dtype=table.dtype, device=table.device) if dtable is None else dtable
-    _heads(dq, q, "dq")
-    _heads(dk, k, "dk")
-    _heads(dv, v, "dv")
+    plain = torch.contiguous_format
+    if dq is None:
+        dq = torch.empty_like(q, memory_format=plain)
+    else:
+        _heads(dq, q, "dq")
+    if dk is None:
+        dk = torch.empty_like(k, memory_format=plain)
+    else:
+        _heads(dk, k, "dk")
+    if dv is None:
+        dv = torch.empty_like(v, memory_format=plain)
+    else:
+        _heads(dv, v, "dv")
     if dk.shape[0] and dk.stride() != dv.stride():
         raise ValueError("dk and dv must have the same strides")
-    if dtable.shape != table.shape or dtable.dtype != table.dtype or not dtable.is_contiguous():
+    if dtable is None:
+        dtable = torch.empty_like(table, memory_format=plain)
+    elif dtable.shape != table.shape or dtable.dtype is not table.dtype or not dtable.is_contiguous():
         raise ValueError("dtable must be contiguous with the shape and dtype of table")
     _same_device(dout, out, dq, dk, dv, dtable)
     p = _bias_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table, buckets, pos_q, pos_k,
@@ -493,11 +516,13 @@ def ragged_attn_bias_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v
     lib = load()
     ws, addr, size = _workspace(lib.ragged_attn_bias_bwd_workspace, p, q)
     some = p.cu_seqlens_q
-    _check(lib.ragged_attn_bias_bwd(p, out.data_ptr() or some, out.stride(0) if Tq > 1 else H * d,
-                                    dout.data_ptr() or some, dout.stride(0) if Tq > 1 else H * d,
-                                    dq.data_ptr() or some, dq.stride(0), dq.stride(1), dk.data_ptr() or some,
-                                    dv.data_ptr() or some, dk.stride(0), dk.stride(1), dtable.data_ptr(), addr, size,
-                                    _stream(None)))
+    status = lib.ragged_attn_bias_bwd(p, out.data_ptr() or some, out.stride(0) if Tq > 1 else H * d,
+                                      dout.data_ptr() or some, dout.stride(0) if Tq > 1 else H * d,
+                                      dq.data_ptr() or some, dq.stride(0), dq.stride(1), dk.data_ptr() or some,
+                                      dv.data_ptr() or some, dk.stride(0), dk.stride(1), dtable.data_ptr(), addr, size,
+                                      _current_stream())
+    if status:
+        _check(status)
     return dq, dk, dv, dtable
 
 
@@ -515,16 +540,19 @@ def ragged_attn_weight(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, cu_s
                                       buckets, pos_q, pos_k, scale, prev, weight)
     H, Tk = q.shape[1], k.shape[0]
     if weight is None:
-        weight = torch.empty((H, Tk), dtype=torch.float32, device=k.device)
+        weight = k.new_empty((H, Tk), dtype=torch.float32)
     ws = weight.stride(0) if H > 1 else Tk
     for t, what in ((weight, "weight"), (prev, "prev")):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (H, Tk) or (Tk > 1 and t.stride(1) != 1) or
+        if t is not None and (t.dtype is not torch.float32 or t.shape != (H, Tk) or (Tk > 1 and t.stride(1) != 1) or
                               (H > 1 and t.stride(0) != ws)):
             raise ValueError(f"{what} must be float32 [H, Tk] with unit innermost stride, prev as weight")
     _same_device(weight, prev)
     p = _bias_problem(q, k, k, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table, buckets, pos_q, pos_k,
                       scale, lse)
-    _check(load().ragged_attn_weight(p, _ptr(prev) or None, weight.data_ptr() or p.cu_seqlens_q, ws, _stream(None)))
+    status = load().ragged_attn_weight(p, None if prev is None else prev.data_ptr() or None,
+                                       weight.data_ptr() or p.cu_seqlens_q, ws, _current_stream())
+    if status:
+        _check(status)
     return weight
 
 
@@ -543,30 +571,31 @@ def ragged_evict(rows: Optional[torch.Tensor], weight: torch.Tensor, cu_seqlens:
             return ragged_evict(rows, weight, cu_seqlens, max_seqlen, budget, sinks, recents, pos, total)
     H, T = weight.shape
     B = cu_seqlens.shape[0] - 1
-    if weight.dtype != torch.float32 or (T > 1 and weight.stride(1) != 1):
+    if weight.dtype is not torch.float32 or (T > 1 and weight.stride(1) != 1):
         raise ValueError("weight must be float32 [H, T] with unit innermost stride")
     if rows is not None and (rows.shape[0] != T or not rows.is_contiguous()):
         raise ValueError("rows must be contiguous [T, ...]")
-    _int32(cu_seqlens, None, "cu_seqlens")
+    _int32(cu_seqlens, -1, "cu_seqlens")
     _int32(budget, B, "budget")
     if pos is not None:
         _int32(pos, T, "pos")
     _same_device(rows, weight, cu_seqlens, budget, pos)
     n = T if total is None else int(total)
-    dev = weight.device
-    rows_out = None if rows is None else torch.empty((n,) + tuple(rows.shape[1:]), dtype=rows.dtype, device=dev)
-    ints = torch.empty(2 * n + B + 1, dtype=torch.int32, device=dev)
-    cu_out, src_idx, pos_out = ints[:B + 1], ints[B + 1:B + 1 + n], ints[B + 1 + n:]
-    weight_out = torch.empty((H, n), dtype=torch.float32, device=dev)
+    rows_out = None if rows is None else rows.new_empty((n,) + rows.shape[1:])
+    cu_out, src_idx, pos_out = cu_seqlens.new_empty(2 * n + B + 1).split_with_sizes((B + 1, n, n))
+    weight_out = weight.new_empty((H, n))
     copy = rows is not None and n > 0 and T > 0
     row_bytes = rows.stride(0) * rows.element_size() if copy else 0
     some = cu_seqlens.data_ptr()
-    _check(load().ragged_evict(rows.data_ptr() if copy else None, row_bytes, weight.data_ptr() or some,
-                               weight.stride(0) if H > 1 else 0, H, some, B, int(max_seqlen), budget.data_ptr() or some,
-                               int(sinks), int(recents), _ptr(pos) or None, n, rows_out.data_ptr() if copy else None,
-                               cu_out.data_ptr(), src_idx.data_ptr() if n else None,
-                               weight_out.data_ptr() if n else None, n, pos_out.data_ptr() if n else None,
-                               _stream(None)))
+    status = load().ragged_evict(rows.data_ptr() if copy else None, row_bytes, weight.data_ptr() or some,
+                                 weight.stride(0) if H > 1 else 0, H, some, B, int(max_seqlen),
+                                 budget.data_ptr() or some, int(sinks), int(recents),
+                                 None if pos is None else pos.data_ptr() or None, n,
+                                 rows_out.data_ptr() if copy else None, cu_out.data_ptr(),
+                                 src_idx.data_ptr() if n else None, weight_out.data_ptr() if n else None, n,
+                                 pos_out.data_ptr() if n else None, _current_stream())
+    if status:
+        _check(status)
     return rows_out, cu_out, src_idx, weight_out, pos_out
 
 

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "bias_bwd.cuh"
+#include "bias_few.cuh"
 #include "evict.cuh"
 
 namespace {
@@ -107,9 +108,58 @@ dim3 bias_grid(int64_t tiles, int heads, int B) {
     return dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(heads), static_cast<unsigned>(B));
 }
 
+// Few query rows per key / value head go to the kernels that share one 16- or
+// 32-row MMA tile among them: the 128-row tiles would be mostly empty, and
+// read the keys once per query head.
+bool few_rows(const ragged::bias::Problem& p) {
+    return static_cast<int64_t>(p.group) * p.max_q <= ragged::bias::kFewMaxRows;
+}
+// CTAs per (sequence, key / value head): enough to fill the GPU a few times,
+// each with at least one block of keys per warp.
+int few_splits(const ragged::bias::Problem& p, int limit) {
+    const int64_t base = static_cast<int64_t>(p.B) * p.Hkv, want = (3LL * sm_count() + base - 1) / base;
+    const int64_t most = (p.max_k + ragged::bias::kFewKeys * ragged::bias::kFewWarps - 1) / (ragged::bias::kFewKeys * ragged::bias::kFewWarps);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, most), limit)));
+}
+DeviceFlags g_few_smem[2][2], g_few_weight_smem[2][2];
+
+template <typename T, int MT>
+ragged_status launch_few(const ragged::bias::Problem& p, uint16_t* out, int64_t out_tok, cudaStream_t s) {
+    using namespace ragged::bias;
+    auto kernel = bias_few_kernel<T, MT>;
+    ragged_status st = ensure_smem(kernel, few_smem_bytes<false>(MT, kMaxDistance, kMaxBuckets), g_few_smem[kTypeSlot<T>][MT - 1]);
+    if (st != RAGGED_OK) return st;
+    int splits = few_splits(p, kFewMaxSplits);
+    while (splits & (splits - 1)) splits &= splits - 1;   // cluster sizes are powers of two
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = bias_grid(splits, p.Hkv, p.B);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = few_smem_bytes<false>(MT, p.D, p.num_buckets);
+    cfg.stream = s;
+    cudaLaunchAttribute cluster{};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = static_cast<unsigned>(splits);
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = splits > 1 ? 1 : 0;
+    return cuda_check(cudaLaunchKernelEx(&cfg, kernel, p, out, out_tok), "attention (few rows) launch");
+}
+
+template <typename T, int MT>
+ragged_status launch_few_weight(const ragged::bias::Problem& p, const float* prev, float* weight, int64_t stride, cudaStream_t s) {
+    using namespace ragged::bias;
+    auto kernel = bias_few_weight_kernel<T, MT>;
+    ragged_status st = ensure_smem(kernel, few_smem_bytes<true>(MT, kMaxDistance, kMaxBuckets), g_few_weight_smem[kTypeSlot<T>][MT - 1]);
+    if (st != RAGGED_OK) return st;
+    kernel<<<bias_grid(few_splits(p, 1 << 16), p.Hkv, p.B), kFewThreads, few_smem_bytes<true>(MT, p.D, p.num_buckets), s>>>(p, prev, weight, stride);
+    return cuda_check(cudaGetLastError(), "attention weight (few rows) launch");
+}
+
 template <typename T>
 ragged_status launch_bias_fwd(const ragged::bias::Problem& p, uint16_t* out, int64_t out_tok, cudaStream_t s) {
     using namespace ragged::bias;
+    if (few_rows(p))
+        return p.group * p.max_q <= 16 ? launch_few<T, 1>(p, out, out_tok, s) : launch_few<T, 2>(p, out, out_tok, s);
     ragged_status st = ensure_smem(bias_fwd_kernel<T>, fwd_smem_bytes(kMaxDistance), g_bias_fwd_smem[kTypeSlot<T>]);
     if (st != RAGGED_OK) return st;
     bias_fwd_kernel<T><<<bias_grid(tiles128(p.max_q), p.H, p.B), kThreads, fwd_smem_bytes(p.D), s>>>(p, out, out_tok);
@@ -137,6 +187,9 @@ template <typename T>
 ragged_status launch_bias_weight(const ragged::bias::Problem& p, const float* prev, float* weight, int64_t stride,
                                  cudaStream_t s) {
     using namespace ragged::bias;
+    if (few_rows(p))
+        return p.group * p.max_q <= 16 ? launch_few_weight<T, 1>(p, prev, weight, stride, s)
+                                       : launch_few_weight<T, 2>(p, prev, weight, stride, s);
     ragged_status st = ensure_smem(bias_weight_kernel<T>, weight_smem_bytes(kMaxDistance), g_bias_weight_smem[kTypeSlot<T>]);
     if (st != RAGGED_OK) return st;
     bias_weight_kernel<T><<<bias_grid(tiles128(p.max_k), p.H, p.B), kThreads, weight_smem_bytes(p.D), s>>>(p, prev, weight, stride);

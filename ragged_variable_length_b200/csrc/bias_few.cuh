@@ -1,0 +1,466 @@
+// Attention with a learned relative position bias for few query rows per key /
+// value head (one new token, or a few, against a cache; very short
+// sequences), and the weights that the keys collect from them.
+//
+// The group * q_len rows that share a key / value head make one MMA tile of
+// 16 rows (or two), so every key and value is read once for all of them: the
+// kernels are bound by those reads.  Each warp streams blocks of 16 keys
+// through a ring of its own (cp.async, no barrier across warps) and keeps its
+// own softmax state; mma.sync is enough, because a block of 4 KB costs a warp
+// 8 to 24 MMAs.  The keys of a sequence are split over the warps of a CTA and
+// over the CTAs of a cluster, whose states are joined through (distributed)
+// shared memory: one launch, no workspace, a fixed order.
+//
+// P is split into two 16-bit parts (value and residual) for P V, which costs
+// nothing next to the loads and leaves the result with its own rounding only.
+#pragma once
+
+#include <limits.h>
+
+#include "bias_common.cuh"
+
+namespace ragged {
+namespace bias {
+
+constexpr int kFewWarps = 4;
+constexpr int kFewThreads = 32 * kFewWarps;
+constexpr int kFewKeys = 16;          // keys per block
+constexpr int kFewStages = 6;         // blocks in flight per warp
+constexpr int kFewMaxRows = 32;
+constexpr int kFewMaxSplits = 8;      // CTAs of a cluster
+
+// Shared memory: the warps' rings (K, V and positions of a block), the query
+// rows, the bucket map as bytes, the rows' table entries.
+template <bool WEIGHT>
+__host__ __device__ constexpr int few_stage_bytes() {
+    return kFewKeys * 128 * (WEIGHT ? 1 : 2) + kFewKeys * 4;
+}
+template <bool WEIGHT>
+__host__ __device__ constexpr int few_smem_bytes(int MT, int D, int num_buckets) {
+    return kFewWarps * kFewStages * few_stage_bytes<WEIGHT>() + MT * 16 * 128 + ((2 * D + 1 + 15) & ~15) +
+           4 * num_buckets * MT * 16;
+}
+
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, int src_bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float cluster_read(const float* p, uint32_t rank) {
+    uint32_t a = smem_addr(p);
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %0, %2;\n\tld.shared::cluster.f32 %1, [%0];" : "+r"(a), "=f"(v) : "r"(rank) : "memory");
+    return v;
+}
+
+// The residual of a pair's rounding, rounded again.
+template <typename T>
+__device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t rounded) {
+    return mma_attn::Mma<T>::pack(lo - to_float<T>(static_cast<uint16_t>(rounded)),
+                                  hi - to_float<T>(static_cast<uint16_t>(rounded >> 16)));
+}
+
+// What both kernels set up: the sequence, this warp's key blocks, the query
+// fragments, the rows' positions and the bias in shared memory.
+template <typename T, int MT, bool WEIGHT>
+struct Few {
+    Seq s;
+    int z, rows, warp, lane, g, c2;   // g: row in a tile, c2: first of this lane's two columns
+    int pq[MT][2];                    // positions of this lane's rows
+    int q_min, q_max;
+    float left[MT][2], right[MT][2];  // bias past either end of the map
+    uint32_t qf[MT][4][4];
+    uint32_t ring;
+    const uint8_t* map;
+    const float* tab;                 // [num_buckets][MT * 16]
+    const uint16_t *kb, *vb;
+
+    __device__ __forceinline__ int head_of(const Problem& p, int row) const { return z * p.group + row / s.q_len; }
+    __device__ __forceinline__ int query_of(int row) const { return row % s.q_len; }
+
+    __device__ __forceinline__ void setup(const Problem& p, uint8_t* smem) {
+        const int tid = threadIdx.x;
+        warp = tid >> 5;
+        lane = tid & 31;
+        g = lane >> 2;
+        c2 = (lane & 3) * 2;
+        rows = p.group * s.q_len;
+        ring = smem_addr(smem) + warp * kFewStages * few_stage_bytes<WEIGHT>();
+        uint8_t* at = smem + kFewWarps * kFewStages * few_stage_bytes<WEIGHT>();
+        const uint32_t sQ = smem_addr(at);
+        uint8_t* m = at + MT * 16 * 128;
+        float* t = reinterpret_cast<float*>(m + ((2 * p.D + 1 + 15) & ~15));
+        map = m;
+        tab = t;
+        const int64_t head = z * p.kv_head;
+        kb = p.k + s.k_start * p.kv_tok + head;
+        vb = p.v + s.k_start * p.kv_tok + head;
+        for (int i = tid; i < MT * 16 * 8; i += kFewThreads) {
+            const int r = i >> 3, c = i & 7;
+            const bool in = r < rows;
+            const uint16_t* src = in ? p.q + static_cast<int64_t>(s.q_start + query_of(r)) * p.q_tok + head_of(p, r) * p.q_head + c * 8 : p.q;
+            cp_async_16(sQ + mma_attn::swz(r, c), src, in ? 16 : 0);
+        }
+        cp_async_commit();
+        for (int i = tid; i < p.num_buckets * MT * 16; i += kFewThreads) {
+            const int b = i / (MT * 16), r = i - b * (MT * 16);
+            t[i] = r < rows ? bias_log2<T>(__ldg(p.table + static_cast<int64_t>(b) * p.H + head_of(p, r))) : 0.f;
+        }
+        for (int i = tid; i <= 2 * p.D; i += kFewThreads) m[i] = static_cast<uint8_t>(bucket_of(p, i - p.D));   // -1: 255
+        q_min = INT_MAX;
+        q_max = INT_MIN;
+        for (int i = 0; i < s.q_len; ++i) {
+            const int x = query_pos(p, s, i);
+            q_min = min(q_min, x);
+            q_max = max(q_max, x);
+        }
+#pragma unroll
+        for (int t2 = 0; t2 < MT; ++t2)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int r = t2 * 16 + g + 8 * k;
+                pq[t2][k] = r < rows ? query_pos(p, s, query_of(r)) : q_min;
+            }
+        cp_async_wait<0>();
+        __syncthreads();
+#pragma unroll
+        for (int t2 = 0; t2 < MT; ++t2) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)   // rows 0-7 / 8-15 of the first, then of the second eight columns
+                mma_attn::ldmatrix_x4(qf[t2][ks], sQ + mma_attn::swz(t2 * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), 2 * ks + (lane >> 4)));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                left[t2][k] = entry(t2 * 16 + g + 8 * k, 0);
+                right[t2][k] = entry(t2 * 16 + g + 8 * k, 2 * p.D);
+            }
+        }
+    }
+    __device__ __forceinline__ float entry(int row, int index) const {
+        const int b = map[index];
+        return b == 255 ? 0.f : tab[b * (MT * 16) + row];
+    }
+    __device__ __forceinline__ uint32_t stage(int n) const { return ring + (n % kFewStages) * few_stage_bytes<WEIGHT>(); }
+    // One block of keys (and values, positions) into stage n of this warp's ring.
+    __device__ __forceinline__ void load(const Problem& p, int n, int key0) const {
+        const uint32_t st = stage(n);
+        const int r = lane >> 3, c = lane & 7;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = key0 + r + 4 * i;
+            const bool in = row < s.k_len;
+            const int64_t off = static_cast<int64_t>(in ? row : 0) * p.kv_tok + c * 8;
+            cp_async_16(st + mma_attn::swz(r + 4 * i, c), kb + off, in ? 16 : 0);
+            if constexpr (!WEIGHT) cp_async_16(st + kFewKeys * 128 + mma_attn::swz(r + 4 * i, c), vb + off, in ? 16 : 0);
+        }
+        if (p.pos_k != nullptr && lane < kFewKeys) {
+            const int row = min(key0 + lane, s.k_len - 1);   // past the end: a position of the block
+            cp_async_4(st + few_stage_bytes<WEIGHT>() - kFewKeys * 4 + 4 * lane, p.pos_k + s.k_start + row, 4);
+        }
+    }
+    // Scores in base 2 of block n (keys from key0): x[tile][8 keys][row g: 2 columns, row g + 8: 2 columns].
+    __device__ __forceinline__ void scores(const Problem& p, int n, int key0, float (&x)[MT][2][4]) const {
+        const uint32_t st = stage(n);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[t][i][j] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            uint32_t b[4];
+            mma_attn::ldmatrix_x4(b, st + mma_attn::swz((lane >> 4) * 8 + (lane & 7), 2 * ks + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                mma_attn::Mma<T>::run(x[t][0], qf[t][ks], b[0], b[1]);
+                mma_attn::Mma<T>::run(x[t][1], qf[t][ks], b[2], b[3]);
+            }
+        }
+        // Positions of the block's keys, lane by lane; a block past either end of the map has one bias per row.
+        const uint32_t pos = st + few_stage_bytes<WEIGHT>() - kFewKeys * 4;
+        int mine = min(key0 + (lane & 15), s.k_len - 1);
+        if (p.pos_k != nullptr) asm volatile("ld.shared.s32 %0, [%1];" : "=r"(mine) : "r"(pos + 4 * (lane & 15)) : "memory");
+        const int64_t lo = __reduce_min_sync(0xffffffffu, mine), hi = __reduce_max_sync(0xffffffffu, mine);
+        const bool all_left = hi - q_min <= -p.D, all_right = lo - q_max >= p.D;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int col = i * 8 + c2 + j;
+                const int pk = __shfl_sync(0xffffffffu, mine, col);
+                const bool in = key0 + col < s.k_len;
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float e;
+                        if (all_left) e = left[t][k];
+                        else if (all_right) e = right[t][k];
+                        else e = entry(t * 16 + g + 8 * k, max(-p.D, min(p.D, pos_diff(pk, pq[t][k]))) + p.D);
+                        float& v = x[t][i][2 * k + j];
+                        v = in ? fmaf(v, p.scale_log2, e) : -INFINITY;
+                    }
+            }
+    }
+};
+
+// grid (splits, Hkv, B), cluster (splits, 1, 1)
+template <typename T, int MT>
+__global__ void __launch_bounds__(kFewThreads) bias_few_kernel(const Problem p, uint16_t* __restrict__ out, int64_t out_tok) {
+    extern __shared__ __align__(128) uint8_t few_smem[];
+    __shared__ float s_m[kFewWarps][MT * 16], s_l[kFewWarps][MT * 16];
+    __shared__ float s_mc[MT * 16], s_lc[MT * 16];
+    const int splits = gridDim.x, rank = blockIdx.x;
+    Few<T, MT, false> f;
+    f.z = blockIdx.y;
+    if (!read_pair(p, blockIdx.z, f.s) || f.s.q_len == 0) return;   // the same for the whole cluster
+    f.setup(p, few_smem);
+    const int blocks = (f.s.k_len + kFewKeys - 1) / kFewKeys;
+    const int per = (blocks + splits * kFewWarps - 1) / (splits * kFewWarps);   // of one warp
+    // A CTA's blocks are one run of keys; its warps take them in turn.
+    const int first = min(blocks, rank * per * kFewWarps) + f.warp, end = min(blocks, (rank + 1) * per * kFewWarps);
+    float m[MT][2], l[MT][2], o[MT][8][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        m[t][0] = m[t][1] = -INFINITY;
+        l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[t][i][j] = 0.f;
+    }
+#pragma unroll
+    for (int n = 0; n < kFewStages - 1; ++n) {
+        if (first + n * kFewWarps < end) f.load(p, n, (first + n * kFewWarps) * kFewKeys);
+        cp_async_commit();
+    }
+    int n = 0;
+    for (int blk = first; blk < end; blk += kFewWarps, ++n) {
+        cp_async_wait<kFewStages - 2>();
+        __syncwarp();
+        const int ahead = blk + (kFewStages - 1) * kFewWarps;
+        if (ahead < end) f.load(p, n + kFewStages - 1, ahead * kFewKeys);
+        cp_async_commit();
+        float x[MT][2][4];
+        f.scores(p, n, blk * kFewKeys, x);
+        uint32_t hi[MT][4], lo[MT][4];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            float alpha[2], ref[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float v = fmaxf(fmaxf(x[t][0][2 * k], x[t][0][2 * k + 1]), fmaxf(x[t][1][2 * k], x[t][1][2 * k + 1]));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                const float next = fmaxf(m[t][k], v);
+                ref[k] = next == -INFINITY ? 0.f : next;
+                alpha[k] = mma_attn::fast_exp2(m[t][k] - ref[k]);
+                m[t][k] = next;
+            }
+            if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    o[t][i][0] *= alpha[0];
+                    o[t][i][1] *= alpha[0];
+                    o[t][i][2] *= alpha[1];
+                    o[t][i][3] *= alpha[1];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float a = mma_attn::fast_exp2(x[t][i][2 * k] - ref[k]), b = mma_attn::fast_exp2(x[t][i][2 * k + 1] - ref[k]);
+                    sum += a + b;
+                    const uint32_t w = mma_attn::Mma<T>::pack(a, b);
+                    hi[t][2 * i + k] = w;
+                    lo[t][2 * i + k] = pack_rest<T>(a, b, w);
+                }
+                l[t][k] = l[t][k] * alpha[k] + sum;
+            }
+        }
+        const uint32_t sv = f.stage(n) + kFewKeys * 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {   // 16 value columns
+            uint32_t b[4];
+            mma_attn::ldmatrix_x4_trans(b, sv + mma_attn::swz(((f.lane >> 3) & 1) * 8 + (f.lane & 7), 2 * c + (f.lane >> 4)));
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                mma_attn::Mma<T>::run(o[t][2 * c], hi[t], b[0], b[1]);
+                mma_attn::Mma<T>::run(o[t][2 * c], lo[t], b[0], b[1]);
+                mma_attn::Mma<T>::run(o[t][2 * c + 1], hi[t], b[2], b[3]);
+                mma_attn::Mma<T>::run(o[t][2 * c + 1], lo[t], b[2], b[3]);
+            }
+        }
+        __syncwarp();   // the stage may be overwritten
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    // The warps' states, then the CTA's, then the cluster's: out = sum 2^(m - M) o / sum 2^(m - M) l.
+    float* so = reinterpret_cast<float*>(few_smem);   // [warp][row][64], over the rings
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = t * 16 + f.g + 8 * k;
+            float v = l[t][k];
+            v += __shfl_xor_sync(0xffffffffu, v, 1);
+            v += __shfl_xor_sync(0xffffffffu, v, 2);
+            if (f.c2 == 0) {
+                s_m[f.warp][r] = m[t][k];
+                s_l[f.warp][r] = v;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float2*>(so + (f.warp * MT * 16 + r) * 64 + i * 8 + f.c2) = make_float2(o[t][i][2 * k], o[t][i][2 * k + 1]);
+        }
+    __syncthreads();
+    const int rows = f.rows;
+    for (int i = threadIdx.x; i < rows * 64; i += kFewThreads) {
+        const int r = i >> 6, d = i & 63;
+        float top = s_m[0][r];
+#pragma unroll
+        for (int w = 1; w < kFewWarps; ++w) top = fmaxf(top, s_m[w][r]);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float acc = 0.f, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) {
+            const float a = mma_attn::fast_exp2(s_m[w][r] - ref);
+            acc = fmaf(a, so[(w * MT * 16 + r) * 64 + d], acc);
+            sum = fmaf(a, s_l[w][r], sum);
+        }
+        so[r * 64 + d] = acc;   // of warp 0's part, which only this thread reads
+        if (d == 0) {
+            s_mc[r] = top;
+            s_lc[r] = sum;
+        }
+    }
+    if (splits > 1) cluster_sync();
+    else __syncthreads();
+    for (int i = rank * kFewThreads + threadIdx.x; i < rows * 32; i += splits * kFewThreads) {
+        const int r = i >> 5, d = (i & 31) * 2;
+        float a0, a1, sum, top;
+        if (splits == 1) {
+            top = s_mc[r];
+            sum = s_lc[r];
+            a0 = so[r * 64 + d];
+            a1 = so[r * 64 + d + 1];
+        } else {
+            float mc[kFewMaxSplits];
+            top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < kFewMaxSplits; ++c) {
+                mc[c] = c < splits ? cluster_read(&s_mc[r], c) : -INFINITY;
+                top = fmaxf(top, mc[c]);
+            }
+            const float ref = top == -INFINITY ? 0.f : top;
+            a0 = a1 = sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < kFewMaxSplits; ++c)
+                if (c < splits) {
+                    const float w = mma_attn::fast_exp2(mc[c] - ref);
+                    sum = fmaf(w, cluster_read(&s_lc[r], c), sum);
+                    a0 = fmaf(w, cluster_read(so + r * 64 + d, c), a0);
+                    a1 = fmaf(w, cluster_read(so + r * 64 + d + 1, c), a1);
+                }
+        }
+        const bool empty = sum == 0.f;
+        const float inv = 1.f / sum;
+        const int h = f.head_of(p, r);
+        const int64_t t = f.s.q_start + f.query_of(r);
+        *reinterpret_cast<uint32_t*>(out + t * out_tok + h * 64 + d) = empty ? 0u : mma_attn::Mma<T>::pack(a0 * inv, a1 * inv);
+        if (d == 0) p.lse[h * p.lse_stride + t] = empty ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+    if (splits > 1) cluster_sync();   // this CTA's shared memory has been read
+}
+
+// weight[h, j] = prev[h, j] + sum_i exp(s[i, j] - lse_i).  grid (splits, Hkv, B)
+template <typename T, int MT>
+__global__ void __launch_bounds__(kFewThreads)
+    bias_few_weight_kernel(const Problem p, const float* prev, float* weight, int64_t weight_stride) {
+    extern __shared__ __align__(128) uint8_t few_smem[];
+    __shared__ float s_p[kFewWarps][MT * 16][kFewKeys + 1];
+    const int splits = gridDim.x, rank = blockIdx.x;
+    Few<T, MT, true> f;
+    f.z = blockIdx.y;
+    if (!read_pair(p, blockIdx.z, f.s) || f.s.k_len == 0) return;
+    const int blocks = (f.s.k_len + kFewKeys - 1) / kFewKeys;
+    const int per = (blocks + splits * kFewWarps - 1) / (splits * kFewWarps);
+    const int begin = min(blocks, rank * per * kFewWarps), end = min(blocks, (rank + 1) * per * kFewWarps);
+    if (begin >= end) return;
+    const int64_t at = f.z * p.group * weight_stride + f.s.k_start;
+    if (f.s.q_len == 0) {   // nothing to add
+        for (int h = 0; h < p.group; ++h)
+            for (int j = begin * kFewKeys + threadIdx.x; j < min(end * kFewKeys, f.s.k_len); j += kFewThreads)
+                weight[at + h * weight_stride + j] = prev != nullptr ? prev[at + h * weight_stride + j] : 0.f;
+        return;
+    }
+    f.setup(p, few_smem);
+    const int first = begin + f.warp;
+    float lse[MT][2];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = t * 16 + f.g + 8 * k;
+            lse[t][k] = r < f.rows ? lse_log2(__ldg(p.lse + f.head_of(p, r) * p.lse_stride + f.s.q_start + f.query_of(r))) : INFINITY;
+        }
+    // A lane's share of the results: key lane % 16 of heads lane / 16, + 2, ...; what they held
+    // before is loaded one block ahead.
+    const int key = f.lane & 15, h0 = f.lane >> 4;
+    float old[MT * 8];
+    auto load_old = [&](int blk) {
+#pragma unroll
+        for (int i = 0; i < MT * 8; ++i) {
+            const int h = h0 + 2 * i, j = blk * kFewKeys + key;
+            old[i] = prev != nullptr && h < p.group && blk < end && j < f.s.k_len ? prev[at + h * weight_stride + j] : 0.f;
+        }
+    };
+    load_old(first);
+#pragma unroll
+    for (int n = 0; n < kFewStages - 1; ++n) {
+        if (first + n * kFewWarps < end) f.load(p, n, (first + n * kFewWarps) * kFewKeys);
+        cp_async_commit();
+    }
+    int n = 0;
+    for (int blk = first; blk < end; blk += kFewWarps, ++n) {
+        cp_async_wait<kFewStages - 2>();
+        __syncwarp();
+        const int ahead = blk + (kFewStages - 1) * kFewWarps;
+        if (ahead < end) f.load(p, n + kFewStages - 1, ahead * kFewKeys);
+        cp_async_commit();
+        float x[MT][2][4];
+        f.scores(p, n, blk * kFewKeys, x);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s_p[f.warp][t * 16 + f.g + 8 * (j >> 1)][i * 8 + f.c2 + (j & 1)] = mma_attn::fast_exp2(x[t][i][j] - lse[t][j >> 1]);
+        __syncwarp();
+        const int j = blk * kFewKeys + key;
+#pragma unroll
+        for (int i = 0; i < MT * 8; ++i) {
+            const int h = h0 + 2 * i;
+            if (h < p.group && j < f.s.k_len) {
+                float sum = 0.f;
+                for (int q = 0; q < f.s.q_len; ++q) sum += s_p[f.warp][h * f.s.q_len + q][key];
+                weight[at + h * weight_stride + j] = old[i] + sum;
+            }
+        }
+        load_old(blk + kFewWarps);
+        __syncwarp();
+    }
+    cp_async_wait<0>();
+}
+
+}  // namespace bias
+}  // namespace ragged
