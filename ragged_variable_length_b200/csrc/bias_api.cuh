@@ -114,10 +114,10 @@ dim3 bias_grid(int64_t tiles, int heads, int B) {
 bool few_rows(const ragged::bias::Problem& p) {
     return static_cast<int64_t>(p.group) * p.max_q <= ragged::bias::kFewMaxRows;
 }
-// CTAs per (sequence, key / value head): enough to fill the GPU a few times,
+// CTAs per (sequence, key / value head): what one wave of two per SM holds,
 // each with at least one block of keys per warp.
 int few_splits(const ragged::bias::Problem& p, int limit) {
-    const int64_t base = static_cast<int64_t>(p.B) * p.Hkv, want = (3LL * sm_count() + base - 1) / base;
+    const int64_t base = static_cast<int64_t>(p.B) * p.Hkv, want = 2LL * sm_count() / base;
     const int64_t most = (p.max_k + ragged::bias::kFewKeys * ragged::bias::kFewWarps - 1) / (ragged::bias::kFewKeys * ragged::bias::kFewWarps);
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, most), limit)));
 }
@@ -127,14 +127,14 @@ template <typename T, int MT>
 ragged_status launch_few(const ragged::bias::Problem& p, uint16_t* out, int64_t out_tok, cudaStream_t s) {
     using namespace ragged::bias;
     auto kernel = bias_few_kernel<T, MT>;
-    ragged_status st = ensure_smem(kernel, few_smem_bytes<false>(MT, kMaxDistance, kMaxBuckets), g_few_smem[kTypeSlot<T>][MT - 1]);
+    ragged_status st = ensure_smem(kernel, few_smem_bytes<MT, false>(kMaxDistance, kMaxBuckets), g_few_smem[kTypeSlot<T>][MT - 1]);
     if (st != RAGGED_OK) return st;
     int splits = few_splits(p, kFewMaxSplits);
     while (splits & (splits - 1)) splits &= splits - 1;   // cluster sizes are powers of two
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = bias_grid(splits, p.Hkv, p.B);
     cfg.blockDim = dim3(kFewThreads);
-    cfg.dynamicSmemBytes = few_smem_bytes<false>(MT, p.D, p.num_buckets);
+    cfg.dynamicSmemBytes = few_smem_bytes<MT, false>(p.D, p.num_buckets);
     cfg.stream = s;
     cudaLaunchAttribute cluster{};
     cluster.id = cudaLaunchAttributeClusterDimension;
@@ -149,9 +149,9 @@ template <typename T, int MT>
 ragged_status launch_few_weight(const ragged::bias::Problem& p, const float* prev, float* weight, int64_t stride, cudaStream_t s) {
     using namespace ragged::bias;
     auto kernel = bias_few_weight_kernel<T, MT>;
-    ragged_status st = ensure_smem(kernel, few_smem_bytes<true>(MT, kMaxDistance, kMaxBuckets), g_few_weight_smem[kTypeSlot<T>][MT - 1]);
+    ragged_status st = ensure_smem(kernel, few_smem_bytes<MT, true>(kMaxDistance, kMaxBuckets), g_few_weight_smem[kTypeSlot<T>][MT - 1]);
     if (st != RAGGED_OK) return st;
-    kernel<<<bias_grid(few_splits(p, 1 << 16), p.Hkv, p.B), kFewThreads, few_smem_bytes<true>(MT, p.D, p.num_buckets), s>>>(p, prev, weight, stride);
+    kernel<<<bias_grid(few_splits(p, 1 << 16), p.Hkv, p.B), kFewThreads, few_smem_bytes<MT, true>(p.D, p.num_buckets), s>>>(p, prev, weight, stride);
     return cuda_check(cudaGetLastError(), "attention weight (few rows) launch");
 }
 

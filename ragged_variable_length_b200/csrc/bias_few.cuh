@@ -22,22 +22,22 @@
 namespace ragged {
 namespace bias {
 
-constexpr int kFewWarps = 4;
+constexpr int kFewWarps = 8;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kFewKeys = 16;          // keys per block
-constexpr int kFewStages = 6;         // blocks in flight per warp
+constexpr int kFewStages = 3;         // ring of a warp: two blocks in flight beside the current one
 constexpr int kFewMaxRows = 32;
 constexpr int kFewMaxSplits = 8;      // CTAs of a cluster
 
 // Shared memory: the warps' rings (K, V and positions of a block), the query
 // rows, the bucket map as bytes, the rows' table entries.
-template <bool WEIGHT>
-__host__ __device__ constexpr int few_stage_bytes() {
-    return kFewKeys * 128 * (WEIGHT ? 1 : 2) + kFewKeys * 4;
+template <int MT, bool WEIGHT>
+__host__ __device__ constexpr int few_stage_bytes() {   // keys, then values or the weights so far, then positions
+    return kFewKeys * 128 + (WEIGHT ? MT * 16 * kFewKeys * 4 : kFewKeys * 128) + kFewKeys * 4;
 }
-template <bool WEIGHT>
-__host__ __device__ constexpr int few_smem_bytes(int MT, int D, int num_buckets) {
-    return kFewWarps * kFewStages * few_stage_bytes<WEIGHT>() + MT * 16 * 128 + ((2 * D + 1 + 15) & ~15) +
+template <int MT, bool WEIGHT>
+__host__ __device__ constexpr int few_smem_bytes(int D, int num_buckets) {
+    return kFewWarps * kFewStages * few_stage_bytes<MT, WEIGHT>() + MT * 16 * 128 + ((2 * D + 1 + 15) & ~15) +
            4 * num_buckets * MT * 16;
 }
 
@@ -70,6 +70,7 @@ __device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t round
 // fragments, the rows' positions and the bias in shared memory.
 template <typename T, int MT, bool WEIGHT>
 struct Few {
+    static constexpr int kStage = few_stage_bytes<MT, WEIGHT>();
     Seq s;
     int z, rows, warp, lane, g, c2;   // g: row in a tile, c2: first of this lane's two columns
     int pq[MT][2];                    // positions of this lane's rows
@@ -84,30 +85,33 @@ struct Few {
     __device__ __forceinline__ int head_of(const Problem& p, int row) const { return z * p.group + row / s.q_len; }
     __device__ __forceinline__ int query_of(int row) const { return row % s.q_len; }
 
-    __device__ __forceinline__ void setup(const Problem& p, uint8_t* smem) {
-        const int tid = threadIdx.x;
-        warp = tid >> 5;
-        lane = tid & 31;
+    // What the loads need.
+    __device__ __forceinline__ void begin(const Problem& p, uint8_t* smem) {
+        warp = threadIdx.x >> 5;
+        lane = threadIdx.x & 31;
         g = lane >> 2;
         c2 = (lane & 3) * 2;
         rows = p.group * s.q_len;
-        ring = smem_addr(smem) + warp * kFewStages * few_stage_bytes<WEIGHT>();
-        uint8_t* at = smem + kFewWarps * kFewStages * few_stage_bytes<WEIGHT>();
-        const uint32_t sQ = smem_addr(at);
-        uint8_t* m = at + MT * 16 * 128;
-        float* t = reinterpret_cast<float*>(m + ((2 * p.D + 1 + 15) & ~15));
-        map = m;
-        tab = t;
+        ring = smem_addr(smem) + warp * kFewStages * kStage;
         const int64_t head = z * p.kv_head;
         kb = p.k + s.k_start * p.kv_tok + head;
         vb = p.v + s.k_start * p.kv_tok + head;
+    }
+    // What the scores need (the first blocks are on their way meanwhile).
+    __device__ __forceinline__ void setup(const Problem& p, uint8_t* smem) {
+        const int tid = threadIdx.x;
+        uint8_t* sq = smem + kFewWarps * kFewStages * kStage;
+        uint8_t* m = sq + MT * 16 * 128;
+        float* t = reinterpret_cast<float*>(m + ((2 * p.D + 1 + 15) & ~15));
+        map = m;
+        tab = t;
         for (int i = tid; i < MT * 16 * 8; i += kFewThreads) {
             const int r = i >> 3, c = i & 7;
-            const bool in = r < rows;
-            const uint16_t* src = in ? p.q + static_cast<int64_t>(s.q_start + query_of(r)) * p.q_tok + head_of(p, r) * p.q_head + c * 8 : p.q;
-            cp_async_16(sQ + mma_attn::swz(r, c), src, in ? 16 : 0);
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (r < rows)
+                w = __ldg(reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(s.q_start + query_of(r)) * p.q_tok + head_of(p, r) * p.q_head) + c);
+            *reinterpret_cast<uint4*>(sq + mma_attn::swz(r, c)) = w;
         }
-        cp_async_commit();
         for (int i = tid; i < p.num_buckets * MT * 16; i += kFewThreads) {
             const int b = i / (MT * 16), r = i - b * (MT * 16);
             t[i] = r < rows ? bias_log2<T>(__ldg(p.table + static_cast<int64_t>(b) * p.H + head_of(p, r))) : 0.f;
@@ -127,8 +131,8 @@ struct Few {
                 const int r = t2 * 16 + g + 8 * k;
                 pq[t2][k] = r < rows ? query_pos(p, s, query_of(r)) : q_min;
             }
-        cp_async_wait<0>();
         __syncthreads();
+        const uint32_t sQ = smem_addr(sq);
 #pragma unroll
         for (int t2 = 0; t2 < MT; ++t2) {
 #pragma unroll
@@ -145,7 +149,7 @@ struct Few {
         const int b = map[index];
         return b == 255 ? 0.f : tab[b * (MT * 16) + row];
     }
-    __device__ __forceinline__ uint32_t stage(int n) const { return ring + (n % kFewStages) * few_stage_bytes<WEIGHT>(); }
+    __device__ __forceinline__ uint32_t stage(int n) const { return ring + (n % kFewStages) * kStage; }
     // One block of keys (and values, positions) into stage n of this warp's ring.
     __device__ __forceinline__ void load(const Problem& p, int n, int key0) const {
         const uint32_t st = stage(n);
@@ -160,7 +164,7 @@ struct Few {
         }
         if (p.pos_k != nullptr && lane < kFewKeys) {
             const int row = min(key0 + lane, s.k_len - 1);   // past the end: a position of the block
-            cp_async_4(st + few_stage_bytes<WEIGHT>() - kFewKeys * 4 + 4 * lane, p.pos_k + s.k_start + row, 4);
+            cp_async_4(st + kStage - kFewKeys * 4 + 4 * lane, p.pos_k + s.k_start + row, 4);
         }
     }
     // Scores in base 2 of block n (keys from key0): x[tile][8 keys][row g: 2 columns, row g + 8: 2 columns].
@@ -182,31 +186,50 @@ struct Few {
                 mma_attn::Mma<T>::run(x[t][1], qf[t][ks], b[2], b[3]);
             }
         }
-        // Positions of the block's keys, lane by lane; a block past either end of the map has one bias per row.
-        const uint32_t pos = st + few_stage_bytes<WEIGHT>() - kFewKeys * 4;
-        int mine = min(key0 + (lane & 15), s.k_len - 1);
-        if (p.pos_k != nullptr) asm volatile("ld.shared.s32 %0, [%1];" : "=r"(mine) : "r"(pos + 4 * (lane & 15)) : "memory");
-        const int64_t lo = __reduce_min_sync(0xffffffffu, mine), hi = __reduce_max_sync(0xffffffffu, mine);
-        const bool all_left = hi - q_min <= -p.D, all_right = lo - q_max >= p.D;
+        // A block whose keys are all past one end of the map has one bias per row.
+        int mine = key0 + (lane & 15);
+        int64_t lo = key0, hi = key0 + kFewKeys - 1;
+        if (p.pos_k != nullptr) {
+            asm volatile("ld.shared.s32 %0, [%1];" : "=r"(mine) : "r"(st + kStage - kFewKeys * 4 + 4 * (lane & 15)) : "memory");
+            lo = __reduce_min_sync(0xffffffffu, mine);
+            hi = __reduce_max_sync(0xffffffffu, mine);
+        }
+        const bool all_left = hi - q_min <= -p.D;
+        if (all_left || lo - q_max >= p.D) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int col = i * 8 + c2 + j;
-                const int pk = __shfl_sync(0xffffffffu, mine, col);
-                const bool in = key0 + col < s.k_len;
+                for (int k = 0; k < 2; ++k) {
+                    const float e = all_left ? left[t][k] : right[t][k];
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float e;
-                        if (all_left) e = left[t][k];
-                        else if (all_right) e = right[t][k];
-                        else e = entry(t * 16 + g + 8 * k, max(-p.D, min(p.D, pos_diff(pk, pq[t][k]))) + p.D);
-                        float& v = x[t][i][2 * k + j];
-                        v = in ? fmaf(v, p.scale_log2, e) : -INFINITY;
-                    }
-            }
+                        for (int j = 0; j < 2; ++j) x[t][i][2 * k + j] = fmaf(x[t][i][2 * k + j], p.scale_log2, e);
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int pk = __shfl_sync(0xffffffffu, mine, i * 8 + c2 + j);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int d = max(-p.D, min(p.D, pos_diff(pk, pq[t][k])));
+                            x[t][i][2 * k + j] = fmaf(x[t][i][2 * k + j], p.scale_log2, entry(t * 16 + g + 8 * k, d + p.D));
+                        }
+                }
+        }
+        if (key0 + kFewKeys > s.k_len) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (key0 + i * 8 + c2 + j >= s.k_len)
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) x[t][i][j] = x[t][i][2 + j] = -INFINITY;
+        }
     }
 };
 
@@ -220,11 +243,17 @@ __global__ void __launch_bounds__(kFewThreads) bias_few_kernel(const Problem p, 
     Few<T, MT, false> f;
     f.z = blockIdx.y;
     if (!read_pair(p, blockIdx.z, f.s) || f.s.q_len == 0) return;   // the same for the whole cluster
-    f.setup(p, few_smem);
+    f.begin(p, few_smem);
     const int blocks = (f.s.k_len + kFewKeys - 1) / kFewKeys;
     const int per = (blocks + splits * kFewWarps - 1) / (splits * kFewWarps);   // of one warp
     // A CTA's blocks are one run of keys; its warps take them in turn.
     const int first = min(blocks, rank * per * kFewWarps) + f.warp, end = min(blocks, (rank + 1) * per * kFewWarps);
+#pragma unroll
+    for (int n = 0; n < kFewStages - 1; ++n) {
+        if (first + n * kFewWarps < end) f.load(p, n, (first + n * kFewWarps) * kFewKeys);
+        cp_async_commit();
+    }
+    f.setup(p, few_smem);
     float m[MT][2], l[MT][2], o[MT][8][4];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
@@ -234,11 +263,6 @@ __global__ void __launch_bounds__(kFewThreads) bias_few_kernel(const Problem p, 
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[t][i][j] = 0.f;
-    }
-#pragma unroll
-    for (int n = 0; n < kFewStages - 1; ++n) {
-        if (first + n * kFewWarps < end) f.load(p, n, (first + n * kFewWarps) * kFewKeys);
-        cp_async_commit();
     }
     int n = 0;
     for (int blk = first; blk < end; blk += kFewWarps, ++n) {
@@ -252,38 +276,40 @@ __global__ void __launch_bounds__(kFewThreads) bias_few_kernel(const Problem p, 
         uint32_t hi[MT][4], lo[MT][4];
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            float alpha[2], ref[2];
+            // The reference maximum is raised only by a block that exceeds it by 2^8
+            // (the first one always does); until then lanes need not agree on a maximum.
+            bool grow = false;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float v = fmaxf(fmaxf(x[t][0][2 * k], x[t][0][2 * k + 1]), fmaxf(x[t][1][2 * k], x[t][1][2 * k + 1]));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                const float next = fmaxf(m[t][k], v);
-                ref[k] = next == -INFINITY ? 0.f : next;
-                alpha[k] = mma_attn::fast_exp2(m[t][k] - ref[k]);
-                m[t][k] = next;
-            }
-            if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+            for (int k = 0; k < 2; ++k)
+                grow |= fmaxf(fmaxf(x[t][0][2 * k], x[t][0][2 * k + 1]), fmaxf(x[t][1][2 * k], x[t][1][2 * k + 1])) > m[t][k] + 8.f;
+            if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    o[t][i][0] *= alpha[0];
-                    o[t][i][1] *= alpha[0];
-                    o[t][i][2] *= alpha[1];
-                    o[t][i][3] *= alpha[1];
+                for (int k = 0; k < 2; ++k) {
+                    float v = fmaxf(fmaxf(x[t][0][2 * k], x[t][0][2 * k + 1]), fmaxf(x[t][1][2 * k], x[t][1][2 * k + 1]));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                    const float next = fmaxf(m[t][k], v);
+                    const float alpha = next == -INFINITY ? 1.f : mma_attn::fast_exp2(m[t][k] - next);
+                    m[t][k] = next;
+                    l[t][k] *= alpha;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        o[t][i][2 * k] *= alpha;
+                        o[t][i][2 * k + 1] *= alpha;
+                    }
                 }
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                float sum = 0.f;
+                const float ref = m[t][k] == -INFINITY ? 0.f : m[t][k];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float a = mma_attn::fast_exp2(x[t][i][2 * k] - ref[k]), b = mma_attn::fast_exp2(x[t][i][2 * k + 1] - ref[k]);
-                    sum += a + b;
+                    const float a = mma_attn::fast_exp2(x[t][i][2 * k] - ref), b = mma_attn::fast_exp2(x[t][i][2 * k + 1] - ref);
+                    l[t][k] += a + b;
                     const uint32_t w = mma_attn::Mma<T>::pack(a, b);
                     hi[t][2 * i + k] = w;
                     lo[t][2 * i + k] = pack_rest<T>(a, b, w);
                 }
-                l[t][k] = l[t][k] * alpha[k] + sum;
             }
         }
         const uint32_t sv = f.stage(n) + kFewKeys * 128;
@@ -402,8 +428,23 @@ __global__ void __launch_bounds__(kFewThreads)
                 weight[at + h * weight_stride + j] = prev != nullptr ? prev[at + h * weight_stride + j] : 0.f;
         return;
     }
-    f.setup(p, few_smem);
+    f.begin(p, few_smem);
     const int first = begin + f.warp;
+    // The weights so far travel with the keys: [head][16 keys] of a stage, where there are any.
+    auto load = [&](int n, int blk) {
+        f.load(p, n, blk * kFewKeys);
+        if (prev != nullptr)
+            for (int i = f.lane; i < p.group * kFewKeys; i += 32) {
+                const int h = i / kFewKeys, j = blk * kFewKeys + i % kFewKeys;
+                cp_async_4(f.stage(n) + kFewKeys * 128 + 4 * i, prev + at + h * weight_stride + min(j, f.s.k_len - 1), 4);
+            }
+    };
+#pragma unroll
+    for (int n = 0; n < kFewStages - 1; ++n) {
+        if (first + n * kFewWarps < end) load(n, first + n * kFewWarps);
+        cp_async_commit();
+    }
+    f.setup(p, few_smem);
     float lse[MT][2];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -412,29 +453,12 @@ __global__ void __launch_bounds__(kFewThreads)
             const int r = t * 16 + f.g + 8 * k;
             lse[t][k] = r < f.rows ? lse_log2(__ldg(p.lse + f.head_of(p, r) * p.lse_stride + f.s.q_start + f.query_of(r))) : INFINITY;
         }
-    // A lane's share of the results: key lane % 16 of heads lane / 16, + 2, ...; what they held
-    // before is loaded one block ahead.
-    const int key = f.lane & 15, h0 = f.lane >> 4;
-    float old[MT * 8];
-    auto load_old = [&](int blk) {
-#pragma unroll
-        for (int i = 0; i < MT * 8; ++i) {
-            const int h = h0 + 2 * i, j = blk * kFewKeys + key;
-            old[i] = prev != nullptr && h < p.group && blk < end && j < f.s.k_len ? prev[at + h * weight_stride + j] : 0.f;
-        }
-    };
-    load_old(first);
-#pragma unroll
-    for (int n = 0; n < kFewStages - 1; ++n) {
-        if (first + n * kFewWarps < end) f.load(p, n, (first + n * kFewWarps) * kFewKeys);
-        cp_async_commit();
-    }
     int n = 0;
     for (int blk = first; blk < end; blk += kFewWarps, ++n) {
         cp_async_wait<kFewStages - 2>();
         __syncwarp();
         const int ahead = blk + (kFewStages - 1) * kFewWarps;
-        if (ahead < end) f.load(p, n + kFewStages - 1, ahead * kFewKeys);
+        if (ahead < end) load(n + kFewStages - 1, ahead);
         cp_async_commit();
         float x[MT][2][4];
         f.scores(p, n, blk * kFewKeys, x);
@@ -446,18 +470,18 @@ __global__ void __launch_bounds__(kFewThreads)
                 for (int j = 0; j < 4; ++j)
                     s_p[f.warp][t * 16 + f.g + 8 * (j >> 1)][i * 8 + f.c2 + (j & 1)] = mma_attn::fast_exp2(x[t][i][j] - lse[t][j >> 1]);
         __syncwarp();
-        const int j = blk * kFewKeys + key;
-#pragma unroll
-        for (int i = 0; i < MT * 8; ++i) {
-            const int h = h0 + 2 * i;
-            if (h < p.group && j < f.s.k_len) {
+        // Key lane % 16 of heads lane / 16, + 2, ...: this block's sums over the queries, in their order.
+        const int key = f.lane & 15, j = blk * kFewKeys + key;
+        if (j < f.s.k_len)
+            for (int h = f.lane >> 4; h < p.group; h += 2) {
                 float sum = 0.f;
                 for (int q = 0; q < f.s.q_len; ++q) sum += s_p[f.warp][h * f.s.q_len + q][key];
-                weight[at + h * weight_stride + j] = old[i] + sum;
+                float old = 0.f;
+                if (prev != nullptr)
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(old) : "r"(f.stage(n) + kFewKeys * 128 + 4 * (h * kFewKeys + key)) : "memory");
+                weight[at + h * weight_stride + j] = old + sum;
             }
-        }
-        load_old(blk + kFewWarps);
-        __syncwarp();
+        __syncwarp();   // the stage and s_p may be overwritten
     }
     cp_async_wait<0>();
 }
