@@ -497,6 +497,7 @@ RAGGED_API ragged_status ragged_attn_weight(const ragged_bias_attn *problem, con
  *   rows          device rows of row_bytes (a multiple of 16), 16-byte aligned;
  *                 or NULL with rows_out NULL: only the selection.
  *   weight        device float [H, weight_stride], as ragged_attn_weight writes.
+ *   tokens        rows of the input (at least cu_seqlens[B]).
  *   cu_seqlens    device int32 [B + 1], 0 <= B <= 65535;  1 <= max_seqlen <=
  *                 RAGGED_MAX_TOKENS bounds every L_b (a longer sequence keeps
  *                 nothing and sets RAGGED_DEV_BAD_SEQLENS).
@@ -509,13 +510,18 @@ RAGGED_API ragged_status ragged_attn_weight(const ragged_bias_attn *problem, con
  *   src_idx       int32 [capacity];
  *   weight_out    float [H, weight_out_stride >= capacity] or NULL;
  *   pos_out       int32 [capacity] or NULL.
+ *   workspace     device scratch of this call, 16-byte aligned: 4 * tokens
+ *                 bytes where max_seqlen is above RAGGED_EVICT_ONE_LAUNCH; not
+ *                 used (may be NULL) up to there.
  * Outputs must not overlap inputs.  Rows past cu_out[B] are not written.
  */
+#define RAGGED_EVICT_ONE_LAUNCH 1024
 RAGGED_API ragged_status ragged_evict(const void *rows, int64_t row_bytes, const float *weight, int64_t weight_stride,
-                                      int64_t H, const int32_t *cu_seqlens, int64_t B, int64_t max_seqlen,
+                                      int64_t H, int64_t tokens, const int32_t *cu_seqlens, int64_t B, int64_t max_seqlen,
                                       const int32_t *budget, int64_t sinks, int64_t recents, const int32_t *pos,
                                       int64_t capacity, void *rows_out, int32_t *cu_out, int32_t *src_idx,
-                                      float *weight_out, int64_t weight_out_stride, int32_t *pos_out, void *stream);
+                                      float *weight_out, int64_t weight_out_stride, int32_t *pos_out,
+                                      void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
  * ragged_get_device_status - read and clear the status word of the current

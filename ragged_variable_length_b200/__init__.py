@@ -46,6 +46,7 @@ RAGGED_DEV_BAD_BUCKETS = 0x4
 RAGGED_DEV_CAPACITY = 0x8
 RAGGED_MAX_TOKENS = 16384
 RAGGED_NOALLOC_SCRATCH_BYTES = 16 << 20
+RAGGED_EVICT_ONE_LAUNCH = 1024
 RAGGED_PIPELINE_AUTO = 0
 RAGGED_PIPELINE_FUSED = 1
 RAGGED_PIPELINE_SPLIT = 2
@@ -120,7 +121,8 @@ def load(path: Optional[str] = None):
     lib.ragged_attn_bias_bwd_workspace.argtypes = [problem, size]
     lib.ragged_attn_bias_bwd.argtypes = [problem, vp, i64, vp, i64, vp, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp]
     lib.ragged_attn_weight.argtypes = [problem, vp, vp, i64, vp]
-    lib.ragged_evict.argtypes = [vp, i64, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp]
+    lib.ragged_evict.argtypes = [vp, i64, vp, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, vp, vp, i64, vp,
+                                 vp, i64, vp]
     for name in ("ragged_rel_buckets", "ragged_attn_bias_fwd_workspace", "ragged_attn_bias_fwd",
                  "ragged_attn_bias_bwd_workspace", "ragged_attn_bias_bwd", "ragged_attn_weight", "ragged_evict"):
         getattr(lib, name).restype = ctypes.c_int
@@ -584,16 +586,18 @@ def ragged_evict(rows: Optional[torch.Tensor], weight: torch.Tensor, cu_seqlens:
     rows_out = None if rows is None else rows.new_empty((n,) + rows.shape[1:])
     cu_out, src_idx, pos_out = cu_seqlens.new_empty(2 * n + B + 1).split_with_sizes((B + 1, n, n))
     weight_out = weight.new_empty((H, n))
+    ws = weight.new_empty(T) if max_seqlen > RAGGED_EVICT_ONE_LAUNCH and T else None
     copy = rows is not None and n > 0 and T > 0
     row_bytes = rows.stride(0) * rows.element_size() if copy else 0
     some = cu_seqlens.data_ptr()
     status = load().ragged_evict(rows.data_ptr() if copy else None, row_bytes, weight.data_ptr() or some,
-                                 weight.stride(0) if H > 1 else 0, H, some, B, int(max_seqlen),
+                                 weight.stride(0) if H > 1 else 0, H, T, some, B, int(max_seqlen),
                                  budget.data_ptr() or some, int(sinks), int(recents),
                                  None if pos is None else pos.data_ptr() or None, n,
                                  rows_out.data_ptr() if copy else None, cu_out.data_ptr(),
                                  src_idx.data_ptr() if n else None, weight_out.data_ptr() if n else None, n,
-                                 pos_out.data_ptr() if n else None, _current_stream())
+                                 pos_out.data_ptr() if n else None, None if ws is None else ws.data_ptr(), 4 * T,
+                                 _current_stream())
     if status:
         _check(status)
     return rows_out, cu_out, src_idx, weight_out, pos_out

@@ -196,8 +196,6 @@ ragged_status launch_bias_weight(const ragged::bias::Problem& p, const float* pr
     return cuda_check(cudaGetLastError(), "attention weight launch");
 }
 
-DeviceFlags g_evict_smem;
-
 // x^a * y^b >= u^c * v^d in whole numbers (up to 64 factors below 2^16 each).
 struct BigUint {
     uint32_t w[72] = {1};
@@ -346,9 +344,11 @@ ragged_status ragged_attn_weight(const ragged_bias_attn* a, const float* prev, f
 }
 
 ragged_status ragged_evict(const void* rows, int64_t row_bytes, const float* weight, int64_t weight_stride, int64_t H,
-                           const int32_t* cu_seqlens, int64_t B, int64_t max_seqlen, const int32_t* budget, int64_t sinks,
-                           int64_t recents, const int32_t* pos, int64_t capacity, void* rows_out, int32_t* cu_out,
-                           int32_t* src_idx, float* weight_out, int64_t weight_out_stride, int32_t* pos_out, void* stream) {
+                           int64_t tokens, const int32_t* cu_seqlens, int64_t B, int64_t max_seqlen,
+                           const int32_t* budget, int64_t sinks, int64_t recents, const int32_t* pos, int64_t capacity,
+                           void* rows_out, int32_t* cu_out, int32_t* src_idx, float* weight_out,
+                           int64_t weight_out_stride, int32_t* pos_out, void* workspace, int64_t workspace_bytes,
+                           void* stream) {
     if (B < 0) return fail(RAGGED_ERR_INVALID_ARG, "B = %lld is negative", (long long)B);
     if (B > 65535) return fail(RAGGED_ERR_UNSUPPORTED, "B = %lld exceeds 65535", (long long)B);
     if (H < 1 || H > 65534) return fail(RAGGED_ERR_INVALID_ARG, "H = %lld outside [1, 65534]", (long long)H);
@@ -356,6 +356,8 @@ ragged_status ragged_evict(const void* rows, int64_t row_bytes, const float* wei
         return fail(RAGGED_ERR_INVALID_ARG, "max_seqlen = %lld outside [1, %d]", (long long)max_seqlen, RAGGED_MAX_TOKENS);
     if (sinks < 0 || recents < 0 || sinks > RAGGED_MAX_TOKENS || recents > RAGGED_MAX_TOKENS)
         return fail(RAGGED_ERR_INVALID_ARG, "sinks and recents must lie in [0, %d]", RAGGED_MAX_TOKENS);
+    if (tokens < 0 || tokens >= (int64_t(1) << 31))
+        return fail(RAGGED_ERR_INVALID_ARG, "tokens = %lld outside [0, 2^31)", (long long)tokens);
     if (capacity < 0 || capacity >= (int64_t(1) << 31))
         return fail(RAGGED_ERR_INVALID_ARG, "capacity = %lld outside [0, 2^31)", (long long)capacity);
     if (cu_out == nullptr || !aligned4(cu_out)) return fail(RAGGED_ERR_INVALID_ARG, "cu_out must be a 4-byte aligned device pointer");
@@ -379,19 +381,32 @@ ragged_status ragged_evict(const void* rows, int64_t row_bytes, const float* wei
         return fail(RAGGED_ERR_INVALID_ARG, "the outputs must not be the inputs");
     if (weight_stride < 0 || weight_out_stride < 0 || (weight_out != nullptr && H > 1 && weight_out_stride < capacity))
         return fail(RAGGED_ERR_INVALID_ARG, "weight strides are too small");
-    ragged::evict::Args a{weight, weight_stride, cu_seqlens, budget, pos, static_cast<int>(B), static_cast<int>(H),
-                          static_cast<int>(max_seqlen), static_cast<int>(sinks), static_cast<int>(recents), capacity,
-                          cu_out, src_idx, pos_out, weight_out, weight_out_stride, static_cast<const uint4*>(rows),
-                          static_cast<uint4*>(rows_out), static_cast<uint32_t>(rows ? row_bytes / 16 : 0)};
-    ragged_status st = ensure_smem(ragged::evict::select_kernel, RAGGED_MAX_TOKENS * 4, g_evict_smem);
+    using namespace ragged::evict;
+    const bool one_launch = max_seqlen <= kShortLen;
+    ragged_status st = check_workspace(workspace, workspace_bytes, one_launch ? 0 : 4 * tokens);
     if (st != RAGGED_OK) return st;
-    ragged::evict::select_kernel<<<static_cast<unsigned>(B), ragged::evict::kThreads, static_cast<size_t>(max_seqlen) * 4, s>>>(a);
+    Args a{weight, weight_stride, cu_seqlens, budget, pos, static_cast<int>(B), static_cast<int>(H),
+           static_cast<int>(max_seqlen), static_cast<int>(sinks), static_cast<int>(recents), capacity, cu_out, src_idx,
+           pos_out, capacity > 0 ? weight_out : nullptr, weight_out_stride, static_cast<const uint4*>(rows),
+           static_cast<uint4*>(rows_out), static_cast<uint32_t>(rows ? row_bytes / 16 : 0),
+           static_cast<uint32_t*>(workspace), tokens};
+    if (capacity == 0) a.rows = nullptr;
+    if (one_launch) {
+        // A few CTAs per sequence where there are few sequences: the selection is
+        // short enough to be repeated, the rows are shared out.
+        const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(4LL * sm_count() / B, (max_seqlen + 15) / 16));
+        short_kernel<<<dim3(static_cast<unsigned>(splits), static_cast<unsigned>(B)), kShortThreads, 0, s>>>(a);
+        return cuda_check(cudaGetLastError(), "evict launch");
+    }
+    keys_kernel<<<dim3(static_cast<unsigned>((max_seqlen + 255) / 256), static_cast<unsigned>(B)), 256, 0, s>>>(a);
+    st = cuda_check(cudaGetLastError(), "evict key launch");
+    if (st != RAGGED_OK) return st;
+    long_kernel<<<static_cast<unsigned>(B), kLongThreads, 0, s>>>(a);
     st = cuda_check(cudaGetLastError(), "evict selection launch");
-    if (st != RAGGED_OK || capacity == 0 || (rows == nullptr && weight_out == nullptr)) return st;
-    const int64_t warps = ragged::evict::kCopyThreads / 32;
-    const int64_t blocks = std::min<int64_t>((capacity + warps - 1) / warps, 16LL * sm_count());
-    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(weight_out ? 1 + H : 1));
-    ragged::evict::copy_kernel<<<grid, ragged::evict::kCopyThreads, 0, s>>>(a);
+    if (st != RAGGED_OK || (a.rows == nullptr && a.weight_out == nullptr)) return st;
+    const dim3 grid(static_cast<unsigned>((capacity + kCopyThreads - 1) / kCopyThreads),
+                    static_cast<unsigned>(a.weight_out ? 1 + H : 1));
+    copy_kernel<<<grid, kCopyThreads, 0, s>>>(a);
     return cuda_check(cudaGetLastError(), "evict copy launch");
 }
 

@@ -110,18 +110,20 @@ EVICTS = [
     (dict(row_bytes=24), BAD, "multiple of 16"), (dict(row_bytes=0), BAD, "multiple of 16"), (dict(rows=A8), BAD, "16-byte"),
     (dict(rows=3 * A16), BAD, "rows_out must not be rows"), (dict(weight=A2), BAD, "4-byte"), (dict(pos=A2), BAD, "4-byte"),
     (dict(weight_out=A16), BAD, "the outputs"), (dict(cu_out=A16), BAD, "the outputs"), (dict(pos=5 * A16), BAD, "the outputs"),
-    (dict(weight_out_stride=100), BAD, "stride"), (dict(weight_stride=-1), BAD, "stride"),
+    (dict(weight_out_stride=100), BAD, "stride"), (dict(weight_stride=-1), BAD, "stride"), (dict(tokens=-1), BAD, "tokens"),
+    (dict(max_seqlen=1025, ws=None), BAD, "workspace"), (dict(max_seqlen=1025, ws_bytes=1596), BAD, "workspace"),
+    (dict(max_seqlen=1025, ws=A8), BAD, "workspace"),
 ]
 
 
 @pytest.mark.parametrize("kw,status,needle", EVICTS, ids=[str(p[0]) for p in EVICTS])
 def test_evict_rejects(lib, kw, status, needle):
-    a = dict(rows=A16, row_bytes=768, weight=A16, weight_stride=400, H=6, cu=A16, B=2, max_seqlen=197, budget=A16, sinks=1, recents=0, pos=None,
+    a = dict(rows=A16, row_bytes=768, weight=A16, weight_stride=400, H=6, tokens=400, ws=A16, ws_bytes=1600, cu=A16, B=2, max_seqlen=197, budget=A16, sinks=1, recents=0, pos=None,
              capacity=400, rows_out=3 * A16, cu_out=2 * A16, src=2 * A16, weight_out=4 * A16, weight_out_stride=400, pos_out=5 * A16)
     a.update(kw)
-    assert lib.ragged_evict(a["rows"], a["row_bytes"], a["weight"], a["weight_stride"], a["H"], a["cu"], a["B"], a["max_seqlen"], a["budget"],
+    assert lib.ragged_evict(a["rows"], a["row_bytes"], a["weight"], a["weight_stride"], a["H"], a["tokens"], a["cu"], a["B"], a["max_seqlen"], a["budget"],
                             a["sinks"], a["recents"], a["pos"], a["capacity"], a["rows_out"], a["cu_out"], a["src"], a["weight_out"],
-                            a["weight_out_stride"], a["pos_out"], None) == status
+                            a["weight_out_stride"], a["pos_out"], a["ws"], a["ws_bytes"], None) == status
     assert needle in rv.ragged_last_error()
 
 
