@@ -360,85 +360,25 @@ def _on_stream(stream):
     return torch.cuda.stream(stream)
 
 
-def _same_device(*tensors) -> None:
-    """One device for all, and the current one: the library launches there."""
-    index = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"a tensor is on {t.device}, not on the current CUDA device {index}")
+_tc = None
 
 
-_i32 = torch.int32
-
-
-def _int32(t: torch.Tensor, n: int, what: str) -> None:
-    if t.dtype is not _i32 or t.dim() != 1 or not t.is_contiguous() or (n >= 0 and t.shape[0] != n):
-        raise ValueError(f"{what} must be contiguous int32" + (f" [{n}]" if n >= 0 else ""))
-
-
-def _bias_problem(q, k, v, cu_q, cu_k, max_q, max_k, table, buckets, pos_q, pos_k, scale, lse) -> BiasAttn:
-    """The checked problem of the three attention operators with a position bias (v: k where it is not read)."""
-    Tq, H, d = q.shape
-    shape = k.shape
-    dt = q.dtype
-    q_tok, q_head, q_one = q.stride()
-    ks = k.stride()
-    if v.shape != shape or shape[2] != d or k.dtype is not dt or v.dtype is not dt or table.dtype is not dt:
-        raise ValueError("q [Tq, H, d], k and v [Tk, Hkv, d] and table must have one dtype and head_dim")
-    if q_one != 1 or ks[2] != 1 or v.stride() != ks:
-        raise ValueError("q, k and v need a unit innermost stride, and k and v the same strides")
-    nb, heads = table.shape
-    if heads != H or not table.is_contiguous():
-        raise ValueError("table must be contiguous [num_buckets, H]")
-    _int32(cu_q, -1, "cu_seqlens_q")
-    B = cu_q.shape[0] - 1
-    if cu_k is not cu_q:
-        _int32(cu_k, B + 1, "cu_seqlens_k")
-    _int32(buckets, -1, "buckets")
-    entries = buckets.shape[0]
-    if entries % 2 == 0:
-        raise ValueError("buckets must have an odd length, 2 * max_distance + 1")
-    if pos_q is not None:
-        _int32(pos_q, Tq, "pos_q")
-    if pos_k is not None:
-        _int32(pos_k, shape[0], "pos_k")
-    if lse.dtype is not torch.float32 or lse.shape != (H, Tq) or (Tq > 1 and lse.stride(1) != 1):
-        raise ValueError("lse must be float32 [H, Tq] with unit innermost stride")
-    _same_device(q, k, v, cu_q, cu_k, table, buckets, pos_q, pos_k, lse)
-    some = cu_q.data_ptr()   # stands for the address of a tensor without elements, which is never read
-    return BiasAttn(q.data_ptr() or some, k.data_ptr() or some, v.data_ptr() or some, q_tok, q_head, ks[0], ks[1],
-                    some, cu_k.data_ptr(), B, max_q, max_k, H, shape[1], d, table.data_ptr(), buckets.data_ptr(), nb,
-                    entries // 2, None if pos_q is None else pos_q.data_ptr(),
-                    None if pos_k is None else pos_k.data_ptr(), lse.data_ptr() or some,
-                    lse.stride(0) if Tq else 0, d ** -0.5 if scale is None else scale, _dtype_code(q))
-
-
-def _current_stream() -> int:
-    """Handle of torch's current stream (without the Stream object around it)."""
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-
-
-def _workspace(sizer, problem, like: torch.Tensor):
-    """Scratch of one call from torch's allocator: (tensor or None, address, bytes)."""
-    n = ctypes.c_int64(0)
-    status = sizer(problem, n)
-    if status:
-        _check(status)
-    if n.value == 0:
-        return None, None, 0
-    t = like.new_empty(n.value, dtype=torch.uint8)
-    return t, t.data_ptr(), n.value
-
-
-def _heads(t: torch.Tensor, like: torch.Tensor, what: str) -> None:
-    if t.shape != like.shape or t.dtype != like.dtype or t.stride(2) != 1:
-        raise ValueError(f"{what} must have the shape and dtype of its input and a unit innermost stride")
-
-
-def _rows_of_heads(t: torch.Tensor, like: torch.Tensor, what: str) -> None:
-    _heads(t, like, what)
-    if t.shape[1] > 1 and t.stride(1) != t.shape[2]:
-        raise ValueError(f"{what} must be [T, H, head_dim] with contiguous heads")
+def _torchcall():
+    """The tensor side of the calls below (_torchcall), bound to the loaded library."""
+    global _tc
+    if _tc is None:
+        import importlib
+        try:
+            m = importlib.import_module(__name__ + "._torchcall")
+        except ImportError as e:
+            raise RuntimeError("the _torchcall extension is missing: build it with "
+                               "`python -m ragged_variable_length_b200.build`") from e
+        lib = load()
+        m.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
+                 ("ragged_attn_bias_fwd_workspace", "ragged_attn_bias_fwd", "ragged_attn_bias_bwd_workspace",
+                  "ragged_attn_bias_bwd", "ragged_attn_weight", "ragged_evict")])
+        _tc = m
+    return _tc
 
 
 def ragged_attn_bias_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
@@ -454,23 +394,11 @@ def ragged_attn_bias_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_s
         with _on_stream(stream):
             return ragged_attn_bias_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table,
                                         buckets, pos_q, pos_k, scale, out, lse)
-    Tq, H, d = q.shape
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    else:
-        _rows_of_heads(out, q, "out")
-        _same_device(out)
-    if lse is None:
-        lse = q.new_empty((H, Tq), dtype=torch.float32)
-    p = _bias_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table, buckets, pos_q, pos_k,
-                      scale, lse)
-    lib = load()
-    ws, addr, size = _workspace(lib.ragged_attn_bias_fwd_workspace, p, q)
-    status = lib.ragged_attn_bias_fwd(p, out.data_ptr() or p.cu_seqlens_q, out.stride(0) if Tq > 1 else H * d, addr, size,
-                                      _current_stream())
-    if status:
-        _check(status)
-    return out, lse
+    r = (_tc or _torchcall()).bias_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table, buckets,
+                                       pos_q, pos_k, scale, out, lse)
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 def ragged_attn_bias_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
@@ -487,45 +415,11 @@ def ragged_attn_bias_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v
         with _on_stream(stream):
             return ragged_attn_bias_bwd(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                                         max_seqlen_k, table, buckets, pos_q, pos_k, scale, dq, dk, dv, dtable)
-    Tq, H, d = q.shape
-    _rows_of_heads(out, q, "out")
-    if dout.shape != q.shape or dout.dtype != q.dtype:
-        raise ValueError("dout must have the shape and dtype of out")
-    if dout.stride(2) != 1 or (H > 1 and dout.stride(1) != d) or (Tq > 1 and dout.stride(0) < H * d):
-        dout = dout.contiguous()   # a broadcast or transposed gradient
-    plain = torch.contiguous_format
-    if dq is None:
-        dq = torch.empty_like(q, memory_format=plain)
-    else:
-        _heads(dq, q, "dq")
-    if dk is None:
-        dk = torch.empty_like(k, memory_format=plain)
-    else:
-        _heads(dk, k, "dk")
-    if dv is None:
-        dv = torch.empty_like(v, memory_format=plain)
-    else:
-        _heads(dv, v, "dv")
-    if dk.shape[0] and dk.stride() != dv.stride():
-        raise ValueError("dk and dv must have the same strides")
-    if dtable is None:
-        dtable = torch.empty_like(table, memory_format=plain)
-    elif dtable.shape != table.shape or dtable.dtype is not table.dtype or not dtable.is_contiguous():
-        raise ValueError("dtable must be contiguous with the shape and dtype of table")
-    _same_device(dout, out, dq, dk, dv, dtable)
-    p = _bias_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table, buckets, pos_q, pos_k,
-                      scale, lse)
-    lib = load()
-    ws, addr, size = _workspace(lib.ragged_attn_bias_bwd_workspace, p, q)
-    some = p.cu_seqlens_q
-    status = lib.ragged_attn_bias_bwd(p, out.data_ptr() or some, out.stride(0) if Tq > 1 else H * d,
-                                      dout.data_ptr() or some, dout.stride(0) if Tq > 1 else H * d,
-                                      dq.data_ptr() or some, dq.stride(0), dq.stride(1), dk.data_ptr() or some,
-                                      dv.data_ptr() or some, dk.stride(0), dk.stride(1), dtable.data_ptr(), addr, size,
-                                      _current_stream())
-    if status:
-        _check(status)
-    return dq, dk, dv, dtable
+    r = (_tc or _torchcall()).bias_bwd(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+                                       table, buckets, pos_q, pos_k, scale, dq, dk, dv, dtable)
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 def ragged_attn_weight(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, cu_seqlens_q: torch.Tensor,
@@ -540,22 +434,11 @@ def ragged_attn_weight(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, cu_s
         with _on_stream(stream):
             return ragged_attn_weight(q, k, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table,
                                       buckets, pos_q, pos_k, scale, prev, weight)
-    H, Tk = q.shape[1], k.shape[0]
-    if weight is None:
-        weight = k.new_empty((H, Tk), dtype=torch.float32)
-    ws = weight.stride(0) if H > 1 else Tk
-    for t, what in ((weight, "weight"), (prev, "prev")):
-        if t is not None and (t.dtype is not torch.float32 or t.shape != (H, Tk) or (Tk > 1 and t.stride(1) != 1) or
-                              (H > 1 and t.stride(0) != ws)):
-            raise ValueError(f"{what} must be float32 [H, Tk] with unit innermost stride, prev as weight")
-    _same_device(weight, prev)
-    p = _bias_problem(q, k, k, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table, buckets, pos_q, pos_k,
-                      scale, lse)
-    status = load().ragged_attn_weight(p, None if prev is None else prev.data_ptr() or None,
-                                       weight.data_ptr() or p.cu_seqlens_q, ws, _current_stream())
-    if status:
-        _check(status)
-    return weight
+    r = (_tc or _torchcall()).attn_weight(q, k, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table,
+                                          buckets, pos_q, pos_k, scale, prev, weight)
+    if r.__class__ is int:
+        _check(r)
+    return r[0]
 
 
 def ragged_evict(rows: Optional[torch.Tensor], weight: torch.Tensor, cu_seqlens: torch.Tensor, max_seqlen: int,
@@ -571,36 +454,10 @@ def ragged_evict(rows: Optional[torch.Tensor], weight: torch.Tensor, cu_seqlens:
     if stream is not None:
         with _on_stream(stream):
             return ragged_evict(rows, weight, cu_seqlens, max_seqlen, budget, sinks, recents, pos, total)
-    H, T = weight.shape
-    B = cu_seqlens.shape[0] - 1
-    if weight.dtype is not torch.float32 or (T > 1 and weight.stride(1) != 1):
-        raise ValueError("weight must be float32 [H, T] with unit innermost stride")
-    if rows is not None and (rows.shape[0] != T or not rows.is_contiguous()):
-        raise ValueError("rows must be contiguous [T, ...]")
-    _int32(cu_seqlens, -1, "cu_seqlens")
-    _int32(budget, B, "budget")
-    if pos is not None:
-        _int32(pos, T, "pos")
-    _same_device(rows, weight, cu_seqlens, budget, pos)
-    n = T if total is None else int(total)
-    rows_out = None if rows is None else rows.new_empty((n,) + rows.shape[1:])
-    cu_out, src_idx, pos_out = cu_seqlens.new_empty(2 * n + B + 1).split_with_sizes((B + 1, n, n))
-    weight_out = weight.new_empty((H, n))
-    ws = weight.new_empty(T) if max_seqlen > RAGGED_EVICT_ONE_LAUNCH and T else None
-    copy = rows is not None and n > 0 and T > 0
-    row_bytes = rows.stride(0) * rows.element_size() if copy else 0
-    some = cu_seqlens.data_ptr()
-    status = load().ragged_evict(rows.data_ptr() if copy else None, row_bytes, weight.data_ptr() or some,
-                                 weight.stride(0) if H > 1 else 0, H, T, some, B, int(max_seqlen),
-                                 budget.data_ptr() or some, int(sinks), int(recents),
-                                 None if pos is None else pos.data_ptr() or None, n,
-                                 rows_out.data_ptr() if copy else None, cu_out.data_ptr(),
-                                 src_idx.data_ptr() if n else None, weight_out.data_ptr() if n else None, n,
-                                 pos_out.data_ptr() if n else None, None if ws is None else ws.data_ptr(), 4 * T,
-                                 _current_stream())
-    if status:
-        _check(status)
-    return rows_out, cu_out, src_idx, weight_out, pos_out
+    r = (_tc or _torchcall()).evict(rows, weight, cu_seqlens, max_seqlen, budget, sinks, recents, pos, total)
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 class _PipelineArgs(ctypes.Structure):

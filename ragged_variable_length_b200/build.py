@@ -1,4 +1,5 @@
-"""Builds libragged.so (the CUDA kernels and their C ABI) for sm_100a with nvcc.
+"""Builds libragged.so (the CUDA kernels and their C ABI) for sm_100a with nvcc,
+and the two CPython extensions of the binding.
 
     python -m ragged_variable_length_b200.build [--force] [--verbose-ptxas]
 
@@ -76,6 +77,36 @@ def build_fastcall(force: bool = False) -> str:
     return out
 
 
+TORCHCALL_SRC = os.path.join(CSRC, "torchcall.cpp")
+
+
+def torchcall_path() -> str:
+    import sysconfig
+    return os.path.join(HERE, "_torchcall" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def build_torchcall(force: bool = False) -> str:
+    """CPython extension with the tensor side of the position-bias and eviction calls (against torch's C++ headers)."""
+    import sysconfig
+
+    import torch
+    out = torchcall_path()
+    deps = [TORCHCALL_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))]
+    if not force and os.path.exists(out) and all(os.path.getmtime(out) >= os.path.getmtime(d) for d in deps):
+        return out
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = f"{out}.{os.getpid()}.tmp"
+    headers = [sysconfig.get_paths()["include"], f"{base}/include", f"{base}/include/torch/csrc/api/include",
+               f"{cuda}/include"]
+    subprocess.run(["g++", "-O2", "-std=c++17", "-Wall", "-Wno-attributes", "-shared", "-fPIC",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+                    *[x for h in headers for x in ("-isystem", h)], TORCHCALL_SRC, "-o", tmp, f"-L{base}/lib",
+                    "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], check=True)
+    os.replace(tmp, out)
+    return out
+
+
 def _compile(lib: str, force: bool, ptxas_verbose: bool, test_hooks: bool) -> str:
     if not force and not stale(lib):
         return lib
@@ -92,6 +123,7 @@ def _compile(lib: str, force: bool, ptxas_verbose: bool, test_hooks: bool) -> st
 
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     build_fastcall(force)
+    build_torchcall(force)
     return _compile(LIB, force, ptxas_verbose, False)
 
 

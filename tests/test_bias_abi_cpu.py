@@ -162,3 +162,59 @@ def test_struct_matches_the_header(lib):
     body = re.search(r"typedef struct ragged_bias_attn \{(.*?)\} ragged_bias_attn;", text, re.S).group(1)
     names = [n.strip(" *\n") for line in body.split(";") for n in re.sub(r"^\s*(const )?\w+ ", "", line.strip()).split(",") if line.strip()]
     assert names == [n for n, _ in rv.BiasAttn._fields_]
+
+
+def _tensors(**kw):
+    """Arguments of ragged_attn_bias_fwd on the CPU: every check before the device's passes."""
+    h = torch.float16
+    a = dict(q=torch.zeros(8, 4, 64, dtype=h), k=torch.zeros(8, 2, 64, dtype=h), v=torch.zeros(8, 2, 64, dtype=h),
+             cu_seqlens_q=torch.zeros(3, dtype=torch.int32), cu_seqlens_k=torch.zeros(3, dtype=torch.int32), max_seqlen_q=8, max_seqlen_k=8,
+             table=torch.zeros(4, 4, dtype=h), buckets=torch.zeros(5, dtype=torch.int32))
+    a.update(kw)
+    return a
+
+
+I32, F16 = torch.int32, torch.float16
+REFUSED = [
+    (dict(), "current CUDA device"), (dict(q=torch.zeros(8, 4, 32, dtype=F16)), "head_dim"), (dict(q=torch.zeros(8, 4, dtype=F16)), "Tq, H"),
+    (dict(k=torch.zeros(8, 2, 64, dtype=torch.bfloat16)), "one dtype"), (dict(table=torch.zeros(4, 4)), "one dtype"),
+    (dict(v=torch.zeros(9, 2, 64, dtype=F16)), "one dtype"), (dict(v=torch.zeros(2, 8, 64, dtype=F16).transpose(0, 1)), "strides"),
+    (dict(q=torch.zeros(8, 64, 4, dtype=F16).transpose(1, 2)), "innermost"), (dict(table=torch.zeros(4, 3, dtype=F16)), "num_buckets"),
+    (dict(table=torch.zeros(4, 4, dtype=F16).t()), "contiguous"), (dict(cu_seqlens_q=torch.zeros(3)), "int32"),
+    (dict(cu_seqlens_k=torch.zeros(4, dtype=I32)), "int32"), (dict(cu_seqlens_q=torch.zeros(0, dtype=I32)), "at least one"),
+    (dict(buckets=torch.zeros(6, dtype=I32)), "odd"), (dict(buckets=torch.zeros(5)), "int32"), (dict(pos_q=torch.zeros(7, dtype=I32)), "pos_q"),
+    (dict(pos_k=torch.zeros(16, dtype=I32)[::2]), "pos_k"), (dict(lse=torch.zeros(4, 7)), "lse"), (dict(lse=torch.zeros(4, 8, dtype=F16)), "lse"),
+    (dict(lse=torch.zeros(1, 8).expand(4, 8)), "overlap"), (dict(out=torch.zeros(8, 4, 32, dtype=F16)), "out"),
+    (dict(out=torch.zeros(4, 8, 64, dtype=F16).transpose(0, 1)), "contiguous heads"), (dict(out=torch.zeros(1, 4, 64, dtype=F16).expand(8, 4, 64)), "heads"),
+]
+
+
+@pytest.mark.parametrize("kw,needle", REFUSED, ids=[str(n) + "-" + w for n, (_, w) in enumerate(REFUSED)])
+def test_attention_refuses_tensors(lib, kw, needle):
+    with pytest.raises(ValueError, match=needle):
+        rv.ragged_attn_bias_fwd(**_tensors(**kw))
+
+
+def test_gradient_weight_and_eviction_refuse_tensors(lib):
+    a = _tensors(lse=torch.zeros(4, 8))
+    rest = {n: a[n] for n in ("cu_seqlens_q", "cu_seqlens_k", "max_seqlen_q", "max_seqlen_k", "table", "buckets", "lse")}
+    bwd = dict(rest, dout=a["q"], q=a["q"], k=a["k"], v=a["v"], out=a["q"])
+    for kw, needle in ((dict(dout=a["q"][:7]), "dout"), (dict(out=a["k"]), "out"), (dict(lse=torch.zeros(4, 9)), "lse"), (dict(), "current CUDA device")):
+        with pytest.raises(ValueError, match=needle):
+            rv.ragged_attn_bias_bwd(**dict(bwd, **kw))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        rv.ragged_attn_weight(q=a["q"], k=a["k"], **rest)
+    w, cu, budget = torch.zeros(2, 9), torch.zeros(3, dtype=I32), torch.zeros(2, dtype=I32)
+    for args, needle in (((None, w.half(), cu, 9, budget), "weight"), ((None, w.t().contiguous().t(), cu, 9, budget), "weight"),
+                         ((torch.zeros(8, 8), w, cu, 9, budget), "rows"), ((torch.zeros(9, 16)[:, ::2], w, cu, 9, budget), "rows"),
+                         ((None, w, cu.long(), 9, budget), "int32"), ((None, w, cu, 9, budget[:1]), "budget"),
+                         ((None, w, cu, 9, budget, 1, 0, torch.zeros(8, dtype=I32)), "pos"), ((None, w, cu, 9, budget), "current CUDA device")):
+        with pytest.raises(ValueError, match=needle):
+            rv.ragged_evict(*args)
+    with pytest.raises(TypeError, match="tensor"):
+        rv.ragged_evict(None, w, cu, 9, None)
+
+
+def test_struct_layout_of_the_binding():
+    """ctypes' copy of the struct, which these tests use, has the size that the header's fields give."""
+    assert ctypes.sizeof(rv.BiasAttn) == 3 * 8 + 4 * 8 + 2 * 8 + 6 * 8 + 2 * 8 + 2 * 8 + 3 * 8 + 8 + 8
