@@ -81,15 +81,16 @@ int64_t bwd_workspace(const ragged_bias_attn* a) {
 }
 int64_t fwd_workspace(const ragged_bias_attn*) { return 0; }
 
-// Positions that the query-gradient kernel's expanded table covers: what two
-// CTAs per SM leave room for next to the gradient's sums, unless that is too
-// little to be of use (many buckets, or a far-reaching map): then one CTA.
-constexpr int kTwoPerSm = (228 * 1024) / 2 - 1024 - 2048;   // less the reserved and the static part
-constexpr int bwd_q_span(int D, int num_buckets) {
-    const int entries = (kTwoPerSm - ragged::bias::bwd_q_fixed_bytes(num_buckets) - 32) / 6;
+// Positions that a kernel's expanded table covers: what two CTAs per SM leave
+// room for next to `fixed` bytes, unless that is too little to be of use (many
+// buckets, or a far-reaching map): then one CTA.
+constexpr int kTwoPerSm = (228 * 1024) / 2 - 1024 - 3072;   // less the reserved and the static part
+constexpr int bias_span(int D, int fixed, int bytes_per_entry) {
+    const int entries = (kTwoPerSm - fixed - 64) / bytes_per_entry;
     const int span = (entries - 1 - ragged::bias::kVecPad) / 2 - D;
     return span < 256 ? ragged::bias::kSpan : span < ragged::bias::kSpan ? span : ragged::bias::kSpan;
 }
+constexpr int bwd_q_span(int D, int num_buckets) { return bias_span(D, ragged::bias::bwd_q_fixed_bytes(num_buckets), 6); }
 constexpr int kBwdQSmemMax = ragged::bias::bwd_q_smem_bytes(ragged::bias::kMaxDistance, ragged::bias::kMaxBuckets, ragged::bias::kSpan);
 
 ragged_status check_workspace(const void* ws, int64_t have, int64_t need) {
@@ -106,6 +107,25 @@ constexpr int kTypeSlot = std::is_same<T, __half>::value ? 0 : 1;
 
 dim3 bias_grid(int64_t tiles, int heads, int B) {
     return dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(heads), static_cast<unsigned>(B));
+}
+
+// Heads that one CTA walks over where two CTAs fit an SM: the number with the
+// least work on the fullest of the grid's slots, in units of a tile's time.  A
+// CTA's set-up costs about kSetup tiles, a head's start and end kHead.
+int heads_per_cta(int64_t row_tiles, int heads, int64_t col_tiles) {
+    constexpr int64_t kSetup = 4, kHead = 1;
+    const int64_t slots = 2LL * sm_count();
+    int best = 1;
+    int64_t best_cost = INT64_MAX;
+    for (int n = 1; n <= heads; ++n) {
+        const int64_t ctas = row_tiles * ((heads + n - 1) / n);
+        const int64_t cost = ((ctas + slots - 1) / slots) * (kSetup + n * (kHead + col_tiles));
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = n;
+        }
+    }
+    return best;
 }
 
 // Few query rows per key / value head go to the kernels that share one 16- or
@@ -160,9 +180,13 @@ ragged_status launch_bias_fwd(const ragged::bias::Problem& p, uint16_t* out, int
     using namespace ragged::bias;
     if (few_rows(p))
         return p.group * p.max_q <= 16 ? launch_few<T, 1>(p, out, out_tok, s) : launch_few<T, 2>(p, out, out_tok, s);
-    ragged_status st = ensure_smem(bias_fwd_kernel<T>, fwd_smem_bytes(kMaxDistance), g_bias_fwd_smem[kTypeSlot<T>]);
+    ragged_status st = ensure_smem(bias_fwd_kernel<T>, fwd_smem_bytes(kMaxDistance, kSpan), g_bias_fwd_smem[kTypeSlot<T>]);
     if (st != RAGGED_OK) return st;
-    bias_fwd_kernel<T><<<bias_grid(tiles128(p.max_q), p.H, p.B), kThreads, fwd_smem_bytes(p.D), s>>>(p, out, out_tok);
+    const int span = bias_span(p.D, fwd_fixed_bytes(), 5);
+    const int64_t tiles = tiles128(p.max_q);
+    const int heads = heads_per_cta(tiles * p.B, p.H, (p.max_k + kTile - 1) / kTile);
+    bias_fwd_kernel<T><<<bias_grid(tiles, (p.H + heads - 1) / heads, p.B), kThreads, fwd_smem_bytes(p.D, span), s>>>(
+        p, out, out_tok, heads, span);
     return cuda_check(cudaGetLastError(), "attention (position bias) launch");
 }
 

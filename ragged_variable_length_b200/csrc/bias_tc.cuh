@@ -55,7 +55,11 @@ enum TileKind { kGeneral = 0, kLeft = 1, kRight = 2, kConsecutive = 3, kClamped 
 
 __host__ __device__ constexpr int vec_entries(int D, int span) { return 2 * (D + span) + 1 + kVecPad; }
 
-__device__ __forceinline__ void row_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Barrier of the NR row threads.
+template <int NR = 128>
+__device__ __forceinline__ void row_barrier() {
+    asm volatile("bar.sync 1, %0;" ::"n"(NR) : "memory");
+}
 
 // The expanded table and the columns' offsets of one CTA.
 struct Bias {
@@ -69,18 +73,26 @@ struct Bias {
     int p_row;
 };
 
-// Extremes of the rows' positions over the 128 row threads.
+// Extremes of the rows' positions over the NR row threads (s_red: 2 ints per
+// warp; a barrier inside).
+template <int NR = 128>
 __device__ __forceinline__ void bias_rows(Bias& t, const Problem& p, int pos, bool valid, int span, int* s_red) {
+    constexpr int W = NR / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int lo = __reduce_min_sync(0xffffffffu, valid ? pos : INT_MAX);
     const int hi = __reduce_max_sync(0xffffffffu, valid ? pos : INT_MIN);
     if (lane == 0) {
         s_red[warp] = lo;
-        s_red[4 + warp] = hi;
+        s_red[W + warp] = hi;
     }
-    row_barrier();
-    t.rmin = min(min(s_red[0], s_red[1]), min(s_red[2], s_red[3]));
-    const int rmax = max(max(s_red[4], s_red[5]), max(s_red[6], s_red[7]));
+    row_barrier<NR>();
+    int rmax = s_red[W];
+    t.rmin = s_red[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+        t.rmin = min(t.rmin, s_red[w]);
+        rmax = max(rmax, s_red[W + w]);
+    }
     const int64_t R = static_cast<int64_t>(rmax) - t.rmin;
     t.D = p.D;
     t.near = R <= span;
@@ -88,6 +100,25 @@ __device__ __forceinline__ void bias_rows(Bias& t, const Problem& p, int pos, bo
     t.last = 2 * (t.D + t.R);
     t.p_row = pos;
     t.row = valid && t.near ? 4u * static_cast<uint32_t>(t.R - (pos - t.rmin)) : 0u;
+}
+
+// The bucket of every entry of the expanded table (255: none), once per CTA,
+// and a head's entries from it.  SIGN = 1: rows are queries, -1: rows are
+// keys.  NR row threads; no barriers inside.
+constexpr uint8_t kNoBucket = 255;
+template <int SIGN, int NR>
+__device__ __forceinline__ void bias_ids(const Bias& t, const Problem& p, uint8_t* ids) {
+#pragma unroll 4
+    for (int x = threadIdx.x; x <= t.last; x += NR) ids[x] = static_cast<uint8_t>(bucket_of(p, SIGN * (x - t.D - t.R)));
+    for (int x = t.last + 1 + threadIdx.x; x <= t.last + kVecPad; x += NR) ids[x] = kNoBucket;   // past a partial tile's end
+}
+template <int NR>
+__device__ __forceinline__ void bias_fill(const Bias& t, const uint8_t* ids) {
+#pragma unroll 4
+    for (int x = threadIdx.x; x <= t.last + kVecPad; x += NR) {
+        const int b = ids[x];
+        t.vec[x] = b == kNoBucket ? 0.f : t.tab[b];
+    }
 }
 
 // Expands head h's column of the table; SIGN = 1: rows are queries, -1: rows
@@ -112,14 +143,14 @@ __device__ __forceinline__ void bias_expand(const Bias& t, const Problem& p, int
     row_barrier();
 }
 
-// Offsets and tile kinds of columns [c0, c0 + kChunk) (positions from pos_of).
-// All 128 row threads; the caller puts a barrier before and after.
-template <class PosOf>
+// Offsets and tile kinds of columns [c0, c0 + CHUNK) (positions from pos_of).
+// All NR row threads; the caller puts a barrier before and after.
+template <int NR = 128, int CHUNK = kChunk, class PosOf>
 __device__ __forceinline__ void bias_columns(const Bias& t, int c0, int len, PosOf pos_of) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-    for (int k = 0; k < kChunkTiles / kRowWarps; ++k) {
-        const int tile = warp + k * kRowWarps, c = c0 + tile * kTile + lane;
+    for (int k = 0; k < (CHUNK / kTile) / (NR / 32); ++k) {
+        const int tile = warp + k * (NR / 32), c = c0 + tile * kTile + lane;
         if (c0 + tile * kTile >= len) break;
         const bool v0 = c < len, v1 = c + 32 < len;
         const int p0 = v0 ? pos_of(c) : 0, p1 = v1 ? pos_of(c + 32) : 0;
@@ -192,15 +223,35 @@ __device__ __forceinline__ void load_rows(uint32_t s_tile, const uint16_t* base,
     }
 }
 
-// Bounded waits of one CTA; once one has given up, no other waits.
+// A waiting thread sleeps for up to kWaitNs before it looks again: without the
+// hint the polls of the MMA and load warps took more issue slots than the
+// element-wise work (60 % of all instructions).
+constexpr uint32_t kWaitNs = 4000;
+constexpr uint32_t kWaitLimit = 1u << 18;   // about a second
+
+__device__ __forceinline__ bool mbar_try(uint32_t mbar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(mbar), "r"(parity), "r"(kWaitNs)
+        : "memory");
+    return done != 0;
+}
+// Bounded waits of one CTA; once one has given up, the others soon do.
 struct Wait {
     int* s_fail;
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {   // one thread
-        if (*reinterpret_cast<volatile int*>(s_fail) || !mbar_wait(bar, parity)) {
-            atomicExch(s_fail, 1);
-            return false;
+        if (mbar_try(bar, parity)) return true;
+        const uint32_t limit = min(spin_limit(), kWaitLimit);
+        for (uint32_t i = 0; i < limit; ++i) {
+            if (mbar_try(bar, parity)) return true;
+            if (*reinterpret_cast<volatile int*>(s_fail)) return false;
         }
-        return true;
+        atomicExch(s_fail, 1);
+        return false;
     }
     __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {   // all lanes, one answer
         return __all_sync(0xffffffffu, (*this)(bar, parity));
@@ -228,6 +279,21 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols, int warp
     }
 }
 
+// 32 values of a row (packed pairs) to 16-bit global memory.
+__device__ __forceinline__ void store_half_row(uint16_t* dst, const uint32_t (&w)[16]) {
+    if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c * 16), "r"(w[8 * c]),
+                         "r"(w[8 * c + 1]), "r"(w[8 * c + 2]), "r"(w[8 * c + 3]), "r"(w[8 * c + 4]), "r"(w[8 * c + 5]),
+                         "r"(w[8 * c + 6]), "r"(w[8 * c + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(dst + c * 8) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    }
+}
 // 64 values of a row (packed pairs) to 16-bit global memory.
 __device__ __forceinline__ void store_row(uint16_t* dst, const uint32_t (&w)[32]) {
     if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
@@ -258,42 +324,219 @@ __device__ __forceinline__ void store_tmem_row(uint32_t taddr, float f, uint16_t
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  grid (query tiles, H, B), two CTAs per SM.
+// The bias of a group of 128 row threads in 16 bits: the entries are the
+// table's own values, so nothing is lost, and 32 rows that spread over 64
+// positions read 32 words, one per bank, where fp32 entries would take two or
+// three passes.  Scores are formed in base e, x = s * scale + bias, and the
+// factor log2 e goes into the exponent's multiply-add.
+// ---------------------------------------------------------------------------
+
+// A table entry as the kernels keep it: finite values stay within +-2^126, so
+// that a row whose keys all carry the type's lowest value keeps its softmax
+// over them when log2 e multiplies it.
+template <typename T>
+__device__ __forceinline__ uint16_t bias_bits(uint16_t x) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const uint16_t mag = x & 0x7fffu;
+        if (mag > 0x7e80u && mag < 0x7f80u) return static_cast<uint16_t>((x & 0x8000u) | 0x7e80u);
+    }
+    return x;
+}
+
+struct Bias16 {
+    uint16_t* vec;   // [2 (D + span) + 1 + pad], one head's entries
+    int* off;        // [kChunk] byte offsets into vec (kClamped: positions)
+    int* kind;       // [kChunkTiles]
+    int rmin, R, D, last;
+    bool near;
+    uint32_t row;    // byte offset of this thread's row
+    int p_row;
+};
+
+// Barrier of one group's 128 row threads (w: the group).
+__device__ __forceinline__ void group_barrier(int w) { asm volatile("bar.sync %0, 128;" ::"r"(w + 1) : "memory"); }
+
+// Extremes of the group's row positions (s_red: 8 ints; a barrier inside).
+__device__ __forceinline__ void bias_rows(Bias16& t, const Problem& p, int w, int pos, bool valid, int span, int* s_red) {
+    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const int lo = __reduce_min_sync(0xffffffffu, valid ? pos : INT_MAX);
+    const int hi = __reduce_max_sync(0xffffffffu, valid ? pos : INT_MIN);
+    if (lane == 0) {
+        s_red[warp] = lo;
+        s_red[4 + warp] = hi;
+    }
+    group_barrier(w);
+    t.rmin = min(min(s_red[0], s_red[1]), min(s_red[2], s_red[3]));
+    const int rmax = max(max(s_red[4], s_red[5]), max(s_red[6], s_red[7]));
+    const int64_t R = static_cast<int64_t>(rmax) - t.rmin;
+    t.D = p.D;
+    t.near = R <= span;
+    t.R = t.near ? static_cast<int>(R) : 0;
+    t.last = 2 * (t.D + t.R);
+    t.p_row = pos;
+    t.row = valid && t.near ? 2u * static_cast<uint32_t>(t.R - (pos - t.rmin)) : 0u;
+}
+// The bucket of every entry (255: none), by n of the CTA's threads.
+template <int SIGN>
+__device__ __forceinline__ void bias_ids(const Bias16& t, const Problem& p, uint8_t* ids, int tid, int n) {
+#pragma unroll 4
+    for (int x = tid; x <= t.last; x += n) ids[x] = static_cast<uint8_t>(bucket_of(p, SIGN * (x - t.D - t.R)));
+    for (int x = t.last + 1 + tid; x <= t.last + kVecPad; x += n) ids[x] = kNoBucket;
+}
+// One head's entries from its column of the table (tab), by the group.
+__device__ __forceinline__ void bias_fill(const Bias16& t, const uint8_t* ids, const uint16_t* tab) {
+#pragma unroll 4
+    for (int x = threadIdx.x & 127; x <= t.last + kVecPad; x += 128) {
+        const int b = ids[x];
+        t.vec[x] = b == kNoBucket ? uint16_t(0) : tab[b];
+    }
+}
+// Offsets and kinds of columns [c0, c0 + kChunk), by the group; barriers around it are the caller's.
+template <class PosOf>
+__device__ __forceinline__ void bias_columns(const Bias16& t, int c0, int len, PosOf pos_of) {
+    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const int lo = -t.D, hi = t.R + t.D;
+    auto clamped = [&](int x) {
+        const int64_t d = static_cast<int64_t>(x) - t.rmin;
+        return d < lo ? lo : d > hi ? hi : static_cast<int>(d);
+    };
+    int pos[kChunkTiles / 4][2];   // all loads first
+#pragma unroll
+    for (int k = 0; k < kChunkTiles / 4; ++k) {
+        const int c = c0 + (warp + k * 4) * kTile + lane;
+        pos[k][0] = c < len ? pos_of(c) : 0;
+        pos[k][1] = c + 32 < len ? pos_of(c + 32) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kChunkTiles / 4; ++k) {
+        const int tile = warp + k * 4, c = c0 + tile * kTile + lane;
+        if (c0 + tile * kTile >= len) break;
+        const bool v0 = c < len, v1 = c + 32 < len;
+        const int o0 = clamped(pos[k][0]), o1 = clamped(pos[k][1]);
+        const int first = __shfl_sync(0xffffffffu, o0, 0);
+        const bool left = __all_sync(0xffffffffu, (!v0 || o0 == lo) && (!v1 || o1 == lo));
+        const bool right = __all_sync(0xffffffffu, (!v0 || o0 == hi) && (!v1 || o1 == hi));
+        const bool run = __all_sync(0xffffffffu, (!v0 || o0 == first + lane) && (!v1 || o1 == first + 32 + lane));
+        int* off = t.off + tile * kTile;
+        if (t.near) {
+            off[lane] = v0 ? 2 * (o0 - lo) : 0;
+            off[lane + 32] = v1 ? 2 * (o1 - lo) : 0;
+        } else {
+            off[lane] = pos[k][0];
+            off[lane + 32] = pos[k][1];
+        }
+        if (lane == 0) t.kind[tile] = !t.near ? kClamped : left ? kLeft : right ? kRight : run ? kConsecutive : kGeneral;
+    }
+}
+// x = x * scale + bias for 32 columns from column c of a tile (not for kLeft, kRight).
+template <typename T>
+__device__ __forceinline__ void bias_add(const Bias16& t, int kind, const int* off, int c, float scale, float (&x)[32]) {
+    const uint64_t sc2 = f2(scale, scale);
+    const char* row = reinterpret_cast<const char*>(t.vec) + t.row;
+    auto at = [&](int o) { return to_float<T>(*reinterpret_cast<const uint16_t*>(row + o)); };
+    if (kind == kConsecutive) {
+        const char* e = row + off[0] + 2 * c;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float e0 = to_float<T>(*reinterpret_cast<const uint16_t*>(e + 4 * i)), e1 = to_float<T>(*reinterpret_cast<const uint16_t*>(e + 4 * i + 2));
+            f2_split(f2_fma(f2(x[2 * i], x[2 * i + 1]), sc2, f2(e0, e1)), x[2 * i], x[2 * i + 1]);
+        }
+    } else if (kind == kGeneral) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int4 o = *reinterpret_cast<const int4*>(off + c + 4 * i);
+            f2_split(f2_fma(f2(x[4 * i], x[4 * i + 1]), sc2, f2(at(o.x), at(o.y))), x[4 * i], x[4 * i + 1]);
+            f2_split(f2_fma(f2(x[4 * i + 2], x[4 * i + 3]), sc2, f2(at(o.z), at(o.w))), x[4 * i + 2], x[4 * i + 3]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const int d = max(-t.D, min(t.D, pos_diff(off[c + i], t.p_row)));
+            x[i] = fmaf(x[i], scale, to_float<T>(t.vec[d + t.D]));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Forward.  grid (query tiles, groups of heads, B), two CTAs per SM.
 //
-// TMEM (256 columns): S of three tiles, each replaced in place by its P
-// (packed 16-bit pairs, the A operand of P V), and O.  Q K^T runs three tiles
-// ahead of P V: the tensor core executes one thread's MMAs in order, so
-// Q K^T(g + 3), issued behind P V(g), finds P(g) read.  Softmax in one pass
-// with a reference maximum that is raised, and the running sum and O
-// rescaled, only when a tile exceeds it by 2^8.  P is rounded to the 16-bit
-// type of V: the product's operands must have one type, and the rounding
-// (half a step, independent per element) adds about as much to the result as
-// its own final rounding does; the sum that divides is of the unrounded P.
+// A CTA holds the positions of its 128 queries and walks over its heads; the
+// tile counter runs on from head to head, so the loads and the first scores of
+// a head are under way while the one before it finishes.  TMEM (256 columns): S of
+// three tiles, each replaced in place by its P (packed 16-bit pairs, the A
+// operand of P V), and O.  Q K^T runs three tiles ahead of P V: the tensor
+// core executes one thread's MMAs in order, so Q K^T(g + 3), issued behind
+// P V(g), finds P(g) read.  A head's result is read out of O when the first P
+// of the next head is ready, before it is handed over (its product overwrites
+// O).
+//
+// Softmax in one pass with a reference maximum that is raised, and the running
+// sum and O rescaled, only when a tile exceeds it by 2^8.  P is rounded to the
+// 16-bit type of V: the product's operands must have one type, and the
+// rounding (half a step, independent per element) adds about as much to the
+// result as its own final rounding does; the sum that divides is of the
+// unrounded P.
 // ---------------------------------------------------------------------------
 
 constexpr int kFwdK = 3, kFwdV = 5;
 
-__host__ __device__ constexpr int fwd_smem_bytes(int D) {
-    return 1024 + kRowBytes + (kFwdK + kFwdV) * kTileBytes + 4 * (vec_entries(D, kSpan) + 3) + 4 * kChunk;
+__host__ __device__ constexpr int fwd_fixed_bytes() { return 1024 + 2 * kRowBytes + (kFwdK + kFwdV) * kTileBytes + 4 * kChunk; }
+__host__ __device__ constexpr int vec16_bytes(int D, int span) { return 2 * ((vec_entries(D, span) + 7) & ~7); }
+__host__ __device__ constexpr int ids_bytes(int D, int span) { return (vec_entries(D, span) + 15) & ~15; }
+__host__ __device__ constexpr int fwd_smem_bytes(int D, int span) {
+    return fwd_fixed_bytes() + 2 * vec16_bytes(D, span) + ids_bytes(D, span);
+}
+
+// The start of a CTA: the load warp sets up the barriers and begins at once,
+// the MMA warp takes the TMEM and waits for the barriers, the row threads join
+// when they have prepared the bias.
+__device__ __forceinline__ void start_loads() { asm volatile("bar.arrive 2, 64;" ::: "memory"); }
+__device__ __forceinline__ uint32_t start_mma(uint32_t* s_tmem, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(s_tmem)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    fence_before_sync();
+    asm volatile("bar.sync 2, 64;" ::: "memory");
+    asm volatile("bar.arrive 3, 160;" ::: "memory");
+    fence_after_sync();
+    return *s_tmem;
+}
+__device__ __forceinline__ uint32_t start_rows(const uint32_t* s_tmem) {
+    asm volatile("bar.sync 3, 160;" ::: "memory");
+    fence_after_sync();
+    return *s_tmem;
+}
+// The end: all roles meet, and the MMA warp frees the TMEM.
+__device__ __forceinline__ void finish_cta(const uint32_t* s_tmem, uint32_t cols, int warp, const int* s_fail) {
+    fence_before_sync();
+    __syncthreads();
+    if (*s_fail && threadIdx.x == 0) raise_status(RAGGED_DEV_TIMEOUT);
+    if (warp == kTcMmaWarp) {
+        fence_after_sync();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*s_tmem), "r"(cols) : "memory");
+    }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) bias_fwd_kernel(const Problem p, uint16_t* __restrict__ out, int64_t out_tok) {
+__global__ void __launch_bounds__(kThreads, 2)
+    bias_fwd_kernel(const Problem p, uint16_t* __restrict__ out, int64_t out_tok, int heads_per_cta, int span) {
     extern __shared__ uint8_t smem_raw[];
-    // q_full, k_full[3], v_full[5], s_full[3], p_full[4], pv_done[5], drain
-    __shared__ __align__(8) uint64_t s_bar[22];
-    __shared__ float s_tab[kMaxBuckets];
+    // q_full[2], q_empty[2], k_full[3], v_full[5], s_full[3], p_full[4], pv_done[5], done
+    constexpr int kBars = 25;
+    __shared__ __align__(8) uint64_t s_bar[kBars];
+    __shared__ uint16_t s_tab[2][kMaxBuckets];
     __shared__ int s_kind[kChunkTiles], s_red[8];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
 
-    const int q0 = blockIdx.x * kQTile, h = blockIdx.y, b = blockIdx.z;
+    const int q0 = blockIdx.x * kQTile, h0 = blockIdx.y * heads_per_cta, b = blockIdx.z;
+    const int nh = min(heads_per_cta, p.H - h0);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Seq s;
     if (!read_pair(p, b, s) || q0 >= s.q_len) return;
-    if (s.k_len == 0) {   // a query without keys
-        const int r = q0 + tid;
-        if (tid < kQTile && r < s.q_len) {
+    if (s.k_len == 0) {   // queries without keys
+        for (int i = tid; i < nh * kQTile; i += kThreads) {
+            const int h = h0 + i / kQTile, r = q0 + i % kQTile;
+            if (r >= s.q_len) continue;
             const uint32_t zero[32] = {};
             store_row(out + static_cast<int64_t>(s.q_start + r) * out_tok + h * 64, zero);
             p.lse[h * p.lse_stride + s.q_start + r] = -INFINITY;
@@ -301,215 +544,261 @@ __global__ void __launch_bounds__(kThreads, 2) bias_fwd_kernel(const Problem p, 
         return;
     }
     const int nt = (s.k_len + kTile - 1) / kTile;
+    const uint32_t total = static_cast<uint32_t>(nt) * nh;   // tiles of all heads
 
     const uint32_t raw = smem_addr(smem_raw);
-    const uint32_t sQ = (raw + 1023u) & ~1023u;
-    const uint32_t sK = sQ + kRowBytes, sV = sK + kFwdK * kTileBytes;
+    const uint32_t sQ = (raw + 1023u) & ~1023u;   // two buffers, by head
+    const uint32_t sK = sQ + 2 * kRowBytes, sV = sK + kFwdK * kTileBytes;
     uint8_t* extra = smem_raw + (sV - raw) + kFwdV * kTileBytes;
-
     const uint32_t bar0 = smem_addr(&s_bar[0]);
-    const uint32_t q_full = bar0, drain = bar0 + 8u * 21;
-    auto k_full = [&](uint32_t g) { return bar0 + 8u * (1 + g % kFwdK); };
-    auto v_full = [&](uint32_t g) { return bar0 + 8u * (4 + g % kFwdV); };
-    auto s_full = [&](uint32_t g) { return bar0 + 8u * (9 + g % 3); };
+    auto q_full = [&](uint32_t i) { return bar0 + 8u * (i & 1); };
+    auto q_empty = [&](uint32_t i) { return bar0 + 8u * (2 + (i & 1)); };
+    auto k_full = [&](uint32_t g) { return bar0 + 8u * (4 + g % kFwdK); };
+    auto v_full = [&](uint32_t g) { return bar0 + 8u * (7 + g % kFwdV); };
+    auto s_full = [&](uint32_t g) { return bar0 + 8u * (12 + g % 3); };
     // Warps without rows run up to three tiles ahead of others, so four
     // consecutive tiles have barriers of their own.
-    auto p_full = [&](uint32_t g) { return bar0 + 8u * (12 + (g & 3)); };
-    auto pv_done = [&](uint32_t g) { return bar0 + 8u * (16 + g % kFwdV); };
-    if (tid == 0) {
-        mbar_init(q_full, 32);
-        for (int i = 0; i < kFwdK; ++i) mbar_init(k_full(i), 32);
-        for (int i = 0; i < kFwdV; ++i) mbar_init(v_full(i), 32);
-        for (int i = 0; i < 3; ++i) mbar_init(s_full(i), 1);
-        for (int i = 0; i < 4; ++i) mbar_init(p_full(i), 128);
-        for (int i = 0; i < kFwdV; ++i) mbar_init(pv_done(i), 1);
-        mbar_init(drain, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        s_fail = 0;
-    }
-    const uint32_t tmem = tmem_alloc(&s_tmem, kTmemCols, warp);
-    const uint32_t o_col = 3 * kTile;
+    auto p_full = [&](uint32_t g) { return bar0 + 8u * (15 + (g & 3)); };
+    auto pv_done = [&](uint32_t g) { return bar0 + 8u * (19 + g % kFwdV); };
+    const uint32_t done = bar0 + 8u * 24;
+    constexpr uint32_t o_col = 3 * kTile;
     const Wait wait{&s_fail};
 
     if (warp == kTcLoadWarp) {
-        const int64_t z = static_cast<int64_t>(h / p.group) * p.kv_head;
-        const uint16_t* qb = p.q + s.q_start * p.q_tok + h * p.q_head;
-        const uint16_t* kb = p.k + s.k_start * p.kv_tok + z;
-        const uint16_t* vb = p.v + s.k_start * p.kv_tok + z;
-        load_rows<kQTile>(sQ, qb, p.q_tok, q0, s.q_len, lane);
-        cp_async_arrive_noinc(q_full);
+        // ---------------- loads ----------------
+        if (lane < kBars) mbar_init(bar0 + 8 * lane, lane < 2 || (lane >= 4 && lane < 12) ? 32 : lane >= 15 && lane < 19 ? 128 : 1);
+        if (lane == 0) s_fail = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        __syncwarp();
+        start_loads();
         bool ok = !test_hook(1);
-        for (uint32_t g = 0; ok && g < static_cast<uint32_t>(nt); ++g) {
-            // K stage g % 3 is free once Q K^T of tile g - 3 has finished, V
-            // stage g % 5 once P V of tile g - 5 has.
-            if (g >= kFwdK) ok = wait.warp(s_full(g), ((g - kFwdK) / 3) & 1);
+        uint32_t g = 0;
+        for (int i = 0; ok && i < nh; ++i) {
+            const int h = h0 + i;
+            const int64_t z = static_cast<int64_t>(h / p.group) * p.kv_head;
+            const uint16_t* kb = p.k + s.k_start * p.kv_tok + z;
+            const uint16_t* vb = p.v + s.k_start * p.kv_tok + z;
+            if (i >= 2) ok = wait.warp(q_empty(i), ((i >> 1) - 1) & 1);
             if (!ok) break;
-            load_rows<kTile>(sK + (g % kFwdK) * kTileBytes, kb, p.kv_tok, g * kTile, s.k_len, lane);
-            cp_async_arrive_noinc(k_full(g));
-            if (g >= kFwdV) ok = wait.warp(pv_done(g), ((g - kFwdV) / kFwdV) & 1);
-            if (!ok) break;
-            load_rows<kTile>(sV + (g % kFwdV) * kTileBytes, vb, p.kv_tok, g * kTile, s.k_len, lane);
-            cp_async_arrive_noinc(v_full(g));
+            load_rows<kQTile>(sQ + (i & 1) * kRowBytes, p.q + s.q_start * p.q_tok + h * p.q_head, p.q_tok, q0, s.q_len, lane);
+            cp_async_arrive_noinc(q_full(i));
+            for (int t = 0; t < nt; ++t, ++g) {
+                // K stage g % 3 is free once Q K^T of tile g - 3 has finished, V
+                // stage g % 5 once P V of tile g - 5 has.
+                if (g >= kFwdK) ok = wait.warp(s_full(g), (g / 3 - 1) & 1);
+                if (!ok) break;
+                load_rows<kTile>(sK + (g % kFwdK) * kTileBytes, kb, p.kv_tok, t * kTile, s.k_len, lane);
+                cp_async_arrive_noinc(k_full(g));
+                if (g >= kFwdV) ok = wait.warp(pv_done(g), (g / kFwdV - 1) & 1);
+                if (!ok) break;
+                load_rows<kTile>(sV + (g % kFwdV) * kTileBytes, vb, p.kv_tok, t * kTile, s.k_len, lane);
+                cp_async_arrive_noinc(v_full(g));
+            }
         }
         cp_async_wait_all();
     } else if (warp == kTcMmaWarp) {
+        // ---------------- MMA issue (one thread) ----------------
+        const uint32_t tmem = start_mma(&s_tmem, kTmemCols);
         if (lane == 0) {
-            const uint32_t idesc_qk = make_idesc(Cvt<T>::kFormat, 0, kTile);
-            const uint32_t idesc_pv = make_idesc(Cvt<T>::kFormat, 1, 64);
+            const uint32_t idesc_qk = make_idesc(Cvt<T>::kFormat, 0, kTile), idesc_pv = make_idesc(Cvt<T>::kFormat, 1, 64);
+            int qi = 0, qt = 0;   // head and tile of the next scores
             auto issue_qk = [&](uint32_t g) {
+                if (qt == 0 && !wait(q_full(qi), (qi >> 1) & 1)) return false;
                 if (!wait(k_full(g), (g / kFwdK) & 1)) return false;
                 fence_async_smem();   // cp.async wrote through the generic proxy
                 fence_after_sync();
+                const uint32_t sq = sQ + (qi & 1) * kRowBytes;
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_f16(tmem + (g % 3) * kTile, make_sdesc(sQ + ks * 32),
-                            make_sdesc(sK + (g % kFwdK) * kTileBytes + ks * 32), idesc_qk, ks > 0);
+                    mma_f16(tmem + (g % 3) * kTile, make_sdesc(sq + ks * 32), make_sdesc(sK + (g % kFwdK) * kTileBytes + ks * 32),
+                            idesc_qk, ks > 0);
                 mma_commit(s_full(g));
+                if (++qt == nt) {
+                    mma_commit(q_empty(qi));
+                    qt = 0;
+                    ++qi;
+                }
                 return true;
             };
-            bool ok = wait(q_full, 0);
-            const uint32_t n = nt;
-            for (uint32_t g = 0; ok && g < 3 && g < n; ++g) ok = issue_qk(g);
-            for (uint32_t g = 0; ok && g < n; ++g) {
-                ok = wait(p_full(g), (g >> 2) & 1) && wait(v_full(g), (g / kFwdV) & 1);
+            bool ok = true;
+            for (uint32_t g = 0; ok && g < 3 && g < total; ++g) ok = issue_qk(g);
+            int t = 0;
+            for (uint32_t g = 0; ok && g < total; ++g) {
+                ok = wait(v_full(g), (g / kFwdV) & 1) && wait(p_full(g), (g >> 2) & 1);
                 if (!ok) break;
                 fence_async_smem();
                 fence_after_sync();
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
                     mma_f16_ts(tmem + o_col, tmem + (g % 3) * kTile + ks * 8,
-                               make_sdesc(sV + (g % kFwdV) * kTileBytes + ks * 2048), idesc_pv, (g > 0 || ks > 0) ? 1u : 0u);
+                               make_sdesc(sV + (g % kFwdV) * kTileBytes + ks * 2048), idesc_pv, (t > 0 || ks > 0) ? 1u : 0u);
                 mma_commit(pv_done(g));
-                if (g + 3 < n) ok = issue_qk(g + 3);
+                if (g + 3 < total) ok = issue_qk(g + 3);
+                if (++t == nt) t = 0;
             }
-            mma_commit(drain);   // every MMA has finished before TMEM is freed
-            mbar_wait(drain, 0);
+            mma_commit(done);   // every MMA has finished before TMEM is freed
+            mbar_wait(done, 0);
         }
+        __syncwarp();
     } else {
+        // ---------------- softmax and results (one thread per query) ----------------
         const int row = q0 + tid;
         const bool valid = row < s.q_len, warp_rows = q0 + warp * 32 < s.q_len;
-        Bias t;
-        t.vec = reinterpret_cast<float*>(extra);
-        t.off = reinterpret_cast<int*>(extra + 4 * ((vec_entries(p.D, kSpan) + 3) & ~3));
+        const int64_t t_row = s.q_start + row;
+        Bias16 t;
+        uint16_t* const vec0 = reinterpret_cast<uint16_t*>(extra);
+        const int vec_step = vec16_bytes(p.D, span) / 2;
+        uint8_t* ids = extra + 2 * vec16_bytes(p.D, span);
+        t.vec = vec0;
+        t.off = reinterpret_cast<int*>(ids + ids_bytes(p.D, span));
         t.kind = s_kind;
-        t.tab = s_tab;
-        bias_rows(t, p, valid ? query_pos(p, s, row) : 0, valid, kSpan, s_red);
-        bias_expand<T, 1, false>(t, p, h, nullptr);
+        const bool has_entry = tid < p.num_buckets;   // of the table's column of a head
+        const uint16_t* column = p.table + static_cast<int64_t>(has_entry ? tid : 0) * p.H + h0;
+        const uint16_t entry = __ldg(column);
+        bias_rows(t, p, 0, valid ? query_pos(p, s, row) : 0, valid, span, s_red);
+        bias_ids<1>(t, p, ids, tid, 128);
+        bias_columns(t, 0, s.k_len, [&](int c) { return key_pos(p, s, c); });
+        if (has_entry) s_tab[0][tid] = bias_bits<T>(entry);
+        group_barrier(0);
+        bias_fill(t, ids, s_tab[0]);
+        const uint32_t tmem = start_rows(&s_tmem);
 
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        const uint32_t o_lane = t_lane + o_col;
         bool ok = true;
-        int pv_seen = -1;   // pv_done phases are waited for one by one, in order
-        auto confirm_pv = [&](int x) {
-            while (pv_seen < x) {
-                ++pv_seen;
-                ok = ok && wait.warp(pv_done(pv_seen), (pv_seen / kFwdV) & 1);
-            }
-        };
-        float m_ref = -INFINITY, l0 = 0.f, l1 = 0.f;
-        for (int g = 0; g < nt; ++g) {
-            if (g % kChunkTiles == 0) {
-                if (g) row_barrier();
-                bias_columns(t, g * kTile, s.k_len, [&](int c) { return key_pos(p, s, c); });
-                row_barrier();
-            }
-            ok = ok && wait.warp(s_full(g), (g / 3) & 1);
-            if (ok && warp_rows) {
-                fence_after_sync();
-                const uint32_t s_buf = t_lane + static_cast<uint32_t>((g % 3) * kTile);
-                const int kind = t.kind[g % kChunkTiles];
-                const int* off = t.off + (g % kChunkTiles) * kTile;
-                float x[2][32];
-                tmem_ld32(s_buf, x[0]);
-                tmem_ld32(s_buf + 32, x[1]);
-                bias_add(t, kind, off, 0, p.scale_log2, x[0]);
-                bias_add(t, kind, off, 32, p.scale_log2, x[1]);
-                const int cols = s.k_len - g * kTile;
-                if (cols < kTile) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (i >= cols) x[i >> 5][i & 31] = -INFINITY;
-                }
-                float mt = -INFINITY;
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    float m0 = fmax3(x[hf][0], x[hf][1], x[hf][2]), m1 = fmax3(x[hf][16], x[hf][17], x[hf][18]);
-#pragma unroll
-                    for (int i = 3; i < 15; i += 2) {
-                        m0 = fmax3(m0, x[hf][i], x[hf][i + 1]);
-                        m1 = fmax3(m1, x[hf][16 + i], x[hf][17 + i]);
-                    }
-                    mt = fmax3(mt, fmaxf(m0, x[hf][15]), fmaxf(m1, x[hf][31]));
-                }
-                const bool grow = mt > m_ref + kRescaleThreshold;
-                float alpha = 1.f;
-                if (grow) {
-                    alpha = mma_attn::fast_exp2(m_ref - mt);
-                    l0 *= alpha;
-                    l1 *= alpha;
-                    m_ref = mt;
-                }
-                if (g > 0 && __any_sync(0xffffffffu, grow)) {
-                    confirm_pv(g - 1);   // O holds the finished products so far
-                    if (ok) {
-                        fence_after_sync();
-                        const uint64_t a2 = f2(alpha, alpha);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            float part[16];
-                            tmem_ld16(t_lane + o_col + q * 16, part);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                f2_split(f2_mul(f2(part[2 * i], part[2 * i + 1]), a2), part[2 * i], part[2 * i + 1]);
-                            tmem_st16(t_lane + o_col + q * 16, part);
-                        }
-                    }
-                }
-                // A row without a finite score so far has no reference: -inf - 0 gives p = 0.
-                const float ref = m_ref == -INFINITY ? 0.f : -m_ref;
-                const uint64_t nm = f2(ref, ref);
-                uint64_t sum = f2(l0, l1);
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float a, c;
-                        f2_split(f2_add(f2(x[hf][2 * i], x[hf][2 * i + 1]), nm), a, c);
-                        a = mma_attn::fast_exp2(a);
-                        c = mma_attn::fast_exp2(c);
-                        sum = f2_add(sum, f2(a, c));
-                        w[i] = Cvt<T>::pack(a, c);
-                    }
-                    tmem_st16_u(s_buf + hf * 16, w);
-                }
-                f2_split(sum, l0, l1);
-                tmem_wait_st();
-            }
-            if (g >= 2) confirm_pv(g - 2);
-            fence_before_sync();
-            mbar_arrive(p_full(g));
-        }
-        confirm_pv(nt - 1);
-        if (ok && warp_rows) {
+        uint32_t g = 0;
+        // Products up to tile x have finished.  Called when the scores of tile
+        // x + 1 or later have been seen, which were issued behind P V(x - 2): the
+        // barrier's earlier phases are over, so the parity is exact.
+        auto confirm_pv = [&](uint32_t x) { ok = ok && wait.warp(pv_done(x), (x / kFwdV) & 1); };
+        float l_done = 0.f, m_done = 0.f;   // of the head before
+        // Result of head h, whose last product was tile x's.
+        auto finish = [&](int h, uint32_t x, float m, float l) {
+            confirm_pv(x);
+            if (!ok || !warp_rows) return;
             fence_after_sync();
-            const float l = l0 + l1;
             const bool empty = l == 0.f;   // every score is -inf
-            uint32_t w[32];
+            const float inv = 1.f / l;
+            uint16_t* dst = out + t_row * out_tok + h * 64;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 float v[32];
-                tmem_ld32(t_lane + o_col + hf * 32, v);
-                const float inv = 1.f / l;
+                tmem_ld32(o_lane + hf * 32, v);
+                uint32_t pk[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) w[hf * 16 + i] = empty ? 0u : Cvt<T>::pack(v[2 * i] * inv, v[2 * i + 1] * inv);
+                for (int j = 0; j < 16; ++j) pk[j] = empty ? 0u : Cvt<T>::pack(v[2 * j] * inv, v[2 * j + 1] * inv);
+                if (valid) store_half_row(dst + hf * 32, pk);
             }
-            if (valid) {
-                store_row(out + static_cast<int64_t>(s.q_start + row) * out_tok + h * 64, w);
-                p.lse[h * p.lse_stride + s.q_start + row] = empty ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+            if (valid) p.lse[h * p.lse_stride + t_row] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
+        };
+        for (int i = 0; i < nh; ++i) {
+            // This head's entries are complete and the last head's no longer read after
+            // this barrier; the next head's are filled in behind it.
+            if (i + 1 < nh && has_entry) s_tab[(i + 1) & 1][tid] = bias_bits<T>(__ldg(column + i + 1));
+            group_barrier(0);
+            if (i + 1 < nh) {
+                t.vec = vec0 + ((i + 1) & 1) * vec_step;
+                bias_fill(t, ids, s_tab[(i + 1) & 1]);
             }
+            t.vec = vec0 + (i & 1) * vec_step;
+            float m_ref = -INFINITY, l0 = 0.f, l1 = 0.f;
+            for (int tile = 0; tile < nt; ++tile, ++g) {
+                if (tile % kChunkTiles == 0 && (tile > 0 || (i > 0 && nt > kChunkTiles))) {
+                    if (tile > 0) group_barrier(0);
+                    bias_columns(t, tile * kTile, s.k_len, [&](int c) { return key_pos(p, s, c); });
+                    group_barrier(0);
+                }
+                const int kind = t.kind[tile % kChunkTiles];
+                const int* off = t.off + (tile % kChunkTiles) * kTile;
+                ok = ok && wait.warp(s_full(g), (g / 3) & 1);
+                if (ok && warp_rows) {
+                    fence_after_sync();
+                    const uint32_t s_buf = t_lane + static_cast<uint32_t>((g % 3) * kTile);
+                    float x[2][32];
+                    tmem_ld32(s_buf, x[0]);
+                    tmem_ld32(s_buf + 32, x[1]);
+                    // Scores in base 2 are x * scale + add; one bias for the whole tile goes into `add`.
+                    float scale = kLog2e, add = 0.f;
+                    if (kind == kLeft || kind == kRight) {
+                        scale = p.scale_log2;
+                        add = to_float<T>(t.vec[kind == kLeft ? 0 : t.last]) * kLog2e;
+                    } else {
+                        bias_add<T>(t, kind, off, 0, p.scale, x[0]);
+                        bias_add<T>(t, kind, off, 32, p.scale, x[1]);
+                    }
+                    const int cols = s.k_len - tile * kTile;
+                    if (cols < kTile) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            if (c >= cols) x[c >> 5][c & 31] = -INFINITY;
+                    }
+                    float mt = -INFINITY;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        float a = fmax3(x[hf][0], x[hf][1], x[hf][2]), c = fmax3(x[hf][16], x[hf][17], x[hf][18]);
+#pragma unroll
+                        for (int j = 3; j < 15; j += 2) {
+                            a = fmax3(a, x[hf][j], x[hf][j + 1]);
+                            c = fmax3(c, x[hf][16 + j], x[hf][17 + j]);
+                        }
+                        mt = fmax3(mt, fmaxf(a, x[hf][15]), fmaxf(c, x[hf][31]));
+                    }
+                    mt = fmaf(mt, scale, add);
+                    const bool grow = mt > m_ref + kRescaleThreshold;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        float alpha = 1.f;
+                        if (grow) {
+                            alpha = mma_attn::fast_exp2(m_ref - mt);
+                            l0 *= alpha;
+                            l1 *= alpha;
+                            m_ref = mt;
+                        }
+                        if (tile > 0) {   // O holds the head's products so far
+                            confirm_pv(g - 1);
+                            fence_after_sync();
+                            if (ok) {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    float part[16];
+                                    tmem_ld16(o_lane + q * 16, part);
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) part[j] *= alpha;
+                                    tmem_st16(o_lane + q * 16, part);
+                                }
+                            }
+                        }
+                    }
+                    // A row without a finite score so far has no reference: p = 2^-inf = 0.
+                    const float ref = m_ref == -INFINITY ? add : add - m_ref;
+                    const uint64_t sc2 = f2(scale, scale), ref2 = f2(ref, ref);
+                    uint64_t sum = f2(l0, l1);
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float a, c;
+                            f2_split(f2_fma(f2(x[hf][2 * j], x[hf][2 * j + 1]), sc2, ref2), a, c);
+                            a = mma_attn::fast_exp2(a);
+                            c = mma_attn::fast_exp2(c);
+                            sum = f2_add(sum, f2(a, c));
+                            pk[j] = Cvt<T>::pack(a, c);
+                        }
+                        tmem_st16_u(s_buf + hf * 16, pk);
+                    }
+                    f2_split(sum, l0, l1);
+                    tmem_wait_st();
+                }
+                if (tile == 0 && i > 0) finish(h0 + i - 1, g - 1, m_done, l_done);
+                fence_before_sync();
+                mbar_arrive(p_full(g));
+            }
+            m_done = m_ref;
+            l_done = l0 + l1;
         }
+        finish(h0 + nh - 1, g - 1, m_done, l_done);
     }
-    tmem_free(tmem, kTmemCols, warp, &s_fail);
+    finish_cta(&s_tmem, kTmemCols, warp, &s_fail);
 }
 
 }  // namespace bias
