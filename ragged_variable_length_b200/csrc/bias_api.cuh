@@ -71,13 +71,32 @@ ragged_status check_bias_problem(const ragged_bias_attn* a, bool need_v, ragged:
 
 int64_t tiles128(int64_t n) { return (n + ragged::bias::kQTile - 1) / ragged::bias::kQTile; }
 
+// Average length of B sequences of at most `longest` rows: `rows`, the row
+// count that a caller's stride implies, where it says less than B * longest.
+int64_t average_length(int64_t B, int64_t longest, int64_t rows) {
+    return B == 0 ? 1 : std::max<int64_t>(1, (std::min(B * longest, std::max<int64_t>(rows, B)) + B - 1) / B);
+}
+
+// Parts that a key row's queries are split into, where key tiles and heads
+// alone leave SMs without work and each CTA has many query tiles to walk.
+int64_t bwd_parts(const ragged_bias_attn* a) {
+    const int64_t avg_q = average_length(a->B, a->max_seqlen_q, a->lse_stride);
+    const int64_t avg_k = std::max<int64_t>(1, a->max_seqlen_k * avg_q / a->max_seqlen_q);
+    const int64_t ctas = std::max<int64_t>(1, a->B * tiles128(avg_k) * a->Hkv);
+    const int64_t tiles = (avg_q + ragged::bias::kTile - 1) / ragged::bias::kTile;
+    return std::max<int64_t>(1, std::min<int64_t>({8, 2LL * sm_count() / ctas, tiles / 4, tiles * (a->H / a->Hkv) / 16}));
+}
 // Workspace of the backward pass: delta [H, lse_stride] floats, an exponent per
-// (sequence, head, query tile), then the tiles' sums for the table's gradient
-// [B, H, query tiles, num_buckets].
+// (sequence, head, query tile), the tiles' sums for the table's gradient
+// [B, H, query tiles, num_buckets], and the parts' sums of dK and dV.
 int64_t bwd_delta_floats(const ragged_bias_attn* a) { return (a->H * a->lse_stride + 3) & ~int64_t(3); }
 int64_t bwd_items(const ragged_bias_attn* a) { return a->B * a->H * tiles128(a->max_seqlen_q); }
+int64_t bwd_small_floats(const ragged_bias_attn* a) {
+    return (bwd_delta_floats(a) + bwd_items(a) * (1 + a->num_buckets) + 3) & ~int64_t(3);
+}
 int64_t bwd_workspace(const ragged_bias_attn* a) {
-    return 4 * (bwd_delta_floats(a) + bwd_items(a) * (1 + a->num_buckets));
+    const int64_t parts = bwd_parts(a);
+    return 4 * (bwd_small_floats(a) + (parts == 1 ? 0 : parts * a->B * tiles128(a->max_seqlen_k) * ragged::bias::kQTile * a->Hkv * 128));
 }
 int64_t fwd_workspace(const ragged_bias_attn*) { return 0; }
 
@@ -90,7 +109,6 @@ constexpr int bias_span(int D, int fixed, int bytes_per_entry) {
     const int span = (entries - 1 - ragged::bias::kVecPad) / 2 - D;
     return span < 256 ? ragged::bias::kSpan : span < ragged::bias::kSpan ? span : ragged::bias::kSpan;
 }
-constexpr int bwd_q_span(int D, int num_buckets) { return bias_span(D, ragged::bias::bwd_q_fixed_bytes(num_buckets), 6); }
 constexpr int kBwdQSmemMax = ragged::bias::bwd_q_smem_bytes(ragged::bias::kMaxDistance, ragged::bias::kMaxBuckets, ragged::bias::kSpan);
 
 ragged_status check_workspace(const void* ws, int64_t have, int64_t need) {
@@ -109,17 +127,19 @@ dim3 bias_grid(int64_t tiles, int heads, int B) {
     return dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(heads), static_cast<unsigned>(B));
 }
 
-// Heads that one CTA walks over where two CTAs fit an SM: the number with the
-// least work on the fullest of the grid's slots, in units of a tile's time.  A
-// CTA's set-up costs about kSetup tiles, a head's start and end kHead.
-int heads_per_cta(int64_t row_tiles, int heads, int64_t col_tiles) {
-    constexpr int64_t kSetup = 4, kHead = 1;
-    const int64_t slots = 2LL * sm_count();
+// Heads that one CTA walks over: the number with the least time, in units of a
+// tile's, of a grid of `row_tiles` per head over `slots` CTAs at a time.  A CTA's
+// set-up costs about kSetup tiles, a head's start and end kHead; half a wave
+// stands for the uneven end.  (Forward, 64 sequences of 173 to 403 tokens, 12
+// heads: 118, 112, 109, 119, 127, 141 us with 1, 2, 3, 4, 6, 12 heads; 512 of 79
+// to 118, 6 heads: 86, 74, 70, 88, 65 us with 1, 2, 3, 4, 6.)
+int heads_per_cta(int64_t row_tiles, int64_t heads, int64_t col_tiles, int64_t slots) {
+    constexpr double kSetup = 4, kHead = 1;
     int best = 1;
-    int64_t best_cost = INT64_MAX;
+    double best_cost = 1e300;
     for (int n = 1; n <= heads; ++n) {
-        const int64_t ctas = row_tiles * ((heads + n - 1) / n);
-        const int64_t cost = ((ctas + slots - 1) / slots) * (kSetup + n * (kHead + col_tiles));
+        const double waves = static_cast<double>(row_tiles * ((heads + n - 1) / n)) / static_cast<double>(slots);
+        const double cost = (std::max(1.0, waves) + 0.5) * (kSetup + n * (kHead + static_cast<double>(col_tiles)));
         if (cost < best_cost) {
             best_cost = cost;
             best = n;
@@ -184,7 +204,8 @@ ragged_status launch_bias_fwd(const ragged::bias::Problem& p, uint16_t* out, int
     if (st != RAGGED_OK) return st;
     const int span = bias_span(p.D, fwd_fixed_bytes(), 5);
     const int64_t tiles = tiles128(p.max_q);
-    const int heads = heads_per_cta(tiles * p.B, p.H, (p.max_k + kTile - 1) / kTile);
+    const int64_t avg_q = average_length(p.B, p.max_q, p.lse_stride), avg_k = std::max<int64_t>(1, p.max_k * avg_q / p.max_q);
+    const int heads = heads_per_cta(p.B * tiles128(avg_q), p.H, (avg_k + kTile - 1) / kTile, 2LL * sm_count());
     bias_fwd_kernel<T><<<bias_grid(tiles, (p.H + heads - 1) / heads, p.B), kThreads, fwd_smem_bytes(p.D, span), s>>>(
         p, out, out_tok, heads, span);
     return cuda_check(cudaGetLastError(), "attention (position bias) launch");
@@ -194,15 +215,28 @@ template <typename T>
 ragged_status launch_bias_bwd(const ragged::bias::Problem& p, ragged::bias::BwdArgs a, cudaStream_t s) {
     using namespace ragged::bias;
     ragged_status st = ensure_smem(bias_bwd_q_kernel<T>, kBwdQSmemMax, g_bias_bwd_q_smem[kTypeSlot<T>]);
-    if (st == RAGGED_OK) st = ensure_smem(bias_bwd_kv_kernel<T>, bwd_kv_smem_bytes(kMaxDistance), g_bias_bwd_kv_smem[kTypeSlot<T>]);
+    if (st == RAGGED_OK) st = ensure_smem(bias_bwd_kv_kernel<T>, bwd_kv_smem_bytes(kMaxDistance, kSpan), g_bias_bwd_kv_smem[kTypeSlot<T>]);
     if (st != RAGGED_OK) return st;
-    a.span = bwd_q_span(p.D, p.num_buckets);
-    bias_bwd_q_kernel<T><<<bias_grid(a.q_tiles, p.H, p.B), kThreads, bwd_q_smem_bytes(p.D, p.num_buckets, a.span), s>>>(p, a);
+    const int64_t avg_q = average_length(p.B, p.max_q, p.lse_stride), avg_k = std::max<int64_t>(1, p.max_k * avg_q / p.max_q);
+    const int64_t slots = 2LL * sm_count();
+    a.span = bias_span(p.D, bwd_q_fixed_bytes(p.num_buckets), 3);
+    a.heads = heads_per_cta(p.B * tiles128(avg_q), p.H, (avg_k + kTile - 1) / kTile, slots);
+    bias_bwd_q_kernel<T><<<bias_grid(a.q_tiles, (p.H + a.heads - 1) / a.heads, p.B), kBwdThreads,
+                           bwd_q_smem_bytes(p.D, p.num_buckets, a.span), s>>>(p, a);
     st = cuda_check(cudaGetLastError(), "query gradient launch");
     if (st != RAGGED_OK) return st;
-    bias_bwd_kv_kernel<T><<<bias_grid(tiles128(p.max_k), p.Hkv, p.B), kThreads, bwd_kv_smem_bytes(p.D), s>>>(p, a);
+    a.span = bias_span(p.D, bwd_kv_fixed_bytes(), 3);
+    a.heads = a.parts > 1 ? 1 : heads_per_cta(p.B * tiles128(avg_k), p.Hkv, (avg_q + kTile - 1) / kTile * p.group, slots);
+    bias_bwd_kv_kernel<T><<<bias_grid(tiles128(p.max_k) * a.parts, (p.Hkv + a.heads - 1) / a.heads, p.B), kBwdThreads,
+                            bwd_kv_smem_bytes(p.D, a.span), s>>>(p, a);
     st = cuda_check(cudaGetLastError(), "key and value gradient launch");
     if (st != RAGGED_OK) return st;
+    if (a.parts > 1) {
+        const int64_t blocks = std::min<int64_t>((static_cast<int64_t>(p.max_k) * p.Hkv * 16 + 255) / 256, 8LL * sm_count());
+        bias_bwd_parts_kernel<T><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(p.B)), 256, 0, s>>>(p, a);
+        st = cuda_check(cudaGetLastError(), "key and value gradient sum launch");
+        if (st != RAGGED_OK) return st;
+    }
     bias_bwd_table_kernel<T><<<bias_grid(p.num_buckets, p.H, 1), 256, 0, s>>>(p, a);
     return cuda_check(cudaGetLastError(), "table gradient launch");
 }
@@ -214,9 +248,12 @@ ragged_status launch_bias_weight(const ragged::bias::Problem& p, const float* pr
     if (few_rows(p))
         return p.group * p.max_q <= 16 ? launch_few_weight<T, 1>(p, prev, weight, stride, s)
                                        : launch_few_weight<T, 2>(p, prev, weight, stride, s);
-    ragged_status st = ensure_smem(bias_weight_kernel<T>, weight_smem_bytes(kMaxDistance), g_bias_weight_smem[kTypeSlot<T>]);
+    ragged_status st = ensure_smem(bias_weight_kernel<T>, weight_smem_bytes(kMaxDistance, kSpan), g_bias_weight_smem[kTypeSlot<T>]);
     if (st != RAGGED_OK) return st;
-    bias_weight_kernel<T><<<bias_grid(tiles128(p.max_k), p.H, p.B), kThreads, weight_smem_bytes(p.D), s>>>(p, prev, weight, stride);
+    const int64_t avg_q = average_length(p.B, p.max_q, p.lse_stride), avg_k = std::max<int64_t>(1, p.max_k * avg_q / p.max_q);
+    const int heads = heads_per_cta(p.B * tiles128(avg_k), p.H, (avg_q + kTile - 1) / kTile, 3LL * sm_count());
+    bias_weight_kernel<T><<<bias_grid(tiles128(p.max_k), (p.H + heads - 1) / heads, p.B), kThreads, weight_smem_bytes(p.D, kSpan), s>>>(
+        p, prev, weight, stride, heads, kSpan);
     return cuda_check(cudaGetLastError(), "attention weight launch");
 }
 
@@ -344,13 +381,26 @@ ragged_status ragged_attn_bias_bwd(const ragged_bias_attn* a, const void* out, i
     if (st == RAGGED_OK) st = check_workspace(workspace, workspace_bytes, bwd_workspace(a));
     if (st != RAGGED_OK) return st;
     float* ws = static_cast<float*>(workspace);
-    ragged::bias::BwdArgs g{static_cast<const uint16_t*>(out), static_cast<const uint16_t*>(dout), out_tok_stride,
-                            dout_tok_stride, static_cast<uint16_t*>(dq), static_cast<uint16_t*>(dk),
-                            static_cast<uint16_t*>(dv), dq_tok_stride, a->H > 1 ? dq_head_stride : 0, dkv_tok_stride,
-                            a->Hkv > 1 ? dkv_head_stride : 0, ws,
-                            reinterpret_cast<int*>(ws + bwd_delta_floats(a)),
-                            ws + bwd_delta_floats(a) + bwd_items(a), static_cast<uint16_t*>(dtable),
-                            static_cast<int>(tiles128(a->max_seqlen_q)), 0};
+    ragged::bias::BwdArgs g{};
+    g.out = static_cast<const uint16_t*>(out);
+    g.dout = static_cast<const uint16_t*>(dout);
+    g.out_tok = out_tok_stride;
+    g.dout_tok = dout_tok_stride;
+    g.dq = static_cast<uint16_t*>(dq);
+    g.dk = static_cast<uint16_t*>(dk);
+    g.dv = static_cast<uint16_t*>(dv);
+    g.dq_tok = dq_tok_stride;
+    g.dq_head = a->H > 1 ? dq_head_stride : 0;
+    g.dkv_tok = dkv_tok_stride;
+    g.dkv_head = a->Hkv > 1 ? dkv_head_stride : 0;
+    g.delta = ws;
+    g.tile_exp = reinterpret_cast<int*>(ws + bwd_delta_floats(a));
+    g.partial = ws + bwd_delta_floats(a) + bwd_items(a);
+    g.dtable = static_cast<uint16_t*>(dtable);
+    g.q_tiles = static_cast<int>(tiles128(a->max_seqlen_q));
+    g.parts = static_cast<int>(bwd_parts(a));
+    g.part_sums = ws + bwd_small_floats(a);
+    g.part_rows = tiles128(a->max_seqlen_k) * ragged::bias::kQTile;
     return a->dtype == RAGGED_F16 ? launch_bias_bwd<__half>(p, g, s) : launch_bias_bwd<__nv_bfloat16>(p, g, s);
 }
 

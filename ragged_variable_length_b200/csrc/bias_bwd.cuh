@@ -9,6 +9,10 @@
 // one with query rows (dQ, delta, the table), one with key rows (dK, dV,
 // transposed scores).  Each recomputes S and dP, 7 products instead of 5.
 //
+// Both have eight row warps: two threads share a row, one for each half of a
+// tile's 64 columns (nothing is reduced along a row but the table's sums, which
+// have a column per thread).
+//
 // dS and P are rounded to the 16-bit type to be operands of the next product.
 // In f16 they would lose what lies below 2^-14: probabilities of long rows,
 // and gradients far below 1.  Both are therefore scaled by powers of two, which
@@ -21,8 +25,11 @@
 namespace ragged {
 namespace bias {
 
+constexpr int kBwdRows = 256;                   // row threads
+constexpr int kBwdThreads = kBwdRows + 64;      // and the MMA and load warps
+constexpr int kBwdMmaWarp = 8, kBwdLoadWarp = 9;
 constexpr int kBwdStages = 3;
-constexpr int kNoExp = -1000;       // a row (or tile) of zero gradients
+constexpr int kNoExp = -1000;                   // a row (or tile) of zero gradients
 
 template <typename T>
 constexpr bool kScaled = std::is_same<T, __half>::value;
@@ -44,377 +51,575 @@ struct BwdArgs {
     float* partial;   // [B][H][query tiles][num_buckets]
     uint16_t* dtable;
     int q_tiles;
-    int span;         // of the query kernel's expanded table
+    int span, heads;  // of a launch: positions of its expanded table, heads per CTA
+    // Key rows in parts (where the grid would not fill the GPU): queries of a
+    // part, and the parts' fp32 sums [part][B * key rows][Hkv][dK, dV][64].
+    int parts;
+    float* part_sums;
+    int64_t part_rows;   // key rows per sequence, a multiple of 128
 };
 
-__host__ __device__ constexpr int bwd_q_fixed_bytes(int num_buckets) {
-    return 1024 + 2 * kRowBytes + kBwdStages * 2 * kTileBytes + (num_buckets + 1) * 512 + 4 * kChunk;
+__device__ __forceinline__ void rows_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// bias_rows, bias_ids, bias_fill and bias_columns for 256 row threads.  An entry
+// of `ids` without a bucket holds num_buckets, the accumulator's spare row.
+__device__ __forceinline__ void bias_rows256(Bias16& t, const Problem& p, int pos, bool valid, int span, int* s_red) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lo = __reduce_min_sync(0xffffffffu, valid ? pos : INT_MAX);
+    const int hi = __reduce_max_sync(0xffffffffu, valid ? pos : INT_MIN);
+    if (lane == 0) {
+        s_red[warp] = lo;
+        s_red[8 + warp] = hi;
+    }
+    rows_barrier();
+    t.rmin = min(min(s_red[0], s_red[1]), min(s_red[2], s_red[3]));   // both halves hold the same rows
+    const int rmax = max(max(s_red[8], s_red[9]), max(s_red[10], s_red[11]));
+    const int64_t R = static_cast<int64_t>(rmax) - t.rmin;
+    t.D = p.D;
+    t.near = R <= span;
+    t.R = t.near ? static_cast<int>(R) : 0;
+    t.last = 2 * (t.D + t.R);
+    t.p_row = pos;
+    t.row = valid && t.near ? 2u * static_cast<uint32_t>(t.R - (pos - t.rmin)) : 0u;
 }
-__host__ __device__ constexpr int bwd_q_smem_bytes(int D, int num_buckets, int span) {
-    return bwd_q_fixed_bytes(num_buckets) + 4 * ((vec_entries(D, span) + 3) & ~3) + 2 * ((vec_entries(D, span) + 7) & ~7);
+template <int SIGN>
+__device__ __forceinline__ void bias_ids256(const Bias16& t, const Problem& p, uint8_t* ids) {
+#pragma unroll 4
+    for (int x = threadIdx.x; x <= t.last; x += kBwdRows) {
+        const int b = bucket_of(p, SIGN * (x - t.D - t.R));
+        ids[x] = static_cast<uint8_t>(b < 0 ? p.num_buckets : b);
+    }
+    for (int x = t.last + 1 + threadIdx.x; x <= t.last + kVecPad; x += kBwdRows) ids[x] = static_cast<uint8_t>(p.num_buckets);
+}
+// tab[num_buckets] is 0.
+__device__ __forceinline__ void bias_fill256(const Bias16& t, const uint8_t* ids, const uint16_t* tab) {
+#pragma unroll 4
+    for (int x = threadIdx.x; x <= t.last + kVecPad; x += kBwdRows) t.vec[x] = tab[ids[x]];
+}
+template <class PosOf>
+__device__ __forceinline__ void bias_columns256(const Bias16& t, int c0, int len, PosOf pos_of) {
+    const int tile = threadIdx.x >> 5, lane = threadIdx.x & 31, c = c0 + tile * kTile + lane;   // one tile per warp
+    static_assert(kChunkTiles == 8, "eight row warps");
+    if (c0 + tile * kTile >= len) return;
+    const bool v0 = c < len, v1 = c + 32 < len;
+    const int p0 = v0 ? pos_of(c) : 0, p1 = v1 ? pos_of(c + 32) : 0;
+    const int lo = -t.D, hi = t.R + t.D;
+    auto clamped = [&](int x) {
+        const int64_t d = static_cast<int64_t>(x) - t.rmin;
+        return d < lo ? lo : d > hi ? hi : static_cast<int>(d);
+    };
+    const int o0 = clamped(p0), o1 = clamped(p1);
+    const int first = __shfl_sync(0xffffffffu, o0, 0);
+    const bool left = __all_sync(0xffffffffu, (!v0 || o0 == lo) && (!v1 || o1 == lo));
+    const bool right = __all_sync(0xffffffffu, (!v0 || o0 == hi) && (!v1 || o1 == hi));
+    const bool run = __all_sync(0xffffffffu, (!v0 || o0 == first + lane) && (!v1 || o1 == first + 32 + lane));
+    int* off = t.off + tile * kTile;
+    if (t.near) {
+        off[lane] = v0 ? 2 * (o0 - lo) : 0;
+        off[lane + 32] = v1 ? 2 * (o1 - lo) : 0;
+    } else {
+        off[lane] = p0;
+        off[lane + 32] = p1;
+    }
+    if (lane == 0) t.kind[tile] = !t.near ? kClamped : left ? kLeft : right ? kRight : run ? kConsecutive : kGeneral;
 }
 
-// Query rows: dQ, delta, and this tile's sums for the table's gradient.
-// grid (query tiles, H, B), two CTAs per SM where the table is small.
-//
-// TMEM: S, dP (replaced in place by dS) and dQ, 64 columns each.  S of the next
-// tile is computed while dS of this one is, and dP of the next one while its
-// probabilities are.
+__device__ __forceinline__ uint32_t start_rows256(const uint32_t* s_tmem) {
+    asm volatile("bar.sync 3, 288;" ::: "memory");
+    fence_after_sync();
+    return *s_tmem;
+}
+__device__ __forceinline__ uint32_t start_mma256(uint32_t* s_tmem, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(s_tmem)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    fence_before_sync();
+    asm volatile("bar.sync 2, 64;" ::: "memory");
+    asm volatile("bar.arrive 3, 288;" ::: "memory");
+    fence_after_sync();
+    return *s_tmem;
+}
+__device__ __forceinline__ void finish_cta256(const uint32_t* s_tmem, uint32_t cols, int warp, const int* s_fail) {
+    fence_before_sync();
+    __syncthreads();
+    if (*s_fail && threadIdx.x == 0) raise_status(RAGGED_DEV_TIMEOUT);
+    if (warp == kBwdMmaWarp) {
+        fence_after_sync();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*s_tmem), "r"(cols) : "memory");
+    }
+}
+// 32 of a row's 64 fp32 columns at taddr, times f, rounded and stored.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) bias_bwd_q_kernel(const Problem p, const BwdArgs a) {
+__device__ __forceinline__ void store_tmem_half(uint32_t taddr, float f, uint16_t* dst, bool valid) {
+    float v[32];
+    tmem_ld32(taddr, v);
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = Cvt<T>::pack(v[2 * i] * f, v[2 * i + 1] * f);
+    if (valid) store_half_row(dst, w);
+}
+
+// p = 2^(x - lse) of the 32 columns from column c of a tile (x: scores before
+// scale and bias); the negated lse is a row's (nl) or the tile's columns' (neg_lse).
+template <typename T>
+__device__ __forceinline__ void probabilities(const Bias16& t, const Problem& p, int kind, const int* off, int c,
+                                              const float* neg_lse, float nl, float (&x)[32]) {
+    const bool flat = kind == kLeft || kind == kRight;
+    const float scale = flat ? p.scale_log2 : kLog2e;
+    const float add = flat ? to_float<T>(t.vec[kind == kLeft ? 0 : t.last]) * kLog2e : 0.f;
+    if (!flat) bias_add<T>(t, kind, off, c, p.scale, x);
+    const uint64_t sc2 = f2(scale, scale), add2 = f2(add, add);
+    if (neg_lse == nullptr) {
+        const uint64_t c2 = f2(add + nl, add + nl);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float a, b;
+            f2_split(f2_fma(f2(x[2 * i], x[2 * i + 1]), sc2, c2), a, b);
+            x[2 * i] = mma_attn::fast_exp2(a);
+            x[2 * i + 1] = mma_attn::fast_exp2(b);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 l = *reinterpret_cast<const float4*>(neg_lse + c + 4 * i);
+            float a, b;
+            f2_split(f2_fma(f2(x[4 * i], x[4 * i + 1]), sc2, f2_add(f2(l.x, l.y), add2)), a, b);
+            x[4 * i] = mma_attn::fast_exp2(a);
+            x[4 * i + 1] = mma_attn::fast_exp2(b);
+            f2_split(f2_fma(f2(x[4 * i + 2], x[4 * i + 3]), sc2, f2_add(f2(l.z, l.w), add2)), a, b);
+            x[4 * i + 2] = mma_attn::fast_exp2(a);
+            x[4 * i + 3] = mma_attn::fast_exp2(b);
+        }
+    }
+}
+
+__host__ __device__ constexpr int bwd_q_fixed_bytes(int num_buckets) {
+    return 1024 + kBwdStages * 2 * kTileBytes + (num_buckets + 1) * 4 * kBwdRows + 4 * kChunk;
+}
+__host__ __device__ constexpr int bwd_q_smem_bytes(int D, int num_buckets, int span) {
+    return bwd_q_fixed_bytes(num_buckets) + vec16_bytes(D, span) + ids_bytes(D, span);
+}
+
+// Query rows: dQ, delta, and each tile's sums for the table's gradient.
+// grid (query tiles, groups of heads, B), two CTAs per SM where the table is small.
+//
+// TMEM (256 columns): S, dP (each half replaced in place by its dS), dQ, and
+// the rows of Q and dO as packed A operands: an MMA with A in TMEM takes half
+// the time of one with A in shared memory, and the room goes to the table's
+// sums.  S of the next tile is computed while dS of this one is, dP of the
+// next one while its probabilities are.
+template <typename T>
+__global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Problem p, const BwdArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    // stat_full, tile_full[3], s_full, dp_full[2], a_full, b_full, done
-    __shared__ __align__(8) uint64_t s_bar[10];
-    __shared__ float s_tab[kMaxBuckets], s_rowscale[kQTile];
-    __shared__ int s_kind[kChunkTiles], s_red[8];
+    // kv_full[3], kv_done[3], qd_full, s_full, dp_full, a_full, b_full, dq_full, done
+    constexpr int kBars = 13;
+    __shared__ __align__(8) uint64_t s_bar[kBars];
+    __shared__ uint16_t s_tab[kMaxBuckets + 1];
+    __shared__ float s_delta[2][kQTile], s_undo[kQTile];
+    __shared__ int s_kind[kChunkTiles], s_red[16], s_exp[2][kQTile];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
 
-    const int q0 = blockIdx.x * kQTile, h = blockIdx.y, b = blockIdx.z;
+    const int q0 = blockIdx.x * kQTile, h0 = blockIdx.y * a.heads, b = blockIdx.z;
+    const int nh = min(a.heads, p.H - h0);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t item = (static_cast<int64_t>(b) * p.H + h) * a.q_tiles + blockIdx.x;
+    const int64_t item0 = (static_cast<int64_t>(b) * p.H + h0) * a.q_tiles + blockIdx.x;   // + i * q_tiles
     Seq s;
     const bool any = read_pair(p, b, s) && q0 < s.q_len;
     if (!any || s.k_len == 0) {   // nothing for the table; queries without keys get no gradient
-        if (tid < p.num_buckets) a.partial[item * p.num_buckets + tid] = 0.f;
-        if (any && tid < kQTile && q0 + tid < s.q_len) {
-            const uint32_t zero[32] = {};
-            store_row(a.dq + static_cast<int64_t>(s.q_start + q0 + tid) * a.dq_tok + h * a.dq_head, zero);
-        }
+        for (int i = tid; i < nh * p.num_buckets; i += kBwdThreads)
+            a.partial[(item0 + static_cast<int64_t>(i / p.num_buckets) * a.q_tiles) * p.num_buckets + i % p.num_buckets] = 0.f;
+        if (any)
+            for (int i = tid; i < nh * kQTile; i += kBwdThreads) {
+                const int r = q0 + i % kQTile;
+                const uint32_t zero[32] = {};
+                if (r < s.q_len) store_row(a.dq + static_cast<int64_t>(s.q_start + r) * a.dq_tok + (h0 + i / kQTile) * a.dq_head, zero);
+            }
         return;
     }
     const int nt = (s.k_len + kTile - 1) / kTile;
 
     const uint32_t raw = smem_addr(smem_raw);
-    const uint32_t sQ = (raw + 1023u) & ~1023u;
-    const uint32_t sdO = sQ + kRowBytes, sRing = sdO + kRowBytes;   // stage: K, then V
-    float* acc = reinterpret_cast<float*>(smem_raw + (sRing - raw) + kBwdStages * 2 * kTileBytes);   // [buckets + 1][128]
+    const uint32_t sRing = (raw + 1023u) & ~1023u;   // stage: K, then V
+    float* acc = reinterpret_cast<float*>(smem_raw + (sRing - raw) + kBwdStages * 2 * kTileBytes);   // [buckets + 1][256]
     auto stage = [&](uint32_t g) { return sRing + (g % kBwdStages) * 2 * kTileBytes; };
-
     const uint32_t bar0 = smem_addr(&s_bar[0]);
-    const uint32_t stat_full = bar0, s_full = bar0 + 8u * 4, a_full = bar0 + 8u * 7, b_full = bar0 + 8u * 8, done = bar0 + 8u * 9;
-    auto tile_full = [&](uint32_t g) { return bar0 + 8u * (1 + g % kBwdStages); };
-    // Two barriers, so that the load warp's wait for tile g - 2 is exact: that
-    // barrier's next phase needs tile g, which it has yet to load.
-    auto dp_full = [&](uint32_t g) { return bar0 + 8u * (5 + (g & 1)); };
-    if (tid == 0) {
-        mbar_init(stat_full, 32);
-        for (int i = 0; i < kBwdStages; ++i) mbar_init(tile_full(i), 32);
-        mbar_init(s_full, 1);
-        mbar_init(dp_full(0), 1);
-        mbar_init(dp_full(1), 1);
-        mbar_init(a_full, 128);
-        mbar_init(b_full, 128);
-        mbar_init(done, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        s_fail = 0;
-    }
-    const uint32_t tmem = tmem_alloc(&s_tmem, kTmemCols, warp);
-    const uint32_t dp_col = kTile, dq_col = 2 * kTile;
+    auto kv_full = [&](uint32_t g) { return bar0 + 8u * (g % kBwdStages); };
+    auto kv_done = [&](uint32_t g) { return bar0 + 8u * (3 + g % kBwdStages); };
+    const uint32_t qd_full = bar0 + 48, s_full = bar0 + 56, dp_full = bar0 + 64, a_full = bar0 + 72, b_full = bar0 + 80, dq_full = bar0 + 88, done = bar0 + 96;
+    constexpr uint32_t dp_col = kTile, dq_col = 2 * kTile, q_col = 3 * kTile, do_col = 3 * kTile + 32;
     const Wait wait{&s_fail};
 
-    if (warp == kTcLoadWarp) {
-        const int64_t z = static_cast<int64_t>(h / p.group) * p.kv_head;
-        const uint16_t* kb = p.k + s.k_start * p.kv_tok + z;
-        const uint16_t* vb = p.v + s.k_start * p.kv_tok + z;
-        load_rows<kQTile>(sQ, p.q + s.q_start * p.q_tok + h * p.q_head, p.q_tok, q0, s.q_len, lane);
-        load_rows<kQTile>(sdO, a.dout + s.q_start * a.dout_tok + h * 64, a.dout_tok, q0, s.q_len, lane);
-        cp_async_arrive_noinc(stat_full);
+    if (warp == kBwdLoadWarp) {
+        if (lane < kBars) mbar_init(bar0 + 8 * lane, lane < 3 ? 32 : lane == 6 || lane == 9 || lane == 10 ? kBwdRows : 1);
+        if (lane == 0) s_fail = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        __syncwarp();
+        start_loads();
         bool ok = true;
-        for (uint32_t g = 0; g < static_cast<uint32_t>(nt); ++g) {
-            // dP(g - 2) was issued behind dQ(g - 3), the last product of the stage's previous tile.
-            if (g >= kBwdStages) ok = wait.warp(dp_full(g), ((g - 2) >> 1) & 1);
-            if (!ok) break;
-            load_rows<kTile>(stage(g), kb, p.kv_tok, g * kTile, s.k_len, lane);
-            load_rows<kTile>(stage(g) + kTileBytes, vb, p.kv_tok, g * kTile, s.k_len, lane);
-            cp_async_arrive_noinc(tile_full(g));
+        uint32_t g = 0;
+        for (int i = 0; ok && i < nh; ++i) {
+            const int64_t z = static_cast<int64_t>((h0 + i) / p.group) * p.kv_head;
+            const uint16_t* kb = p.k + s.k_start * p.kv_tok + z;
+            const uint16_t* vb = p.v + s.k_start * p.kv_tok + z;
+            for (int t = 0; t < nt; ++t, ++g) {
+                if (g >= kBwdStages) ok = wait.warp(kv_done(g), (g / kBwdStages - 1) & 1);
+                if (!ok) break;
+                load_rows<kTile>(stage(g), kb, p.kv_tok, t * kTile, s.k_len, lane);
+                load_rows<kTile>(stage(g) + kTileBytes, vb, p.kv_tok, t * kTile, s.k_len, lane);
+                cp_async_arrive_noinc(kv_full(g));
+            }
         }
         cp_async_wait_all();
-    } else if (warp == kTcMmaWarp) {
+    } else if (warp == kBwdMmaWarp) {
+        const uint32_t tmem = start_mma256(&s_tmem, kTmemCols);
         if (lane == 0) {
             const uint32_t idesc_s = make_idesc(Cvt<T>::kFormat, 0, kTile), idesc_g = make_idesc(Cvt<T>::kFormat, 1, 64);
-            const uint32_t n = nt;
-            auto product = [&](uint32_t col, uint32_t sa, uint32_t sb) {   // [128, 64] = A B^T over the head dimension
+            auto product = [&](uint32_t col, uint32_t from, uint32_t sb) {   // [128, 64] = A B^T over the head dimension
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_f16(tmem + col, make_sdesc(sa + ks * 32), make_sdesc(sb + ks * 32), idesc_s, ks > 0);
+                for (int ks = 0; ks < 4; ++ks) mma_f16_ts(tmem + col, tmem + from + ks * 8, make_sdesc(sb + ks * 32), idesc_s, ks > 0);
             };
-            bool ok = wait(stat_full, 0) && wait(tile_full(0), 0);
-            if (ok) {
+            bool ok = true;
+            uint32_t g = 0;
+            for (int i = 0; ok && i < nh; ++i) {
+                ok = wait(qd_full, i & 1) && wait(kv_full(g), (g / kBwdStages) & 1);
+                if (!ok) break;
                 fence_async_smem();
                 fence_after_sync();
-                product(0, sQ, stage(0));
+                product(0, q_col, stage(g));
                 mma_commit(s_full);
-                product(dp_col, sdO, stage(0) + kTileBytes);
-                mma_commit(dp_full(0));
-            }
-            for (uint32_t g = 0; ok && g < n; ++g) {
-                ok = wait(a_full, g & 1);
-                if (ok && g + 1 < n) {
-                    ok = wait(tile_full(g + 1), ((g + 1) / kBwdStages) & 1);
+                product(dp_col, do_col, stage(g) + kTileBytes);
+                mma_commit(dp_full);
+                for (int t = 0; t < nt; ++t, ++g) {
+                    const bool more = t + 1 < nt;
+                    if (more) {
+                        ok = wait(kv_full(g + 1), ((g + 1) / kBwdStages) & 1);
+                        if (!ok) break;
+                        fence_async_smem();
+                    }
+                    ok = wait(a_full, g & 1);   // S has been read
                     if (!ok) break;
-                    fence_async_smem();
+                    if (more) {
+                        fence_after_sync();
+                        product(0, q_col, stage(g + 1));
+                        mma_commit(s_full);
+                    }
+                    ok = wait(b_full, g & 1);   // dS is there
+                    if (!ok) break;
                     fence_after_sync();
-                    product(0, sQ, stage(g + 1));
-                    mma_commit(s_full);
-                }
-                ok = ok && wait(b_full, g & 1);
-                if (!ok) break;
-                fence_after_sync();
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_f16_ts(tmem + dq_col, tmem + dp_col + ks * 8, make_sdesc(stage(g) + ks * 2048), idesc_g,
-                               (g > 0 || ks > 0) ? 1u : 0u);
-                if (g + 1 < n) {
-                    product(dp_col, sdO, stage(g + 1) + kTileBytes);
-                    mma_commit(dp_full(g + 1));
+                    for (int ks = 0; ks < 4; ++ks)   // dS of columns 0-31 at dP + 0, of 32-63 at dP + 32
+                        mma_f16_ts(tmem + dq_col, tmem + dp_col + (ks >> 1) * 32 + (ks & 1) * 8, make_sdesc(stage(g) + ks * 2048), idesc_g,
+                                   (t > 0 || ks > 0) ? 1u : 0u);
+                    mma_commit(kv_done(g));
+                    if (more) {
+                        product(dp_col, do_col, stage(g + 1) + kTileBytes);
+                        mma_commit(dp_full);
+                    } else {
+                        mma_commit(dq_full);
+                    }
                 }
             }
             mma_commit(done);
             mbar_wait(done, 0);
         }
+        __syncwarp();
     } else {
-        const int row = q0 + tid;
-        const bool valid = row < s.q_len, warp_rows = q0 + warp * 32 < s.q_len;
+        const int half = warp >> 2, r = tid & 127, row = q0 + r;
+        const bool valid = row < s.q_len, warp_rows = q0 + (warp & 3) * 32 < s.q_len;
         const int64_t t_row = s.q_start + (valid ? row : 0);
-        Bias t;
-        uint8_t* extra = reinterpret_cast<uint8_t*>(acc + (p.num_buckets + 1) * kQTile);
-        t.vec = reinterpret_cast<float*>(extra);
-        uint16_t* ids = reinterpret_cast<uint16_t*>(extra + 4 * ((vec_entries(p.D, a.span) + 3) & ~3));
-        t.off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(ids) + 2 * ((vec_entries(p.D, a.span) + 7) & ~7));
+        Bias16 t;
+        uint8_t* extra = reinterpret_cast<uint8_t*>(acc + (p.num_buckets + 1) * kBwdRows);
+        t.vec = reinterpret_cast<uint16_t*>(extra);
+        uint8_t* ids = extra + vec16_bytes(p.D, a.span);
+        t.off = reinterpret_cast<int*>(ids + ids_bytes(p.D, a.span));
         t.kind = s_kind;
-        t.tab = s_tab;
-        // delta, and the exponent of the row's largest |dO|
-        float delta = 0.f, big = 0.f;
-        if (valid) {
-            const uint4* o = reinterpret_cast<const uint4*>(a.out + t_row * a.out_tok + h * 64);
-            const uint4* d = reinterpret_cast<const uint4*>(a.dout + t_row * a.dout_tok + h * 64);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const uint4 x = __ldg(o + c), y = __ldg(d + c);
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float d0 = to_float<T>(static_cast<uint16_t>(ys[i])), d1 = to_float<T>(static_cast<uint16_t>(ys[i] >> 16));
-                    delta = fmaf(to_float<T>(static_cast<uint16_t>(xs[i])), d0, delta);
-                    delta = fmaf(to_float<T>(static_cast<uint16_t>(xs[i] >> 16)), d1, delta);
-                    if constexpr (kScaled<T>) big = fmaxf(big, fmaxf(fabsf(d0), fabsf(d1)));
-                }
-            }
-            a.delta[h * p.lse_stride + t_row] = delta;
-        }
-        int e = kNoExp;
-        float r = 1.f, undo = 1.f;   // dS is kept times r
-        if constexpr (kScaled<T>) {
-            if (big > 0.f && big < INFINITY) {
-                e = ilogbf(big) + 1;
-                r = pow2(kSExp - e);
-                undo = pow2(e - kSExp);
-            }
-            const int top = __reduce_max_sync(0xffffffffu, e);
-            if (lane == 0) s_red[warp] = top;
-            row_barrier();
-            if (tid == 0) a.tile_exp[item] = max(max(s_red[0], s_red[1]), max(s_red[2], s_red[3]));
-            row_barrier();
-        }
-        const float lse = valid ? lse_log2(p.lse[h * p.lse_stride + t_row]) : INFINITY;
-        for (int n = 0; n <= p.num_buckets; ++n) acc[n * kQTile + tid] = 0.f;
-        bias_rows(t, p, valid ? query_pos(p, s, row) : 0, valid, a.span, s_red);
-        bias_expand<T, 1, true>(t, p, h, ids);
-
-        const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        const uint64_t nl2 = f2(-lse, -lse), r2 = f2(r, r), nd2 = f2(-delta * r, -delta * r);
-        const char* id_row = reinterpret_cast<const char*>(ids) + (t.row >> 1);
+        const bool has_entry = tid < p.num_buckets;
+        const uint16_t* column = p.table + static_cast<int64_t>(has_entry ? tid : 0) * p.H + h0;
+        uint16_t entry = __ldg(column);
+        if (tid == p.num_buckets) s_tab[tid] = 0;
+        bias_rows256(t, p, valid ? query_pos(p, s, row) : 0, valid, a.span, s_red);
+        bias_ids256<1>(t, p, ids);
+        bias_columns256(t, 0, s.k_len, [&](int c) { return key_pos(p, s, c); });
+        const uint32_t tmem = start_rows256(&s_tmem);
+        const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         char* acc_row = reinterpret_cast<char*>(acc + tid);
-        float far_left = 0.f, far_right = 0.f;   // dS of the tiles past either end of the table
+        const uint8_t* id_row = ids + (t.row >> 1);
         bool ok = true;
-        for (int g = 0; g < nt; ++g) {
-            if (g % kChunkTiles == 0) {
-                if (g) row_barrier();
-                bias_columns(t, g * kTile, s.k_len, [&](int c) { return key_pos(p, s, c); });
-                row_barrier();
-            }
-            const int kind = t.kind[g % kChunkTiles];
-            const int* off = t.off + (g % kChunkTiles) * kTile;
-            const int cols = s.k_len - g * kTile;
-            float x[2][32];
-            ok = ok && wait.warp(s_full, g & 1);
+        uint32_t g = 0;
+        float undo = 1.f, far_left = 0.f, far_right = 0.f;
+        // End of head h: dQ, and the table's sums of its tile.
+        auto finish = [&](int i) {
+            ok = ok && wait.warp(dq_full, i & 1);
             if (ok && warp_rows) {
                 fence_after_sync();
-                tmem_ld32(t_lane, x[0]);
-                tmem_ld32(t_lane + 32, x[1]);
+                store_tmem_half<T>(t_lane + dq_col + half * 32, p.scale * undo, a.dq + t_row * a.dq_tok + (h0 + i) * a.dq_head + half * 32, valid);
             }
-            fence_before_sync();
-            mbar_arrive(a_full);
-            if (ok && warp_rows) {
+            *reinterpret_cast<float*>(acc_row + ids[0] * (4 * kBwdRows)) += far_left;
+            *reinterpret_cast<float*>(acc_row + ids[t.last] * (4 * kBwdRows)) += far_right;
+            if (half == 0) s_undo[r] = valid ? undo : 0.f;
+            rows_barrier();
+            for (int n = warp; n < p.num_buckets; n += 8) {   // each thread's sums, unscaled, in a fixed order
+                float sum = 0.f;
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    bias_add(t, kind, off, hf * 32, p.scale_log2, x[hf]);
+                for (int k = 0; k < 8; ++k) {
+                    const int u = lane + 32 * k;
+                    sum += q0 + (u & 127) < s.q_len ? acc[n * kBwdRows + u] * s_undo[u & 127] : 0.f;
+                }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float u, v;
-                        f2_split(f2_add(f2(x[hf][2 * i], x[hf][2 * i + 1]), nl2), u, v);
-                        x[hf][2 * i] = mma_attn::fast_exp2(u);
-                        x[hf][2 * i + 1] = mma_attn::fast_exp2(v);
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (lane == 0) a.partial[(item0 + static_cast<int64_t>(i) * a.q_tiles) * p.num_buckets + n] = sum;
+            }
+            rows_barrier();
+        };
+        for (int i = 0; i < nh; ++i) {
+            const int h = h0 + i;
+            // This thread's halves of the rows of Q, dO and O: delta, the exponent of the largest |dO|.
+            uint4 qw[4], dw[4];
+            float delta = 0.f, big = 0.f;
+            {
+                const uint4* qp = reinterpret_cast<const uint4*>(p.q + t_row * p.q_tok + h * p.q_head) + half * 4;
+                const uint4* dp = reinterpret_cast<const uint4*>(a.dout + t_row * a.dout_tok + h * 64) + half * 4;
+                const uint4* op = reinterpret_cast<const uint4*>(a.out + t_row * a.out_tok + h * 64) + half * 4;
+                uint4 ow[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    qw[c] = valid ? __ldg(qp + c) : make_uint4(0, 0, 0, 0);
+                    dw[c] = valid ? __ldg(dp + c) : make_uint4(0, 0, 0, 0);
+                    ow[c] = valid ? __ldg(op + c) : make_uint4(0, 0, 0, 0);
+                }
+                if (i > 0) finish(i - 1);   // its loads are on their way meanwhile
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t ys[4] = {dw[c].x, dw[c].y, dw[c].z, dw[c].w}, xs[4] = {ow[c].x, ow[c].y, ow[c].z, ow[c].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float d0 = to_float<T>(static_cast<uint16_t>(ys[k])), d1 = to_float<T>(static_cast<uint16_t>(ys[k] >> 16));
+                        delta = fmaf(to_float<T>(static_cast<uint16_t>(xs[k])), d0, delta);
+                        delta = fmaf(to_float<T>(static_cast<uint16_t>(xs[k] >> 16)), d1, delta);
+                        if constexpr (kScaled<T>) big = fmaxf(big, fmaxf(fabsf(d0), fabsf(d1)));
                     }
                 }
-                if (cols < kTile) {
+            }
+            {   // Q and dO to TMEM: every product of the head before has finished
+                uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (i >= cols) x[i >> 5][i & 31] = 0.f;
+                for (int c = 0; c < 4; ++c) {
+                    w[4 * c] = qw[c].x;
+                    w[4 * c + 1] = qw[c].y;
+                    w[4 * c + 2] = qw[c].z;
+                    w[4 * c + 3] = qw[c].w;
+                }
+                tmem_st16_u(t_lane + q_col + half * 16, w);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    w[4 * c] = dw[c].x;
+                    w[4 * c + 1] = dw[c].y;
+                    w[4 * c + 2] = dw[c].z;
+                    w[4 * c + 3] = dw[c].w;
+                }
+                tmem_st16_u(t_lane + do_col + half * 16, w);
+                tmem_wait_st();
+                fence_before_sync();
+                mbar_arrive(qd_full);
+            }
+            s_delta[half][r] = delta;
+            if constexpr (kScaled<T>) s_exp[half][r] = big > 0.f && big < INFINITY ? ilogbf(big) + 1 : kNoExp;
+            for (int n = 0; n <= p.num_buckets; ++n) acc[n * kBwdRows + tid] = 0.f;
+            if (has_entry) s_tab[tid] = bias_bits<T>(entry);
+            rows_barrier();
+            bias_fill256(t, ids, s_tab);
+            if (i + 1 < nh) entry = __ldg(column + i + 1);
+            delta = s_delta[0][r] + s_delta[1][r];
+            if (half == 0 && valid) a.delta[h * p.lse_stride + t_row] = delta;
+            float rs = 1.f;   // dS is kept times rs
+            undo = 1.f;
+            if constexpr (kScaled<T>) {
+                const int e = max(s_exp[0][r], s_exp[1][r]);
+                if (e != kNoExp) {
+                    rs = pow2(kSExp - e);
+                    undo = pow2(e - kSExp);
+                }
+                if (half == 0) {
+                    const int top = __reduce_max_sync(0xffffffffu, e);
+                    if (lane == 0) s_red[warp] = top;
                 }
             }
-            ok = ok && wait.warp(dp_full(g), (g >> 1) & 1);
-            if (ok && warp_rows) {
-                fence_after_sync();
+            const float nl = valid ? -lse_log2(p.lse[h * p.lse_stride + t_row]) : -INFINITY;
+            const uint64_t r2 = f2(rs, rs), nd2 = f2(-delta * rs, -delta * rs);
+            far_left = far_right = 0.f;
+            rows_barrier();
+            if constexpr (kScaled<T>)
+                if (tid == 0) a.tile_exp[item0 + static_cast<int64_t>(i) * a.q_tiles] = max(max(s_red[0], s_red[1]), max(s_red[2], s_red[3]));
+            for (int tile = 0; tile < nt; ++tile, ++g) {
+                if (tile % kChunkTiles == 0 && (tile > 0 || (i > 0 && nt > kChunkTiles))) {
+                    if (tile > 0) rows_barrier();
+                    bias_columns256(t, tile * kTile, s.k_len, [&](int c) { return key_pos(p, s, c); });
+                    rows_barrier();
+                }
+                const int kind = t.kind[tile % kChunkTiles];
+                const int* off = t.off + (tile % kChunkTiles) * kTile;
+                const int cols = s.k_len - tile * kTile - half * 32;
+                float x[32];
+                ok = ok && wait.warp(s_full, g & 1);
+                if (ok && warp_rows) {
+                    fence_after_sync();
+                    tmem_ld32(t_lane + half * 32, x);
+                }
+                fence_before_sync();
+                mbar_arrive(a_full);
+                if (ok && warp_rows) {
+                    probabilities<T>(t, p, kind, off, half * 32, nullptr, nl, x);
+                    if (cols < 32) {
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
+                        for (int c = 0; c < 32; ++c)
+                            if (c >= cols) x[c] = 0.f;
+                    }
+                }
+                ok = ok && wait.warp(dp_full, g & 1);
+                if (ok && warp_rows) {
+                    fence_after_sync();
                     float y[32];
-                    tmem_ld32(t_lane + dp_col + hf * 32, y);
+                    tmem_ld32(t_lane + dp_col + half * 32, y);
                     uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint64_t d = f2_mul(f2(x[hf][2 * i], x[hf][2 * i + 1]), f2_fma(f2(y[2 * i], y[2 * i + 1]), r2, nd2));
-                        f2_split(d, x[hf][2 * i], x[hf][2 * i + 1]);
-                        w[i] = Cvt<T>::pack(x[hf][2 * i], x[hf][2 * i + 1]);
+                    for (int c = 0; c < 16; ++c) {
+                        f2_split(f2_mul(f2(x[2 * c], x[2 * c + 1]), f2_fma(f2(y[2 * c], y[2 * c + 1]), r2, nd2)), x[2 * c], x[2 * c + 1]);
+                        w[c] = Cvt<T>::pack(x[2 * c], x[2 * c + 1]);
                     }
-                    tmem_st16_u(t_lane + dp_col + hf * 16, w);
+                    tmem_st16_u(t_lane + dp_col + half * 32, w);
+                    tmem_wait_st();
                 }
-                tmem_wait_st();
-            }
-            fence_before_sync();
-            mbar_arrive(b_full);
-            if (ok && warp_rows) {   // the table's share, behind the hand-over
-                if (kind == kLeft || kind == kRight) {
-                    float sum = 0.f;
+                fence_before_sync();
+                mbar_arrive(b_full);
+                if (ok && warp_rows) {   // the table's share, behind the hand-over
+                    if (kind == kLeft || kind == kRight) {
+                        uint64_t sum = f2(x[0], x[1]);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) sum += x[0][i] + x[1][i];
-                    if (kind == kLeft) far_left += sum;
-                    else far_right += sum;
-                } else if (kind == kClamped) {
+                        for (int c = 1; c < 16; ++c) sum = f2_add(sum, f2(x[2 * c], x[2 * c + 1]));
+                        float u, v;
+                        f2_split(sum, u, v);
+                        if (kind == kLeft) far_left += u + v;
+                        else far_right += u + v;
+                    } else {
+                        // Addresses first: a load of the next one could not pass a store to the sums.
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) {
-                        const int d = max(-t.D, min(t.D, pos_diff(off[i], t.p_row)));
-                        *reinterpret_cast<float*>(acc_row + ids[d + t.D]) += x[i >> 5][i & 31];
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t at[16];
+                            if (kind == kConsecutive) {
+                                const uint8_t* id = id_row + (off[0] >> 1) + half * 32 + q * 16;
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) at[c] = id[c];
+                            } else if (kind == kGeneral) {
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) {
+                                    const int4 o = *reinterpret_cast<const int4*>(off + half * 32 + q * 16 + 4 * c);
+                                    at[4 * c] = id_row[o.x >> 1];
+                                    at[4 * c + 1] = id_row[o.y >> 1];
+                                    at[4 * c + 2] = id_row[o.z >> 1];
+                                    at[4 * c + 3] = id_row[o.w >> 1];
+                                }
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) at[c] = ids[max(-t.D, min(t.D, pos_diff(off[half * 32 + q * 16 + c], t.p_row))) + t.D];
+                            }
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) *reinterpret_cast<float*>(acc_row + at[c] * (4 * kBwdRows)) += x[q * 16 + c];
+                        }
                     }
-                } else if (kind == kConsecutive) {
-                    const uint16_t* id = reinterpret_cast<const uint16_t*>(id_row + (off[0] >> 1));
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) *reinterpret_cast<float*>(acc_row + id[i]) += x[i >> 5][i & 31];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        *reinterpret_cast<float*>(acc_row + *reinterpret_cast<const uint16_t*>(id_row + (off[i] >> 1))) += x[i >> 5][i & 31];
                 }
             }
         }
-        ok = ok && wait.warp(done, 0);
-        if (ok && warp_rows) {
-            fence_after_sync();
-            store_tmem_row<T>(t_lane + dq_col, p.scale * undo, a.dq + t_row * a.dq_tok + h * a.dq_head, valid);
-        }
-        // This tile's share of the table's gradient: each thread's sums, unscaled, in a fixed order.
-        if (t.last >= 0) {
-            *reinterpret_cast<float*>(acc_row + ids[0]) += far_left;
-            *reinterpret_cast<float*>(acc_row + ids[t.last]) += far_right;
-        }
-        s_rowscale[tid] = valid ? undo : 0.f;
-        row_barrier();
-        for (int n = warp; n < p.num_buckets; n += kRowWarps) {
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int u = lane + 32 * k;
-                sum += q0 + u < s.q_len ? acc[n * kQTile + u] * s_rowscale[u] : 0.f;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == 0) a.partial[item * p.num_buckets + n] = sum;
-        }
+        finish(nh - 1);
     }
-    tmem_free(tmem, kTmemCols, warp, &s_fail);
+    finish_cta256(&s_tmem, kTmemCols, warp, &s_fail);
 }
 
-__host__ __device__ constexpr int bwd_kv_smem_bytes(int D) {
-    return 1024 + 2 * kRowBytes + kBwdStages * 2 * kTileBytes + 4 * ((vec_entries(D, kSpan) + 3) & ~3) + 12 * kChunk;
+__host__ __device__ constexpr int bwd_kv_fixed_bytes() { return 1024 + 2 * kRowBytes + kBwdStages * 2 * kTileBytes + 12 * kChunk; }
+__host__ __device__ constexpr int bwd_kv_smem_bytes(int D, int span) {
+    return bwd_kv_fixed_bytes() + vec16_bytes(D, span) + ids_bytes(D, span);
 }
 
-// Key rows: dK and dV, over the query tiles of every query head of the key's
-// head.  grid (key tiles, Hkv, B), two CTAs per SM.
+// Key rows: dK and dV, over the query tiles of every query head of a key head.
+// grid (key tiles * parts, groups of key heads, B), two CTAs per SM.
 //
-// TMEM: S^T (replaced by P^T), dP^T (replaced by dS^T), dK and dV.
+// TMEM (256 columns): S^T and dP^T (each half replaced in place by its P^T,
+// dS^T), dK and dV.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) bias_bwd_kv_kernel(const Problem p, const BwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Problem p, const BwdArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    // stat_full, tile_full[3], s_full, dp_full[2], a_full, b_full, done
-    __shared__ __align__(8) uint64_t s_bar[10];
-    __shared__ float s_tab[kMaxBuckets];
-    __shared__ int s_kind[kChunkTiles], s_red[8];
+    // kv_full, kv_empty, q_full[3], q_done[3], s_full, dp_full, a_full, b_full, acc_full, done
+    constexpr int kBars = 14;
+    __shared__ __align__(8) uint64_t s_bar[kBars];
+    __shared__ uint16_t s_tab[kMaxBuckets + 1];
+    __shared__ int s_kind[kChunkTiles], s_red[16];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
 
-    const int k0 = blockIdx.x * kQTile, z = blockIdx.y, b = blockIdx.z;
+    const int part = blockIdx.x % a.parts, k0 = (blockIdx.x / a.parts) * kQTile, z0 = blockIdx.y * a.heads, b = blockIdx.z;
+    const int nz = min(a.heads, p.Hkv - z0);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Seq s;
     if (!read_pair(p, b, s) || k0 >= s.k_len) return;
     if (s.q_len == 0) {   // keys without queries
-        if (tid < kQTile && k0 + tid < s.k_len) {
-            const uint32_t zero[32] = {};
-            const int64_t at = static_cast<int64_t>(s.k_start + k0 + tid) * a.dkv_tok + z * a.dkv_head;
-            store_row(a.dk + at, zero);
-            store_row(a.dv + at, zero);
-        }
+        if (part == 0)
+            for (int i = tid; i < nz * kQTile; i += kBwdThreads) {
+                const int r = k0 + i % kQTile;
+                if (r >= s.k_len) continue;
+                const uint32_t zero[32] = {};
+                const int64_t at = static_cast<int64_t>(s.k_start + r) * a.dkv_tok + (z0 + i / kQTile) * a.dkv_head;
+                store_row(a.dk + at, zero);
+                store_row(a.dv + at, zero);
+            }
         return;
     }
-    const int nt = (s.q_len + kTile - 1) / kTile;   // per query head
-    const uint32_t n = static_cast<uint32_t>(nt) * p.group;
+    // This part's query tiles [t0, t1) of every head; a part without any still writes zeros.
+    const int nt_all = (s.q_len + kTile - 1) / kTile, per = (nt_all + a.parts - 1) / a.parts;
+    const int t0 = min(nt_all, part * per), t1 = min(nt_all, t0 + per), nt = t1 - t0;
 
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t sK = (raw + 1023u) & ~1023u;
     const uint32_t sV = sK + kRowBytes, sRing = sV + kRowBytes;   // stage: Q, then dO
     uint8_t* extra = smem_raw + (sRing - raw) + kBwdStages * 2 * kTileBytes;
     auto stage = [&](uint32_t g) { return sRing + (g % kBwdStages) * 2 * kTileBytes; };
-
     const uint32_t bar0 = smem_addr(&s_bar[0]);
-    const uint32_t stat_full = bar0, s_full = bar0 + 8u * 4, a_full = bar0 + 8u * 7, b_full = bar0 + 8u * 8, done = bar0 + 8u * 9;
-    auto tile_full = [&](uint32_t g) { return bar0 + 8u * (1 + g % kBwdStages); };
-    auto dp_full = [&](uint32_t g) { return bar0 + 8u * (5 + (g & 1)); };
-    if (tid == 0) {
-        mbar_init(stat_full, 32);
-        for (int i = 0; i < kBwdStages; ++i) mbar_init(tile_full(i), 32);
-        mbar_init(s_full, 1);
-        mbar_init(dp_full(0), 1);
-        mbar_init(dp_full(1), 1);
-        mbar_init(a_full, 128);
-        mbar_init(b_full, 128);
-        mbar_init(done, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        s_fail = 0;
-    }
-    const uint32_t tmem = tmem_alloc(&s_tmem, kTmemCols, warp);
-    const uint32_t dp_col = kTile, dk_col = 2 * kTile, dv_col = 3 * kTile;
+    const uint32_t kv_full = bar0, kv_empty = bar0 + 8, s_full = bar0 + 64, dp_full = bar0 + 72, a_full = bar0 + 80, b_full = bar0 + 88, acc_full = bar0 + 96, done = bar0 + 104;
+    auto q_full = [&](uint32_t g) { return bar0 + 8u * (2 + g % kBwdStages); };
+    auto q_done = [&](uint32_t g) { return bar0 + 8u * (5 + g % kBwdStages); };
+    constexpr uint32_t dp_col = kTile, dk_col = 2 * kTile, dv_col = 3 * kTile;
     const Wait wait{&s_fail};
+    const uint32_t per_head = static_cast<uint32_t>(nt) * p.group;   // tiles of a key head
 
-    if (warp == kTcLoadWarp) {
-        const int64_t at = s.k_start * p.kv_tok + z * p.kv_head;
-        load_rows<kQTile>(sK, p.k + at, p.kv_tok, k0, s.k_len, lane);
-        load_rows<kQTile>(sV, p.v + at, p.kv_tok, k0, s.k_len, lane);
-        cp_async_arrive_noinc(stat_full);
+    if (warp == kBwdLoadWarp) {
+        if (lane < kBars) mbar_init(bar0 + 8 * lane, lane == 0 || (lane >= 2 && lane < 5) ? 32 : lane == 10 || lane == 11 ? kBwdRows : 1);
+        if (lane == 0) s_fail = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        __syncwarp();
+        start_loads();
         bool ok = true;
         uint32_t g = 0;
-        for (int h = z * p.group; ok && h < (z + 1) * p.group; ++h) {
-            const uint16_t* qb = p.q + s.q_start * p.q_tok + h * p.q_head;
-            const uint16_t* db = a.dout + s.q_start * a.dout_tok + h * 64;
-            for (int i = 0; i < nt; ++i, ++g) {
-                if (g >= kBwdStages) ok = wait.warp(dp_full(g), ((g - 2) >> 1) & 1);
-                if (!ok) break;
-                load_rows<kTile>(stage(g), qb, p.q_tok, i * kTile, s.q_len, lane);
-                load_rows<kTile>(stage(g) + kTileBytes, db, a.dout_tok, i * kTile, s.q_len, lane);
-                cp_async_arrive_noinc(tile_full(g));
+        for (int i = 0; ok && i < nz && nt > 0; ++i) {
+            const int z = z0 + i;
+            if (i > 0) ok = wait.warp(kv_empty, (i - 1) & 1);
+            if (!ok) break;
+            const int64_t at = s.k_start * p.kv_tok + z * p.kv_head;
+            load_rows<kQTile>(sK, p.k + at, p.kv_tok, k0, s.k_len, lane);
+            load_rows<kQTile>(sV, p.v + at, p.kv_tok, k0, s.k_len, lane);
+            cp_async_arrive_noinc(kv_full);
+            for (int h = z * p.group; ok && h < (z + 1) * p.group; ++h) {
+                const uint16_t* qb = p.q + s.q_start * p.q_tok + h * p.q_head;
+                const uint16_t* db = a.dout + s.q_start * a.dout_tok + h * 64;
+                for (int t = t0; t < t1; ++t, ++g) {
+                    if (g >= kBwdStages) ok = wait.warp(q_done(g), (g / kBwdStages - 1) & 1);
+                    if (!ok) break;
+                    load_rows<kTile>(stage(g), qb, p.q_tok, t * kTile, s.q_len, lane);
+                    load_rows<kTile>(stage(g) + kTileBytes, db, a.dout_tok, t * kTile, s.q_len, lane);
+                    cp_async_arrive_noinc(q_full(g));
+                }
             }
         }
         cp_async_wait_all();
-    } else if (warp == kTcMmaWarp) {
+    } else if (warp == kBwdMmaWarp) {
+        const uint32_t tmem = start_mma256(&s_tmem, kTmemCols);
         if (lane == 0) {
             const uint32_t idesc_s = make_idesc(Cvt<T>::kFormat, 0, kTile), idesc_g = make_idesc(Cvt<T>::kFormat, 1, 64);
             auto product = [&](uint32_t col, uint32_t sa, uint32_t sb) {
@@ -422,157 +627,226 @@ __global__ void __launch_bounds__(kThreads, 2) bias_bwd_kv_kernel(const Problem 
                 for (int ks = 0; ks < 4; ++ks)
                     mma_f16(tmem + col, make_sdesc(sa + ks * 32), make_sdesc(sb + ks * 32), idesc_s, ks > 0);
             };
-            auto gradient = [&](uint32_t col, uint32_t from, uint32_t sb, bool first) {   // += A (TMEM) B
+            auto gradient = [&](uint32_t col, uint32_t from, uint32_t sb, bool first) {   // += A (TMEM, two halves) B
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_f16_ts(tmem + col, tmem + from + ks * 8, make_sdesc(sb + ks * 2048), idesc_g, (!first || ks > 0) ? 1u : 0u);
+                    mma_f16_ts(tmem + col, tmem + from + (ks >> 1) * 32 + (ks & 1) * 8, make_sdesc(sb + ks * 2048), idesc_g, (!first || ks > 0) ? 1u : 0u);
             };
-            bool ok = wait(stat_full, 0) && wait(tile_full(0), 0);
-            if (ok) {
+            bool ok = true;
+            uint32_t g = 0;
+            for (int i = 0; ok && i < nz && nt > 0; ++i) {
+                ok = wait(kv_full, i & 1) && wait(q_full(g), (g / kBwdStages) & 1);
+                if (!ok) break;
                 fence_async_smem();
                 fence_after_sync();
-                product(0, sK, stage(0));
+                product(0, sK, stage(g));
                 mma_commit(s_full);
-                product(dp_col, sV, stage(0) + kTileBytes);
-                mma_commit(dp_full(0));
-            }
-            for (uint32_t g = 0; ok && g < n; ++g) {
-                ok = wait(a_full, g & 1);
-                if (!ok) break;
-                fence_after_sync();
-                gradient(dv_col, 0, stage(g) + kTileBytes, g == 0);
-                if (g + 1 < n) {
-                    ok = wait(tile_full(g + 1), ((g + 1) / kBwdStages) & 1);
+                product(dp_col, sV, stage(g) + kTileBytes);
+                mma_commit(dp_full);
+                if (per_head == 1) mma_commit(kv_empty);   // the head's last product with K and V
+                for (uint32_t n = 0; n < per_head; ++n, ++g) {
+                    const bool more = n + 1 < per_head;
+                    if (more) {
+                        ok = wait(q_full(g + 1), ((g + 1) / kBwdStages) & 1);
+                        if (!ok) break;
+                        fence_async_smem();
+                    }
+                    ok = wait(a_full, g & 1);   // P^T is there
                     if (!ok) break;
-                    fence_async_smem();
                     fence_after_sync();
-                    product(0, sK, stage(g + 1));
-                    mma_commit(s_full);
-                }
-                ok = wait(b_full, g & 1);
-                if (!ok) break;
-                fence_after_sync();
-                gradient(dk_col, dp_col, stage(g), g == 0);
-                if (g + 1 < n) {
-                    product(dp_col, sV, stage(g + 1) + kTileBytes);
-                    mma_commit(dp_full(g + 1));
+                    gradient(dv_col, 0, stage(g) + kTileBytes, n == 0);
+                    if (more) {
+                        product(0, sK, stage(g + 1));
+                        mma_commit(s_full);
+                    }
+                    ok = wait(b_full, g & 1);   // dS^T is there
+                    if (!ok) break;
+                    fence_after_sync();
+                    gradient(dk_col, dp_col, stage(g), n == 0);
+                    mma_commit(q_done(g));
+                    if (more) {
+                        product(dp_col, sV, stage(g + 1) + kTileBytes);
+                        mma_commit(dp_full);
+                        if (n + 2 == per_head) mma_commit(kv_empty);
+                    } else {
+                        mma_commit(acc_full);
+                    }
                 }
             }
             mma_commit(done);
             mbar_wait(done, 0);
         }
+        __syncwarp();
     } else {
-        const int row = k0 + tid;
-        const bool valid = row < s.k_len, warp_rows = k0 + warp * 32 < s.k_len;
-        Bias t;
-        t.vec = reinterpret_cast<float*>(extra);
-        t.off = reinterpret_cast<int*>(extra + 4 * ((vec_entries(p.D, kSpan) + 3) & ~3));
-        float* s_lse = reinterpret_cast<float*>(t.off + kChunk);
+        const int half = warp >> 2, r = tid & 127, row = k0 + r;
+        const bool valid = row < s.k_len, warp_rows = k0 + (warp & 3) * 32 < s.k_len;
+        const int64_t t_row = s.k_start + (valid ? row : 0);
+        Bias16 t;
+        t.vec = reinterpret_cast<uint16_t*>(extra);
+        uint8_t* ids = extra + vec16_bytes(p.D, a.span);
+        t.off = reinterpret_cast<int*>(ids + ids_bytes(p.D, a.span));
+        float* s_lse = reinterpret_cast<float*>(t.off + kChunk);   // negated
         float* s_delta = s_lse + kChunk;
         t.kind = s_kind;
-        t.tab = s_tab;
-        bias_rows(t, p, valid ? key_pos(p, s, row) : 0, valid, kSpan, s_red);
-        // One scale for everything that this key sums: the largest |dO| of its queries.
-        int e = 0;
-        if constexpr (kScaled<T>) {
-            int top = kNoExp;
-            const int tiles = (s.q_len + kQTile - 1) / kQTile;
-            for (int i = tid; i < tiles * p.group; i += 128) {
-                const int hh = i / tiles;
-                top = max(top, a.tile_exp[(static_cast<int64_t>(b) * p.H + z * p.group + hh) * a.q_tiles + (i - hh * tiles)]);
-            }
-            top = __reduce_max_sync(0xffffffffu, top);
-            row_barrier();   // bias_rows' extremes are no longer read
-            if (lane == 0) s_red[warp] = top;
-            row_barrier();
-            top = max(max(s_red[0], s_red[1]), max(s_red[2], s_red[3]));
-            e = top == kNoExp ? 0 : top;
-        }
-        const float shift = kScaled<T> ? static_cast<float>(kPExp) : 0.f;
-        const float r = kScaled<T> ? pow2(kSExp - e - kPExp) : 1.f;
-
-        const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        const uint64_t r2 = f2(r, r);
+        const bool has_entry = tid < p.num_buckets;
+        const uint16_t* column = p.table + static_cast<int64_t>(has_entry ? tid : 0) * p.H;
+        uint16_t entry = __ldg(column + z0 * p.group);
+        if (tid == p.num_buckets) s_tab[tid] = 0;
+        bias_rows256(t, p, valid ? key_pos(p, s, row) : 0, valid, a.span, s_red);
+        bias_ids256<-1>(t, p, ids);
+        const uint32_t tmem = start_rows256(&s_tmem);
+        const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         bool ok = true;
         uint32_t g = 0;
-        for (int h = z * p.group; h < (z + 1) * p.group; ++h) {
-            bias_expand<T, -1, false>(t, p, h, nullptr);
-            const float* lse = p.lse + h * p.lse_stride + s.q_start;
-            const float* delta = a.delta + h * p.lse_stride + s.q_start;
-            for (int i0 = 0; i0 < nt; ++i0, ++g) {
-                if (i0 % kChunkTiles == 0) {
-                    if (i0) row_barrier();
-                    const int c0 = i0 * kTile;
-                    bias_columns(t, c0, s.q_len, [&](int c) { return query_pos(p, s, c); });
-                    for (int c = tid; c < kChunk && c0 + c < ((s.q_len + kTile - 1) & ~(kTile - 1)); c += 128) {
-                        const bool in = c0 + c < s.q_len;
-                        s_lse[c] = in ? lse_log2(lse[c0 + c]) - shift : INFINITY;   // no such query: p = 0
-                        s_delta[c] = in ? -delta[c0 + c] * r : 0.f;
-                    }
-                    row_barrier();
-                }
-                const int kind = t.kind[i0 % kChunkTiles], c0 = (i0 % kChunkTiles) * kTile;
-                const int* off = t.off + c0;
-                float x[2][32];
-                ok = ok && wait.warp(s_full, g & 1);
-                if (ok && warp_rows) {
-                    fence_after_sync();
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        tmem_ld32(t_lane + hf * 32, x[hf]);
-                        bias_add(t, kind, off, hf * 32, p.scale_log2, x[hf]);
-                        uint32_t w[16];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 l = *reinterpret_cast<const float4*>(s_lse + c0 + hf * 32 + 4 * i);
-                            float u[4];
-                            f2_split(f2_sub(f2(x[hf][4 * i], x[hf][4 * i + 1]), f2(l.x, l.y)), u[0], u[1]);
-                            f2_split(f2_sub(f2(x[hf][4 * i + 2], x[hf][4 * i + 3]), f2(l.z, l.w)), u[2], u[3]);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) x[hf][4 * i + j] = mma_attn::fast_exp2(u[j]);
-                            w[2 * i] = Cvt<T>::pack(x[hf][4 * i], x[hf][4 * i + 1]);
-                            w[2 * i + 1] = Cvt<T>::pack(x[hf][4 * i + 2], x[hf][4 * i + 3]);
-                        }
-                        tmem_st16_u(t_lane + hf * 16, w);
-                    }
-                    tmem_wait_st();
-                }
-                fence_before_sync();
-                mbar_arrive(a_full);
-                ok = ok && wait.warp(dp_full(g), (g >> 1) & 1);
-                if (ok && warp_rows) {
-                    fence_after_sync();
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        float y[32];
-                        tmem_ld32(t_lane + dp_col + hf * 32, y);
-                        uint32_t w[16];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 d = *reinterpret_cast<const float4*>(s_delta + c0 + hf * 32 + 4 * i);
-                            float u[4];
-                            f2_split(f2_mul(f2(x[hf][4 * i], x[hf][4 * i + 1]), f2_fma(f2(y[4 * i], y[4 * i + 1]), r2, f2(d.x, d.y))), u[0], u[1]);
-                            f2_split(f2_mul(f2(x[hf][4 * i + 2], x[hf][4 * i + 3]), f2_fma(f2(y[4 * i + 2], y[4 * i + 3]), r2, f2(d.z, d.w))), u[2], u[3]);
-                            w[2 * i] = Cvt<T>::pack(u[0], u[1]);
-                            w[2 * i + 1] = Cvt<T>::pack(u[2], u[3]);
-                        }
-                        tmem_st16_u(t_lane + dp_col + hf * 16, w);
-                    }
-                    tmem_wait_st();
-                }
-                fence_before_sync();
-                mbar_arrive(b_full);
-            }
-        }
-        ok = ok && wait.warp(done, 0);
-        if (ok && warp_rows) {
+        const float shift = kScaled<T> ? static_cast<float>(kPExp) : 0.f;
+        // dK and dV of key head z0 + i, half of the columns each (fp32 where the parts are summed up).
+        auto finish = [&](int i, int e) {
+            if (nt > 0) ok = ok && wait.warp(acc_full, i & 1);
+            if (!ok || !warp_rows) return;
             fence_after_sync();
-            const int64_t at = static_cast<int64_t>(s.k_start + (valid ? row : 0)) * a.dkv_tok + z * a.dkv_head;
-            store_tmem_row<T>(t_lane + dk_col, kScaled<T> ? p.scale * pow2(e - kSExp) : p.scale, a.dk + at, valid);
-            store_tmem_row<T>(t_lane + dv_col, kScaled<T> ? pow2(-kPExp) : 1.f, a.dv + at, valid);
+            const float fk = kScaled<T> ? p.scale * pow2(e - kSExp) : p.scale, fv = kScaled<T> ? pow2(-kPExp) : 1.f;
+            const int z = z0 + i;
+            if (a.parts == 1) {
+                const int64_t at = t_row * a.dkv_tok + z * a.dkv_head + half * 32;
+                store_tmem_half<T>(t_lane + dk_col + half * 32, fk, a.dk + at, valid);
+                store_tmem_half<T>(t_lane + dv_col + half * 32, fv, a.dv + at, valid);
+                return;
+            }
+            float* dst = a.part_sums + (((static_cast<int64_t>(part) * p.B + b) * a.part_rows + row) * p.Hkv + z) * 128 + half * 32;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                float v[32];
+                if (nt > 0) tmem_ld32(t_lane + (m ? dv_col : dk_col) + half * 32, v);
+                const float f = m ? fv : fk;
+                if (valid)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        reinterpret_cast<float4*>(dst + m * 64)[c] =
+                            nt > 0 ? make_float4(v[4 * c] * f, v[4 * c + 1] * f, v[4 * c + 2] * f, v[4 * c + 3] * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        };
+        int e_done = 0;
+        for (int i = 0; i < nz; ++i) {
+            const int z = z0 + i;
+            // One scale for everything that a key sums: the largest |dO| of its queries.
+            int e = 0;
+            if constexpr (kScaled<T>) {
+                int top = kNoExp;
+                const int tiles = (s.q_len + kQTile - 1) / kQTile;
+                for (int k = tid; k < tiles * p.group; k += kBwdRows) {
+                    const int hh = k / tiles;
+                    top = max(top, a.tile_exp[(static_cast<int64_t>(b) * p.H + z * p.group + hh) * a.q_tiles + (k - hh * tiles)]);
+                }
+                top = __reduce_max_sync(0xffffffffu, top);
+                rows_barrier();   // s_red's last values are no longer read
+                if (lane == 0) s_red[warp] = top;
+                rows_barrier();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) top = max(top, s_red[k]);
+                e = top == kNoExp ? 0 : top;
+            }
+            const float rs = kScaled<T> ? pow2(kSExp - e - kPExp) : 1.f;
+            const uint64_t r2 = f2(rs, rs);
+            bool first = i > 0;   // the head before is finished when this one's first P is ready
+            for (int h = z * p.group; h < (z + 1) * p.group; ++h) {
+                const float* lse = p.lse + h * p.lse_stride + s.q_start;
+                const float* delta = a.delta + h * p.lse_stride + s.q_start;
+                rows_barrier();   // the last head's table and columns are no longer read
+                if (has_entry) s_tab[tid] = bias_bits<T>(entry);
+                if (has_entry && h + 1 < (z0 + nz) * p.group) entry = __ldg(column + h + 1);
+                rows_barrier();
+                bias_fill256(t, ids, s_tab);
+                for (int tile = 0; tile < nt; ++tile, ++g) {
+                    if (tile % kChunkTiles == 0) {
+                        if (tile) rows_barrier();
+                        const int c0 = (t0 + tile) * kTile;
+                        bias_columns256(t, c0, s.q_len, [&](int c) { return query_pos(p, s, c); });
+#pragma unroll
+                        for (int k = 0; k < kChunk / kBwdRows; ++k) {
+                            const int c = tid + k * kBwdRows;
+                            const bool in = c0 + c < s.q_len;   // no such query: p = 0
+                            s_lse[c] = in ? shift - lse_log2(lse[c0 + c]) : -INFINITY;
+                            s_delta[c] = in ? -delta[c0 + c] * rs : 0.f;
+                        }
+                        rows_barrier();
+                    }
+                    const int kind = t.kind[tile % kChunkTiles], c0 = (tile % kChunkTiles) * kTile;
+                    float x[32];
+                    ok = ok && wait.warp(s_full, g & 1);
+                    if (ok && warp_rows) {
+                        fence_after_sync();
+                        tmem_ld32(t_lane + half * 32, x);
+                        probabilities<T>(t, p, kind, t.off + c0, half * 32, s_lse + c0, 0.f, x);
+                        uint32_t w[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) w[c] = Cvt<T>::pack(x[2 * c], x[2 * c + 1]);
+                        tmem_st16_u(t_lane + half * 32, w);
+                        tmem_wait_st();
+                    }
+                    if (first) {
+                        finish(i - 1, e_done);
+                        first = false;
+                    }
+                    fence_before_sync();
+                    mbar_arrive(a_full);
+                    ok = ok && wait.warp(dp_full, g & 1);
+                    if (ok && warp_rows) {
+                        fence_after_sync();
+                        float y[32];
+                        tmem_ld32(t_lane + dp_col + half * 32, y);
+                        uint32_t w[16];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const float4 d = *reinterpret_cast<const float4*>(s_delta + c0 + half * 32 + 4 * c);
+                            float u, v;
+                            f2_split(f2_mul(f2(x[4 * c], x[4 * c + 1]), f2_fma(f2(y[4 * c], y[4 * c + 1]), r2, f2(d.x, d.y))), u, v);
+                            w[2 * c] = Cvt<T>::pack(u, v);
+                            f2_split(f2_mul(f2(x[4 * c + 2], x[4 * c + 3]), f2_fma(f2(y[4 * c + 2], y[4 * c + 3]), r2, f2(d.z, d.w))), u, v);
+                            w[2 * c + 1] = Cvt<T>::pack(u, v);
+                        }
+                        tmem_st16_u(t_lane + dp_col + half * 32, w);
+                        tmem_wait_st();
+                    }
+                    fence_before_sync();
+                    mbar_arrive(b_full);
+                }
+            }
+            if (nt == 0) finish(i, e);
+            e_done = e;
         }
+        if (nt > 0) finish(nz - 1, e_done);
     }
-    tmem_free(tmem, kTmemCols, warp, &s_fail);
+    finish_cta256(&s_tmem, kTmemCols, warp, &s_fail);
+}
+
+// dK and dV from the parts' sums, in their order.  One thread per 8 values;
+// grid (chunks of a sequence's rows, B).
+template <typename T>
+__global__ void __launch_bounds__(256) bias_bwd_parts_kernel(const Problem p, const BwdArgs a) {
+    const int b = blockIdx.y;
+    Seq s;
+    if (!read_pair(p, b, s) || s.q_len == 0) return;
+    const int64_t n = static_cast<int64_t>(s.k_len) * p.Hkv * 16, step = static_cast<int64_t>(gridDim.x) * 256;
+    const int64_t part_step = static_cast<int64_t>(p.B) * a.part_rows * p.Hkv * 128;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) {
+        const int c = static_cast<int>(i & 15);   // eight values of dK (0-7) or dV
+        const int64_t rz = i >> 4, row = rz / p.Hkv, z = rz - row * p.Hkv;
+        const float* src = a.part_sums + ((b * a.part_rows + row) * p.Hkv + z) * 128 + c * 8;
+        float v[8] = {};
+        for (int k = 0; k < a.parts; ++k) {
+            const float4 x = __ldcs(reinterpret_cast<const float4*>(src + k * part_step)), y = __ldcs(reinterpret_cast<const float4*>(src + k * part_step) + 1);
+            v[0] += x.x;
+            v[1] += x.y;
+            v[2] += x.z;
+            v[3] += x.w;
+            v[4] += y.x;
+            v[5] += y.y;
+            v[6] += y.z;
+            v[7] += y.w;
+        }
+        uint16_t* dst = (c < 8 ? a.dk : a.dv) + (s.k_start + row) * a.dkv_tok + z * a.dkv_head + (c & 7) * 8;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(Cvt<T>::pack(v[0], v[1]), Cvt<T>::pack(v[2], v[3]), Cvt<T>::pack(v[4], v[5]), Cvt<T>::pack(v[6], v[7]));
+    }
 }
 
 // dtable[n, h] = sum of the tiles' sums, in a fixed order.  grid (num_buckets, H)
@@ -598,34 +872,40 @@ __global__ void __launch_bounds__(256) bias_bwd_table_kernel(const Problem p, co
 
 // ---------------------------------------------------------------------------
 // weight[h, j] = prev[h, j] + sum_i exp(s[i, j] - lse_i): key rows, transposed
-// scores, summed along each thread's row.  grid (key tiles, H, B).
+// scores, summed along each thread's row.  grid (key tiles, groups of heads,
+// B), three CTAs per SM; TMEM: two score buffers.
 // ---------------------------------------------------------------------------
 
 constexpr int kWeightStages = 3;
 constexpr uint32_t kWeightTmem = 128;
 
-__host__ __device__ constexpr int weight_smem_bytes(int D) {
-    return 1024 + kRowBytes + kWeightStages * kTileBytes + 4 * ((vec_entries(D, kSpan) + 3) & ~3) + 8 * kChunk;
+__host__ __device__ constexpr int weight_smem_bytes(int D, int span) {
+    return 1024 + kRowBytes + kWeightStages * kTileBytes + 8 * kChunk + vec16_bytes(D, span) + ids_bytes(D, span);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 3)
-    bias_weight_kernel(const Problem p, const float* prev, float* weight, int64_t weight_stride) {
+    bias_weight_kernel(const Problem p, const float* prev, float* weight, int64_t weight_stride, int heads_per_cta, int span) {
     extern __shared__ uint8_t smem_raw[];
-    // k_full, tile_full[3], s_full[3], a_full[2], done
-    __shared__ __align__(8) uint64_t s_bar[10];
-    __shared__ float s_tab[kMaxBuckets];
+    // k_full, k_empty, q_full[3], s_full[3], a_full[2], done
+    constexpr int kBars = 11;
+    __shared__ __align__(8) uint64_t s_bar[kBars];
+    __shared__ uint16_t s_tab[kMaxBuckets];
     __shared__ int s_kind[kChunkTiles], s_red[8];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
 
-    const int k0 = blockIdx.x * kQTile, h = blockIdx.y, b = blockIdx.z;
+    const int k0 = blockIdx.x * kQTile, h0 = blockIdx.y * heads_per_cta, b = blockIdx.z;
+    const int nh = min(heads_per_cta, p.H - h0);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Seq s;
     if (!read_pair(p, b, s) || k0 >= s.k_len) return;
-    const int64_t at = h * weight_stride + s.k_start + k0 + tid;
-    if (s.q_len == 0) {
-        if (tid < kQTile && k0 + tid < s.k_len) weight[at] = prev != nullptr ? prev[at] : 0.f;
+    if (s.q_len == 0) {   // nothing to add
+        for (int i = tid; i < nh * kQTile; i += kThreads) {
+            const int r = k0 + i % kQTile;
+            const int64_t at = (h0 + i / kQTile) * weight_stride + s.k_start + r;
+            if (r < s.k_len) weight[at] = prev != nullptr ? prev[at] : 0.f;
+        }
         return;
     }
     const int nt = (s.q_len + kTile - 1) / kTile;
@@ -635,113 +915,129 @@ __global__ void __launch_bounds__(kThreads, 3)
     const uint32_t sRing = sK + kRowBytes;
     uint8_t* extra = smem_raw + (sRing - raw) + kWeightStages * kTileBytes;
     const uint32_t bar0 = smem_addr(&s_bar[0]);
-    const uint32_t k_full = bar0, done = bar0 + 8u * 9;
-    auto tile_full = [&](uint32_t g) { return bar0 + 8u * (1 + g % 3); };
-    auto s_full = [&](uint32_t g) { return bar0 + 8u * (4 + g % 3); };
-    auto a_full = [&](uint32_t g) { return bar0 + 8u * (7 + (g & 1)); };
-    if (tid == 0) {
-        mbar_init(k_full, 32);
-        for (int i = 0; i < 3; ++i) {
-            mbar_init(tile_full(i), 32);
-            mbar_init(s_full(i), 1);
-        }
-        mbar_init(a_full(0), 128);
-        mbar_init(a_full(1), 128);
-        mbar_init(done, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        s_fail = 0;
-    }
-    const uint32_t tmem = tmem_alloc(&s_tmem, kWeightTmem, warp);
+    const uint32_t k_full = bar0, k_empty = bar0 + 8, done = bar0 + 80;
+    auto q_full = [&](uint32_t g) { return bar0 + 8u * (2 + g % 3); };
+    auto s_full = [&](uint32_t g) { return bar0 + 8u * (5 + g % 3); };
+    auto a_full = [&](uint32_t g) { return bar0 + 8u * (8 + (g & 1)); };
     const Wait wait{&s_fail};
 
     if (warp == kTcLoadWarp) {
-        const uint16_t* qb = p.q + s.q_start * p.q_tok + h * p.q_head;
-        load_rows<kQTile>(sK, p.k + s.k_start * p.kv_tok + (h / p.group) * p.kv_head, p.kv_tok, k0, s.k_len, lane);
-        cp_async_arrive_noinc(k_full);
+        if (lane < kBars) mbar_init(bar0 + 8 * lane, lane == 0 || (lane >= 2 && lane < 5) ? 32 : lane == 8 || lane == 9 ? 128 : 1);
+        if (lane == 0) s_fail = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        __syncwarp();
+        start_loads();
         bool ok = true;
-        for (uint32_t g = 0; g < static_cast<uint32_t>(nt); ++g) {
-            if (g >= kWeightStages) ok = wait.warp(s_full(g), ((g - 3) / 3) & 1);
+        uint32_t g = 0;
+        for (int i = 0; ok && i < nh; ++i) {
+            const int h = h0 + i;
+            if (i > 0) ok = wait.warp(k_empty, (i - 1) & 1);
             if (!ok) break;
-            load_rows<kTile>(sRing + (g % 3) * kTileBytes, qb, p.q_tok, g * kTile, s.q_len, lane);
-            cp_async_arrive_noinc(tile_full(g));
+            load_rows<kQTile>(sK, p.k + s.k_start * p.kv_tok + (h / p.group) * p.kv_head, p.kv_tok, k0, s.k_len, lane);
+            cp_async_arrive_noinc(k_full);
+            const uint16_t* qb = p.q + s.q_start * p.q_tok + h * p.q_head;
+            for (int t = 0; t < nt; ++t, ++g) {
+                if (g >= kWeightStages) ok = wait.warp(s_full(g), (g / 3 - 1) & 1);
+                if (!ok) break;
+                load_rows<kTile>(sRing + (g % 3) * kTileBytes, qb, p.q_tok, t * kTile, s.q_len, lane);
+                cp_async_arrive_noinc(q_full(g));
+            }
         }
         cp_async_wait_all();
     } else if (warp == kTcMmaWarp) {
+        const uint32_t tmem = start_mma(&s_tmem, kWeightTmem);
         if (lane == 0) {
             const uint32_t idesc = make_idesc(Cvt<T>::kFormat, 0, kTile);
-            bool ok = wait(k_full, 0);
-            for (uint32_t g = 0; ok && g < static_cast<uint32_t>(nt); ++g) {
-                ok = wait(tile_full(g), (g / 3) & 1);
-                if (ok && g >= 2) ok = wait(a_full(g), ((g - 2) >> 1) & 1);   // scores of tile g - 2 have been read
-                if (!ok) break;
-                fence_async_smem();
-                fence_after_sync();
+            bool ok = true;
+            uint32_t g = 0;
+            for (int i = 0; ok && i < nh; ++i) {
+                ok = wait(k_full, i & 1);
+                for (int t = 0; ok && t < nt; ++t, ++g) {
+                    ok = wait(q_full(g), (g / 3) & 1);
+                    if (ok && g >= 2) ok = wait(a_full(g), (g / 2 - 1) & 1);   // scores of tile g - 2 have been read
+                    if (!ok) break;
+                    fence_async_smem();
+                    fence_after_sync();
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_f16(tmem + (g & 1) * kTile, make_sdesc(sK + ks * 32), make_sdesc(sRing + (g % 3) * kTileBytes + ks * 32),
-                            idesc, ks > 0);
-                mma_commit(s_full(g));
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_f16(tmem + (g & 1) * kTile, make_sdesc(sK + ks * 32), make_sdesc(sRing + (g % 3) * kTileBytes + ks * 32), idesc, ks > 0);
+                    mma_commit(s_full(g));
+                }
+                mma_commit(k_empty);
             }
             mma_commit(done);
             mbar_wait(done, 0);
         }
+        __syncwarp();
     } else {
         const int row = k0 + tid;
         const bool valid = row < s.k_len, warp_rows = k0 + warp * 32 < s.k_len;
-        Bias t;
-        t.vec = reinterpret_cast<float*>(extra);
-        t.off = reinterpret_cast<int*>(extra + 4 * ((vec_entries(p.D, kSpan) + 3) & ~3));
-        float* s_lse = reinterpret_cast<float*>(t.off + kChunk);
+        Bias16 t;
+        t.vec = reinterpret_cast<uint16_t*>(extra);
+        uint8_t* ids = extra + vec16_bytes(p.D, span);
+        t.off = reinterpret_cast<int*>(ids + ids_bytes(p.D, span));
+        float* s_lse = reinterpret_cast<float*>(t.off + kChunk);   // negated
         t.kind = s_kind;
-        t.tab = s_tab;
-        bias_rows(t, p, valid ? key_pos(p, s, row) : 0, valid, kSpan, s_red);
-        bias_expand<T, -1, false>(t, p, h, nullptr);
-        const float* lse = p.lse + h * p.lse_stride + s.q_start;
+        const bool has_entry = tid < p.num_buckets;
+        const uint16_t* column = p.table + static_cast<int64_t>(has_entry ? tid : 0) * p.H + h0;
+        uint16_t entry = __ldg(column);
+        bias_rows(t, p, 0, valid ? key_pos(p, s, row) : 0, valid, span, s_red);
+        bias_ids<-1>(t, p, ids, tid, 128);
+        const uint32_t tmem = start_rows(&s_tmem);
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        float total = 0.f;
         bool ok = true;
-        for (int g = 0; g < nt; ++g) {
-            if (g % kChunkTiles == 0) {
-                if (g) row_barrier();
-                const int c0 = g * kTile;
-                bias_columns(t, c0, s.q_len, [&](int c) { return query_pos(p, s, c); });
-                for (int c = tid; c < kChunk && c0 + c < ((s.q_len + kTile - 1) & ~(kTile - 1)); c += 128)
-                    s_lse[c] = c0 + c < s.q_len ? lse_log2(lse[c0 + c]) : INFINITY;
-                row_barrier();
-            }
-            const int kind = t.kind[g % kChunkTiles], c0 = (g % kChunkTiles) * kTile;
-            ok = ok && wait.warp(s_full(g), (g / 3) & 1);
-            if (ok && warp_rows) {
-                fence_after_sync();
-                float x[2][32];
-                tmem_ld32(t_lane + (g & 1) * kTile, x[0]);
-                tmem_ld32(t_lane + (g & 1) * kTile + 32, x[1]);
-                fence_before_sync();
-                mbar_arrive(a_full(g));
-                uint64_t sum = f2(0.f, 0.f);
+        uint32_t g = 0;
+        for (int i = 0; i < nh; ++i) {
+            const int h = h0 + i;
+            const float* lse = p.lse + h * p.lse_stride + s.q_start;
+            const int64_t at = h * weight_stride + s.k_start + row;
+            const float old = valid && prev != nullptr ? prev[at] : 0.f;
+            group_barrier(0);   // the last head's table and columns are no longer read
+            if (has_entry) s_tab[tid] = bias_bits<T>(entry);
+            if (i + 1 < nh) entry = __ldg(column + i + 1);
+            group_barrier(0);
+            bias_fill(t, ids, s_tab);
+            float sum_all = 0.f;
+            for (int tile = 0; tile < nt; ++tile, ++g) {
+                if (tile % kChunkTiles == 0) {
+                    if (tile) group_barrier(0);
+                    const int c0 = tile * kTile;
+                    if (i == 0 || nt > kChunkTiles) bias_columns(t, c0, s.q_len, [&](int c) { return query_pos(p, s, c); });
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    bias_add(t, kind, t.off + c0, hf * 32, p.scale_log2, x[hf]);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 l = *reinterpret_cast<const float4*>(s_lse + c0 + hf * 32 + 4 * i);
-                        float u[4];
-                        f2_split(f2_sub(f2(x[hf][4 * i], x[hf][4 * i + 1]), f2(l.x, l.y)), u[0], u[1]);
-                        f2_split(f2_sub(f2(x[hf][4 * i + 2], x[hf][4 * i + 3]), f2(l.z, l.w)), u[2], u[3]);
-                        sum = f2_add(sum, f2(mma_attn::fast_exp2(u[0]), mma_attn::fast_exp2(u[1])));
-                        sum = f2_add(sum, f2(mma_attn::fast_exp2(u[2]), mma_attn::fast_exp2(u[3])));
+                    for (int k = 0; k < kChunk / 128; ++k) {
+                        const int c = tid + k * 128;
+                        if (c0 + c < ((s.q_len + kTile - 1) & ~(kTile - 1))) s_lse[c] = c0 + c < s.q_len ? -lse_log2(lse[c0 + c]) : -INFINITY;
                     }
+                    group_barrier(0);
                 }
-                float a, c;
-                f2_split(sum, a, c);
-                total += a + c;
-            } else {
-                mbar_arrive(a_full(g));
+                const int kind = t.kind[tile % kChunkTiles], c0 = (tile % kChunkTiles) * kTile;
+                ok = ok && wait.warp(s_full(g), (g / 3) & 1);
+                if (ok && warp_rows) {
+                    fence_after_sync();
+                    uint64_t sum = f2(0.f, 0.f);
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        float x[32];
+                        tmem_ld32(t_lane + (g & 1) * kTile + hf * 32, x);
+                        if (hf == 1) {
+                            fence_before_sync();
+                            mbar_arrive(a_full(g));
+                        }
+                        probabilities<T>(t, p, kind, t.off + c0, hf * 32, s_lse + c0, 0.f, x);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) sum = f2_add(sum, f2(x[2 * c], x[2 * c + 1]));
+                    }
+                    float u, v;
+                    f2_split(sum, u, v);
+                    sum_all += u + v;
+                } else {
+                    mbar_arrive(a_full(g));
+                }
             }
+            if (ok && valid) weight[at] = old + sum_all;
         }
-        if (ok && valid) weight[at] = (prev != nullptr ? prev[at] : 0.f) + total;
     }
-    tmem_free(tmem, kWeightTmem, warp, &s_fail);
+    finish_cta(&s_tmem, kWeightTmem, warp, &s_fail);
 }
 
 }  // namespace bias

@@ -55,158 +55,7 @@ enum TileKind { kGeneral = 0, kLeft = 1, kRight = 2, kConsecutive = 3, kClamped 
 
 __host__ __device__ constexpr int vec_entries(int D, int span) { return 2 * (D + span) + 1 + kVecPad; }
 
-// Barrier of the NR row threads.
-template <int NR = 128>
-__device__ __forceinline__ void row_barrier() {
-    asm volatile("bar.sync 1, %0;" ::"n"(NR) : "memory");
-}
-
-// The expanded table and the columns' offsets of one CTA.
-struct Bias {
-    float* vec;
-    int* off;        // [kChunk] byte offsets into vec (kClamped: positions)
-    int* kind;       // [kChunkTiles]
-    float* tab;      // [kMaxBuckets] the head's column of the table, base 2
-    int rmin, R, D, last;   // last: index of the last entry
-    bool near;
-    uint32_t row;    // byte offset of this thread's row into vec
-    int p_row;
-};
-
-// Extremes of the rows' positions over the NR row threads (s_red: 2 ints per
-// warp; a barrier inside).
-template <int NR = 128>
-__device__ __forceinline__ void bias_rows(Bias& t, const Problem& p, int pos, bool valid, int span, int* s_red) {
-    constexpr int W = NR / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int lo = __reduce_min_sync(0xffffffffu, valid ? pos : INT_MAX);
-    const int hi = __reduce_max_sync(0xffffffffu, valid ? pos : INT_MIN);
-    if (lane == 0) {
-        s_red[warp] = lo;
-        s_red[W + warp] = hi;
-    }
-    row_barrier<NR>();
-    int rmax = s_red[W];
-    t.rmin = s_red[0];
-#pragma unroll
-    for (int w = 1; w < W; ++w) {
-        t.rmin = min(t.rmin, s_red[w]);
-        rmax = max(rmax, s_red[W + w]);
-    }
-    const int64_t R = static_cast<int64_t>(rmax) - t.rmin;
-    t.D = p.D;
-    t.near = R <= span;
-    t.R = t.near ? static_cast<int>(R) : 0;
-    t.last = 2 * (t.D + t.R);
-    t.p_row = pos;
-    t.row = valid && t.near ? 4u * static_cast<uint32_t>(t.R - (pos - t.rmin)) : 0u;
-}
-
-// The bucket of every entry of the expanded table (255: none), once per CTA,
-// and a head's entries from it.  SIGN = 1: rows are queries, -1: rows are
-// keys.  NR row threads; no barriers inside.
 constexpr uint8_t kNoBucket = 255;
-template <int SIGN, int NR>
-__device__ __forceinline__ void bias_ids(const Bias& t, const Problem& p, uint8_t* ids) {
-#pragma unroll 4
-    for (int x = threadIdx.x; x <= t.last; x += NR) ids[x] = static_cast<uint8_t>(bucket_of(p, SIGN * (x - t.D - t.R)));
-    for (int x = t.last + 1 + threadIdx.x; x <= t.last + kVecPad; x += NR) ids[x] = kNoBucket;   // past a partial tile's end
-}
-template <int NR>
-__device__ __forceinline__ void bias_fill(const Bias& t, const uint8_t* ids) {
-#pragma unroll 4
-    for (int x = threadIdx.x; x <= t.last + kVecPad; x += NR) {
-        const int b = ids[x];
-        t.vec[x] = b == kNoBucket ? 0.f : t.tab[b];
-    }
-}
-
-// Expands head h's column of the table; SIGN = 1: rows are queries, -1: rows
-// are keys.  IDS: also each entry's row of the gradient accumulator (bytes).
-// All 128 row threads; barriers inside.
-template <typename T, int SIGN, bool IDS>
-__device__ __forceinline__ void bias_expand(const Bias& t, const Problem& p, int h, uint16_t* ids) {
-    const int tid = threadIdx.x;
-    row_barrier();   // the previous head's table is no longer read
-    if (tid < p.num_buckets) t.tab[tid] = bias_log2<T>(__ldg(p.table + static_cast<int64_t>(tid) * p.H + h));
-    row_barrier();
-#pragma unroll 4
-    for (int x = tid; x <= t.last; x += 128) {
-        const int b = bucket_of(p, SIGN * (x - t.D - t.R));
-        t.vec[x] = b < 0 ? 0.f : t.tab[b];
-        if constexpr (IDS) ids[x] = static_cast<uint16_t>((b < 0 ? p.num_buckets : b) * 512);
-    }
-    if (tid < kVecPad) {   // read by the columns past a partial tile's end, which then count as masked
-        t.vec[t.last + 1 + tid] = 0.f;
-        if constexpr (IDS) ids[t.last + 1 + tid] = static_cast<uint16_t>(p.num_buckets * 512);
-    }
-    row_barrier();
-}
-
-// Offsets and tile kinds of columns [c0, c0 + CHUNK) (positions from pos_of).
-// All NR row threads; the caller puts a barrier before and after.
-template <int NR = 128, int CHUNK = kChunk, class PosOf>
-__device__ __forceinline__ void bias_columns(const Bias& t, int c0, int len, PosOf pos_of) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-    for (int k = 0; k < (CHUNK / kTile) / (NR / 32); ++k) {
-        const int tile = warp + k * (NR / 32), c = c0 + tile * kTile + lane;
-        if (c0 + tile * kTile >= len) break;
-        const bool v0 = c < len, v1 = c + 32 < len;
-        const int p0 = v0 ? pos_of(c) : 0, p1 = v1 ? pos_of(c + 32) : 0;
-        const int lo = -t.D, hi = t.R + t.D;
-        auto clamped = [&](int x) {
-            const int64_t d = static_cast<int64_t>(x) - t.rmin;
-            return d < lo ? lo : d > hi ? hi : static_cast<int>(d);
-        };
-        const int o0 = clamped(p0), o1 = clamped(p1);
-        const int first = __shfl_sync(0xffffffffu, o0, 0);   // column 0 of a tile that has any
-        const bool left = __all_sync(0xffffffffu, (!v0 || o0 == lo) && (!v1 || o1 == lo));
-        const bool right = __all_sync(0xffffffffu, (!v0 || o0 == hi) && (!v1 || o1 == hi));
-        const bool run = __all_sync(0xffffffffu, (!v0 || o0 == first + lane) && (!v1 || o1 == first + 32 + lane));
-        int* off = t.off + tile * kTile;
-        if (t.near) {
-            off[lane] = v0 ? 4 * (o0 - lo) : 0;
-            off[lane + 32] = v1 ? 4 * (o1 - lo) : 0;
-        } else {
-            off[lane] = p0;
-            off[lane + 32] = p1;
-        }
-        if (lane == 0) t.kind[tile] = !t.near ? kClamped : left ? kLeft : right ? kRight : run ? kConsecutive : kGeneral;
-    }
-}
-
-// x = x * scale + bias for 32 columns starting at column c of the tile.
-__device__ __forceinline__ void bias_add(const Bias& t, int kind, const int* off, int c, float scale_log2, float (&x)[32]) {
-    const uint64_t sl2 = f2(scale_log2, scale_log2);
-    const char* row = reinterpret_cast<const char*>(t.vec) + t.row;
-    if (kind == kLeft || kind == kRight) {
-        const float e = t.vec[kind == kLeft ? 0 : t.last];
-        const uint64_t b2 = f2(e, e);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f2_split(f2_fma(f2(x[2 * i], x[2 * i + 1]), sl2, b2), x[2 * i], x[2 * i + 1]);
-    } else if (kind == kConsecutive) {
-        const float* e = reinterpret_cast<const float*>(row + off[0]) + c;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            f2_split(f2_fma(f2(x[2 * i], x[2 * i + 1]), sl2, f2(e[2 * i], e[2 * i + 1])), x[2 * i], x[2 * i + 1]);
-    } else if (kind == kGeneral) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int4 o = *reinterpret_cast<const int4*>(off + c + 4 * i);
-            const float e0 = *reinterpret_cast<const float*>(row + o.x), e1 = *reinterpret_cast<const float*>(row + o.y);
-            const float e2 = *reinterpret_cast<const float*>(row + o.z), e3 = *reinterpret_cast<const float*>(row + o.w);
-            f2_split(f2_fma(f2(x[4 * i], x[4 * i + 1]), sl2, f2(e0, e1)), x[4 * i], x[4 * i + 1]);
-            f2_split(f2_fma(f2(x[4 * i + 2], x[4 * i + 3]), sl2, f2(e2, e3)), x[4 * i + 2], x[4 * i + 3]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const int d = max(-t.D, min(t.D, pos_diff(off[c + i], t.p_row)));
-            x[i] = fmaf(x[i], scale_log2, t.vec[d + t.D]);
-        }
-    }
-}
 
 // ROWS rows of one head (base = its row 0), from row0 on, into a swizzled
 // tile, by one warp; rows at or past len are zero-filled without being read.
@@ -258,27 +107,6 @@ struct Wait {
     }
 };
 
-__device__ __forceinline__ uint32_t tmem_alloc(uint32_t* s_tmem, uint32_t cols, int warp) {
-    if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(s_tmem)), "r"(cols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    fence_before_sync();
-    __syncthreads();
-    fence_after_sync();
-    return *s_tmem;
-}
-__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols, int warp, const int* s_fail) {
-    fence_before_sync();
-    __syncthreads();
-    if (*s_fail && threadIdx.x == 0) raise_status(RAGGED_DEV_TIMEOUT);
-    if (warp == 0) {
-        fence_after_sync();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
-    }
-}
-
 // 32 values of a row (packed pairs) to 16-bit global memory.
 __device__ __forceinline__ void store_half_row(uint16_t* dst, const uint32_t (&w)[16]) {
     if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
@@ -309,20 +137,6 @@ __device__ __forceinline__ void store_row(uint16_t* dst, const uint32_t (&w)[32]
             *reinterpret_cast<uint4*>(dst + c * 8) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
     }
 }
-// This thread's 64 fp32 columns at taddr, times f, rounded and stored.
-template <typename T>
-__device__ __forceinline__ void store_tmem_row(uint32_t taddr, float f, uint16_t* dst, bool valid) {
-    uint32_t w[32];
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-        float v[32];
-        tmem_ld32(taddr + hf * 32, v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[hf * 16 + i] = Cvt<T>::pack(v[2 * i] * f, v[2 * i + 1] * f);
-    }
-    if (valid) store_row(dst, w);
-}
-
 // ---------------------------------------------------------------------------
 // The bias of a group of 128 row threads in 16 bits: the entries are the
 // table's own values, so nothing is lost, and 32 rows that spread over 64
