@@ -86,13 +86,13 @@ int64_t bwd_parts(const ragged_bias_attn* a) {
     const int64_t tiles = (avg_q + ragged::bias::kTile - 1) / ragged::bias::kTile;
     return std::max<int64_t>(1, std::min<int64_t>({8, 2LL * sm_count() / ctas, tiles / 4, tiles * (a->H / a->Hkv) / 16}));
 }
-// Workspace of the backward pass: delta [H, lse_stride] floats, an exponent per
+// Workspace of the backward pass: delta [H, lse_stride] floats, four exponents per
 // (sequence, head, query tile), the tiles' sums for the table's gradient
 // [B, H, query tiles, num_buckets], and the parts' sums of dK and dV.
 int64_t bwd_delta_floats(const ragged_bias_attn* a) { return (a->H * a->lse_stride + 3) & ~int64_t(3); }
 int64_t bwd_items(const ragged_bias_attn* a) { return a->B * a->H * tiles128(a->max_seqlen_q); }
 int64_t bwd_small_floats(const ragged_bias_attn* a) {
-    return (bwd_delta_floats(a) + bwd_items(a) * (1 + a->num_buckets) + 3) & ~int64_t(3);
+    return (bwd_delta_floats(a) + bwd_items(a) * (4 + a->num_buckets) + 3) & ~int64_t(3);
 }
 int64_t bwd_workspace(const ragged_bias_attn* a) {
     const int64_t parts = bwd_parts(a);
@@ -105,7 +105,7 @@ int64_t fwd_workspace(const ragged_bias_attn*) { return 0; }
 // buckets, or a far-reaching map): then one CTA.
 constexpr int kTwoPerSm = (228 * 1024) / 2 - 1024 - 3072;   // less the reserved and the static part
 constexpr int bias_span(int D, int fixed, int bytes_per_entry) {
-    const int entries = (kTwoPerSm - fixed - 64) / bytes_per_entry;
+    const int entries = (kTwoPerSm - fixed - 64 - (2 * D + 16)) / bytes_per_entry;
     const int span = (entries - 1 - ragged::bias::kVecPad) / 2 - D;
     return span < 256 ? ragged::bias::kSpan : span < ragged::bias::kSpan ? span : ragged::bias::kSpan;
 }
@@ -395,7 +395,7 @@ ragged_status ragged_attn_bias_bwd(const ragged_bias_attn* a, const void* out, i
     g.dkv_head = a->Hkv > 1 ? dkv_head_stride : 0;
     g.delta = ws;
     g.tile_exp = reinterpret_cast<int*>(ws + bwd_delta_floats(a));
-    g.partial = ws + bwd_delta_floats(a) + bwd_items(a);
+    g.partial = ws + bwd_delta_floats(a) + 4 * bwd_items(a);
     g.dtable = static_cast<uint16_t*>(dtable);
     g.q_tiles = static_cast<int>(tiles128(a->max_seqlen_q));
     g.parts = static_cast<int>(bwd_parts(a));

@@ -47,7 +47,7 @@ struct BwdArgs {
     uint16_t* dv;
     int64_t dq_tok, dq_head, dkv_tok, dkv_head;
     float* delta;     // [H, lse_stride]
-    int* tile_exp;    // [B][H][query tiles]: exponent of the largest |dO|
+    int* tile_exp;    // [B][H][query tiles][4 warps]: exponent of the largest |dO|
     float* partial;   // [B][H][query tiles][num_buckets]
     uint16_t* dtable;
     int q_tiles;
@@ -58,71 +58,6 @@ struct BwdArgs {
     float* part_sums;
     int64_t part_rows;   // key rows per sequence, a multiple of 128
 };
-
-__device__ __forceinline__ void rows_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
-// bias_rows, bias_ids, bias_fill and bias_columns for 256 row threads.  An entry
-// of `ids` without a bucket holds num_buckets, the accumulator's spare row.
-__device__ __forceinline__ void bias_rows256(Bias16& t, const Problem& p, int pos, bool valid, int span, int* s_red) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int lo = __reduce_min_sync(0xffffffffu, valid ? pos : INT_MAX);
-    const int hi = __reduce_max_sync(0xffffffffu, valid ? pos : INT_MIN);
-    if (lane == 0) {
-        s_red[warp] = lo;
-        s_red[8 + warp] = hi;
-    }
-    rows_barrier();
-    t.rmin = min(min(s_red[0], s_red[1]), min(s_red[2], s_red[3]));   // both halves hold the same rows
-    const int rmax = max(max(s_red[8], s_red[9]), max(s_red[10], s_red[11]));
-    const int64_t R = static_cast<int64_t>(rmax) - t.rmin;
-    t.D = p.D;
-    t.near = R <= span;
-    t.R = t.near ? static_cast<int>(R) : 0;
-    t.last = 2 * (t.D + t.R);
-    t.p_row = pos;
-    t.row = valid && t.near ? 2u * static_cast<uint32_t>(t.R - (pos - t.rmin)) : 0u;
-}
-template <int SIGN>
-__device__ __forceinline__ void bias_ids256(const Bias16& t, const Problem& p, uint8_t* ids) {
-#pragma unroll 4
-    for (int x = threadIdx.x; x <= t.last; x += kBwdRows) {
-        const int b = bucket_of(p, SIGN * (x - t.D - t.R));
-        ids[x] = static_cast<uint8_t>(b < 0 ? p.num_buckets : b);
-    }
-    for (int x = t.last + 1 + threadIdx.x; x <= t.last + kVecPad; x += kBwdRows) ids[x] = static_cast<uint8_t>(p.num_buckets);
-}
-// tab[num_buckets] is 0.
-__device__ __forceinline__ void bias_fill256(const Bias16& t, const uint8_t* ids, const uint16_t* tab) {
-#pragma unroll 4
-    for (int x = threadIdx.x; x <= t.last + kVecPad; x += kBwdRows) t.vec[x] = tab[ids[x]];
-}
-template <class PosOf>
-__device__ __forceinline__ void bias_columns256(const Bias16& t, int c0, int len, PosOf pos_of) {
-    const int tile = threadIdx.x >> 5, lane = threadIdx.x & 31, c = c0 + tile * kTile + lane;   // one tile per warp
-    static_assert(kChunkTiles == 8, "eight row warps");
-    if (c0 + tile * kTile >= len) return;
-    const bool v0 = c < len, v1 = c + 32 < len;
-    const int p0 = v0 ? pos_of(c) : 0, p1 = v1 ? pos_of(c + 32) : 0;
-    const int lo = -t.D, hi = t.R + t.D;
-    auto clamped = [&](int x) {
-        const int64_t d = static_cast<int64_t>(x) - t.rmin;
-        return d < lo ? lo : d > hi ? hi : static_cast<int>(d);
-    };
-    const int o0 = clamped(p0), o1 = clamped(p1);
-    const int first = __shfl_sync(0xffffffffu, o0, 0);
-    const bool left = __all_sync(0xffffffffu, (!v0 || o0 == lo) && (!v1 || o1 == lo));
-    const bool right = __all_sync(0xffffffffu, (!v0 || o0 == hi) && (!v1 || o1 == hi));
-    const bool run = __all_sync(0xffffffffu, (!v0 || o0 == first + lane) && (!v1 || o1 == first + 32 + lane));
-    int* off = t.off + tile * kTile;
-    if (t.near) {
-        off[lane] = v0 ? 2 * (o0 - lo) : 0;
-        off[lane + 32] = v1 ? 2 * (o1 - lo) : 0;
-    } else {
-        off[lane] = p0;
-        off[lane + 32] = p1;
-    }
-    if (lane == 0) t.kind[tile] = !t.near ? kClamped : left ? kLeft : right ? kRight : run ? kConsecutive : kGeneral;
-}
 
 __device__ __forceinline__ uint32_t start_rows256(const uint32_t* s_tmem) {
     asm volatile("bar.sync 3, 288;" ::: "memory");
@@ -215,7 +150,8 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
     __shared__ __align__(8) uint64_t s_bar[kBars];
     __shared__ uint16_t s_tab[kMaxBuckets + 1];
     __shared__ float s_delta[2][kQTile], s_undo[kQTile];
-    __shared__ int s_kind[kChunkTiles], s_red[16], s_exp[2][kQTile];
+    __shared__ __align__(16) TileInfo s_tiles[kChunkTiles];
+    __shared__ int s_red[16], s_exp[2][kQTile];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
 
@@ -332,14 +268,40 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
         t.vec = reinterpret_cast<uint16_t*>(extra);
         uint8_t* ids = extra + vec16_bytes(p.D, a.span);
         t.off = reinterpret_cast<int*>(ids + ids_bytes(p.D, a.span));
-        t.kind = s_kind;
+        t.tiles = s_tiles;
+        uint8_t* map = ids + ((vec_entries(p.D, a.span) + 15) & ~15);
         const bool has_entry = tid < p.num_buckets;
         const uint16_t* column = p.table + static_cast<int64_t>(has_entry ? tid : 0) * p.H + h0;
+        // What the set-up needs of global memory, all under way at once.
         uint16_t entry = __ldg(column);
+        const int pos = valid ? query_pos(p, s, row) : 0;
+        auto key_at = [&](int c) { return key_pos(p, s, c); };
+        Columns<kBwdRows> cols;
+        cols.load(0, s.k_len, key_at);
+        // This thread's halves of a head's rows of Q, dO and O, and the row's lse.
+        uint4 qw[4], dw[4], ow[4];
+        float lse = -INFINITY;
+        auto load_row = [&](int h) {
+            const uint4* qp = reinterpret_cast<const uint4*>(p.q + t_row * p.q_tok + h * p.q_head) + half * 4;
+            const uint4* dp = reinterpret_cast<const uint4*>(a.dout + t_row * a.dout_tok + h * 64) + half * 4;
+            const uint4* op = reinterpret_cast<const uint4*>(a.out + t_row * a.out_tok + h * 64) + half * 4;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                qw[c] = valid ? __ldg(qp + c) : make_uint4(0, 0, 0, 0);
+                dw[c] = valid ? __ldg(dp + c) : make_uint4(0, 0, 0, 0);
+                ow[c] = valid ? __ldg(op + c) : make_uint4(0, 0, 0, 0);
+            }
+            if (valid) lse = p.lse[h * p.lse_stride + t_row];
+        };
+        load_row(h0);
+        bias_map<kBwdRows>(p, map, p.num_buckets);
+        if (has_entry) s_tab[tid] = bias_bits<T>(entry);
         if (tid == p.num_buckets) s_tab[tid] = 0;
-        bias_rows256(t, p, valid ? query_pos(p, s, row) : 0, valid, a.span, s_red);
-        bias_ids256<1>(t, p, ids);
-        bias_columns256(t, 0, s.k_len, [&](int c) { return key_pos(p, s, c); });
+        for (int n = 0; n <= p.num_buckets; ++n) acc[n * kBwdRows + tid] = 0.f;
+        bias_rows<kBwdRows>(t, p, pos, valid, a.span, s_red);
+        bias_ids<1, kBwdRows>(t, map, ids, p.num_buckets);
+        cols.store(t, 0, s.k_len);
+        rows_barrier<kBwdRows>();
         const uint32_t tmem = start_rows256(&s_tmem);
         const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         char* acc_row = reinterpret_cast<char*>(acc + tid);
@@ -347,89 +309,75 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
         bool ok = true;
         uint32_t g = 0;
         float undo = 1.f, far_left = 0.f, far_right = 0.f;
-        // End of head h: dQ, and the table's sums of its tile.
-        auto finish = [&](int i) {
-            ok = ok && wait.warp(dq_full, i & 1);
-            if (ok && warp_rows) {
-                fence_after_sync();
-                store_tmem_half<T>(t_lane + dq_col + half * 32, p.scale * undo, a.dq + t_row * a.dq_tok + (h0 + i) * a.dq_head + half * 32, valid);
-            }
-            *reinterpret_cast<float*>(acc_row + ids[0] * (4 * kBwdRows)) += far_left;
-            *reinterpret_cast<float*>(acc_row + ids[t.last] * (4 * kBwdRows)) += far_right;
-            if (half == 0) s_undo[r] = valid ? undo : 0.f;
-            rows_barrier();
-            for (int n = warp; n < p.num_buckets; n += 8) {   // each thread's sums, unscaled, in a fixed order
-                float sum = 0.f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int u = lane + 32 * k;
-                    sum += q0 + (u & 127) < s.q_len ? acc[n * kBwdRows + u] * s_undo[u & 127] : 0.f;
+        // From head i to the next: the table's sums of head i, its dQ once its last product has
+        // finished, and the next head's bias and rows.
+        auto change = [&](int i, bool more) {
+            if (i >= 0) {
+                *reinterpret_cast<float*>(acc_row + ids[0] * (4 * kBwdRows)) += far_left;
+                *reinterpret_cast<float*>(acc_row + ids[t.last] * (4 * kBwdRows)) += far_right;
+                if (half == 0) s_undo[r] = valid ? undo : 0.f;
+                if (more) {
+                    load_row(h0 + i + 1);
+                    if (has_entry) s_tab[tid] = bias_bits<T>(__ldg(column + i + 1));
                 }
+                rows_barrier<kBwdRows>();   // sums complete, the last head's entries no longer read
+                for (int n = warp; n < p.num_buckets; n += 8) {   // each thread's sums, unscaled, in a fixed order
+                    float sum = 0.f;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (lane == 0) a.partial[(item0 + static_cast<int64_t>(i) * a.q_tiles) * p.num_buckets + n] = sum;
+                    for (int k = 0; k < 8; ++k) {
+                        const int u = lane + 32 * k;
+                        sum += q0 + (u & 127) < s.q_len ? acc[n * kBwdRows + u] * s_undo[u & 127] : 0.f;
+                        acc[n * kBwdRows + u] = 0.f;
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (lane == 0) a.partial[(item0 + static_cast<int64_t>(i) * a.q_tiles) * p.num_buckets + n] = sum;
+                }
             }
-            rows_barrier();
+            if (more) bias_fill<kBwdRows>(t, ids, s_tab);
+            if (i >= 0) {
+                ok = ok && wait.warp(dq_full, i & 1);
+                if (ok && warp_rows) {
+                    fence_after_sync();
+                    store_tmem_half<T>(t_lane + dq_col + half * 32, p.scale * undo, a.dq + t_row * a.dq_tok + (h0 + i) * a.dq_head + half * 32, valid);
+                }
+            }
+            if (!more) return;
+            // Q and dO to TMEM: every product of the head before has finished.
+            uint32_t w[16];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                w[4 * c] = qw[c].x;
+                w[4 * c + 1] = qw[c].y;
+                w[4 * c + 2] = qw[c].z;
+                w[4 * c + 3] = qw[c].w;
+            }
+            tmem_st16_u(t_lane + q_col + half * 16, w);
+            float d = 0.f, big = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t ys[4] = {dw[c].x, dw[c].y, dw[c].z, dw[c].w}, xs[4] = {ow[c].x, ow[c].y, ow[c].z, ow[c].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    w[4 * c + k] = ys[k];
+                    const float d0 = to_float<T>(static_cast<uint16_t>(ys[k])), d1 = to_float<T>(static_cast<uint16_t>(ys[k] >> 16));
+                    d = fmaf(to_float<T>(static_cast<uint16_t>(xs[k])), d0, d);
+                    d = fmaf(to_float<T>(static_cast<uint16_t>(xs[k] >> 16)), d1, d);
+                    if constexpr (kScaled<T>) big = fmaxf(big, fmaxf(fabsf(d0), fabsf(d1)));
+                }
+            }
+            tmem_st16_u(t_lane + do_col + half * 16, w);
+            tmem_wait_st();
+            fence_before_sync();
+            mbar_arrive(qd_full);
+            s_delta[half][r] = d;
+            if constexpr (kScaled<T>) s_exp[half][r] = big > 0.f && big < INFINITY ? ilogbf(big) + 1 : kNoExp;
+            rows_barrier<kBwdRows>();   // entries, deltas and cleared sums are there
         };
+        change(-1, true);
         for (int i = 0; i < nh; ++i) {
             const int h = h0 + i;
-            // This thread's halves of the rows of Q, dO and O: delta, the exponent of the largest |dO|.
-            uint4 qw[4], dw[4];
-            float delta = 0.f, big = 0.f;
-            {
-                const uint4* qp = reinterpret_cast<const uint4*>(p.q + t_row * p.q_tok + h * p.q_head) + half * 4;
-                const uint4* dp = reinterpret_cast<const uint4*>(a.dout + t_row * a.dout_tok + h * 64) + half * 4;
-                const uint4* op = reinterpret_cast<const uint4*>(a.out + t_row * a.out_tok + h * 64) + half * 4;
-                uint4 ow[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    qw[c] = valid ? __ldg(qp + c) : make_uint4(0, 0, 0, 0);
-                    dw[c] = valid ? __ldg(dp + c) : make_uint4(0, 0, 0, 0);
-                    ow[c] = valid ? __ldg(op + c) : make_uint4(0, 0, 0, 0);
-                }
-                if (i > 0) finish(i - 1);   // its loads are on their way meanwhile
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t ys[4] = {dw[c].x, dw[c].y, dw[c].z, dw[c].w}, xs[4] = {ow[c].x, ow[c].y, ow[c].z, ow[c].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float d0 = to_float<T>(static_cast<uint16_t>(ys[k])), d1 = to_float<T>(static_cast<uint16_t>(ys[k] >> 16));
-                        delta = fmaf(to_float<T>(static_cast<uint16_t>(xs[k])), d0, delta);
-                        delta = fmaf(to_float<T>(static_cast<uint16_t>(xs[k] >> 16)), d1, delta);
-                        if constexpr (kScaled<T>) big = fmaxf(big, fmaxf(fabsf(d0), fabsf(d1)));
-                    }
-                }
-            }
-            {   // Q and dO to TMEM: every product of the head before has finished
-                uint32_t w[16];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    w[4 * c] = qw[c].x;
-                    w[4 * c + 1] = qw[c].y;
-                    w[4 * c + 2] = qw[c].z;
-                    w[4 * c + 3] = qw[c].w;
-                }
-                tmem_st16_u(t_lane + q_col + half * 16, w);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    w[4 * c] = dw[c].x;
-                    w[4 * c + 1] = dw[c].y;
-                    w[4 * c + 2] = dw[c].z;
-                    w[4 * c + 3] = dw[c].w;
-                }
-                tmem_st16_u(t_lane + do_col + half * 16, w);
-                tmem_wait_st();
-                fence_before_sync();
-                mbar_arrive(qd_full);
-            }
-            s_delta[half][r] = delta;
-            if constexpr (kScaled<T>) s_exp[half][r] = big > 0.f && big < INFINITY ? ilogbf(big) + 1 : kNoExp;
-            for (int n = 0; n <= p.num_buckets; ++n) acc[n * kBwdRows + tid] = 0.f;
-            if (has_entry) s_tab[tid] = bias_bits<T>(entry);
-            rows_barrier();
-            bias_fill256(t, ids, s_tab);
-            if (i + 1 < nh) entry = __ldg(column + i + 1);
-            delta = s_delta[0][r] + s_delta[1][r];
+            const float delta = s_delta[0][r] + s_delta[1][r];
             if (half == 0 && valid) a.delta[h * p.lse_stride + t_row] = delta;
             float rs = 1.f;   // dS is kept times rs
             undo = 1.f;
@@ -439,26 +387,22 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                     rs = pow2(kSExp - e);
                     undo = pow2(e - kSExp);
                 }
-                if (half == 0) {
-                    const int top = __reduce_max_sync(0xffffffffu, e);
-                    if (lane == 0) s_red[warp] = top;
-                }
+                const int top = __reduce_max_sync(0xffffffffu, e);
+                if (half == 0 && lane == 0) a.tile_exp[(item0 + static_cast<int64_t>(i) * a.q_tiles) * 4 + warp] = top;
             }
-            const float nl = valid ? -lse_log2(p.lse[h * p.lse_stride + t_row]) : -INFINITY;
+            const float nl = valid ? -lse_log2(lse) : -INFINITY;
             const uint64_t r2 = f2(rs, rs), nd2 = f2(-delta * rs, -delta * rs);
             far_left = far_right = 0.f;
-            rows_barrier();
-            if constexpr (kScaled<T>)
-                if (tid == 0) a.tile_exp[item0 + static_cast<int64_t>(i) * a.q_tiles] = max(max(s_red[0], s_red[1]), max(s_red[2], s_red[3]));
             for (int tile = 0; tile < nt; ++tile, ++g) {
                 if (tile % kChunkTiles == 0 && (tile > 0 || (i > 0 && nt > kChunkTiles))) {
-                    if (tile > 0) rows_barrier();
-                    bias_columns256(t, tile * kTile, s.k_len, [&](int c) { return key_pos(p, s, c); });
-                    rows_barrier();
+                    cols.load(tile * kTile, s.k_len, key_at);
+                    if (tile > 0) rows_barrier<kBwdRows>();
+                    cols.store(t, tile * kTile, s.k_len);
+                    rows_barrier<kBwdRows>();
                 }
-                const int kind = t.kind[tile % kChunkTiles];
+                const int kind = tile_kind(t, tile % kChunkTiles);
                 const int* off = t.off + (tile % kChunkTiles) * kTile;
-                const int cols = s.k_len - tile * kTile - half * 32;
+                const int left = s.k_len - tile * kTile - half * 32;   // columns of this half
                 float x[32];
                 ok = ok && wait.warp(s_full, g & 1);
                 if (ok && warp_rows) {
@@ -469,10 +413,10 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                 mbar_arrive(a_full);
                 if (ok && warp_rows) {
                     probabilities<T>(t, p, kind, off, half * 32, nullptr, nl, x);
-                    if (cols < 32) {
+                    if (left < 32) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
-                            if (c >= cols) x[c] = 0.f;
+                            if (c >= left) x[c] = 0.f;
                     }
                 }
                 ok = ok && wait.warp(dp_full, g & 1);
@@ -528,8 +472,8 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                     }
                 }
             }
+            change(i, i + 1 < nh);
         }
-        finish(nh - 1);
     }
     finish_cta256(&s_tmem, kTmemCols, warp, &s_fail);
 }
@@ -551,7 +495,8 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
     constexpr int kBars = 14;
     __shared__ __align__(8) uint64_t s_bar[kBars];
     __shared__ uint16_t s_tab[kMaxBuckets + 1];
-    __shared__ int s_kind[kChunkTiles], s_red[16];
+    __shared__ __align__(16) TileInfo s_tiles[kChunkTiles];
+    __shared__ int s_red[16];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
 
@@ -687,13 +632,22 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
         t.off = reinterpret_cast<int*>(ids + ids_bytes(p.D, a.span));
         float* s_lse = reinterpret_cast<float*>(t.off + kChunk);   // negated
         float* s_delta = s_lse + kChunk;
-        t.kind = s_kind;
+        t.tiles = s_tiles;
+        uint8_t* map = ids + ((vec_entries(p.D, a.span) + 15) & ~15);
         const bool has_entry = tid < p.num_buckets;
         const uint16_t* column = p.table + static_cast<int64_t>(has_entry ? tid : 0) * p.H;
-        uint16_t entry = __ldg(column + z0 * p.group);
+        // What the set-up needs of global memory, all under way at once.
+        const uint16_t entry = __ldg(column + z0 * p.group);
+        const int pos = valid ? key_pos(p, s, row) : 0;
+        auto query_at = [&](int c) { return query_pos(p, s, c); };
+        Columns<kBwdRows> cols;
+        cols.load(t0 * kTile, s.q_len, query_at);
+        bias_map<kBwdRows>(p, map, p.num_buckets);
+        if (has_entry) s_tab[tid] = bias_bits<T>(entry);
         if (tid == p.num_buckets) s_tab[tid] = 0;
-        bias_rows256(t, p, valid ? key_pos(p, s, row) : 0, valid, a.span, s_red);
-        bias_ids256<-1>(t, p, ids);
+        bias_rows<kBwdRows>(t, p, pos, valid, a.span, s_red);
+        bias_ids<-1, kBwdRows>(t, map, ids, p.num_buckets);
+        cols.store(t, t0 * kTile, s.q_len);
         const uint32_t tmem = start_rows256(&s_tmem);
         const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         bool ok = true;
@@ -732,15 +686,15 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
             int e = 0;
             if constexpr (kScaled<T>) {
                 int top = kNoExp;
-                const int tiles = (s.q_len + kQTile - 1) / kQTile;
-                for (int k = tid; k < tiles * p.group; k += kBwdRows) {
-                    const int hh = k / tiles;
-                    top = max(top, a.tile_exp[(static_cast<int64_t>(b) * p.H + z * p.group + hh) * a.q_tiles + (k - hh * tiles)]);
+                const int n = (s.q_len + kQTile - 1) / kQTile * 4;   // warps of queries per head
+                for (int k = tid; k < n * p.group; k += kBwdRows) {
+                    const int hh = k / n;
+                    top = max(top, a.tile_exp[(static_cast<int64_t>(b) * p.H + z * p.group + hh) * a.q_tiles * 4 + (k - hh * n)]);
                 }
                 top = __reduce_max_sync(0xffffffffu, top);
-                rows_barrier();   // s_red's last values are no longer read
+                rows_barrier<kBwdRows>();   // s_red's last values are no longer read
                 if (lane == 0) s_red[warp] = top;
-                rows_barrier();
+                rows_barrier<kBwdRows>();
 #pragma unroll
                 for (int k = 0; k < 8; ++k) top = max(top, s_red[k]);
                 e = top == kNoExp ? 0 : top;
@@ -751,26 +705,46 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
             for (int h = z * p.group; h < (z + 1) * p.group; ++h) {
                 const float* lse = p.lse + h * p.lse_stride + s.q_start;
                 const float* delta = a.delta + h * p.lse_stride + s.q_start;
-                rows_barrier();   // the last head's table and columns are no longer read
-                if (has_entry) s_tab[tid] = bias_bits<T>(entry);
-                if (has_entry && h + 1 < (z0 + nz) * p.group) entry = __ldg(column + h + 1);
-                rows_barrier();
-                bias_fill256(t, ids, s_tab);
+                // lse and delta of the first columns are on their way under the barriers and the fill.
+                float l_next[kChunk / kBwdRows], d_next[kChunk / kBwdRows];
+                auto load_stats = [&](int c0) {
+#pragma unroll
+                    for (int k = 0; k < kChunk / kBwdRows; ++k) {
+                        const int c = c0 + tid + k * kBwdRows;
+                        l_next[k] = c < s.q_len ? lse[c] : 0.f;
+                        d_next[k] = c < s.q_len ? delta[c] : 0.f;
+                    }
+                };
+                auto store_stats = [&](int c0) {
+#pragma unroll
+                    for (int k = 0; k < kChunk / kBwdRows; ++k) {
+                        const int c = tid + k * kBwdRows;
+                        const bool in = c0 + c < s.q_len;   // no such query: p = 0
+                        s_lse[c] = in ? shift - lse_log2(l_next[k]) : -INFINITY;
+                        s_delta[c] = in ? -d_next[k] * rs : 0.f;
+                    }
+                };
+                load_stats(t0 * kTile);
+                const bool start = h == z0 * p.group;   // the first head's entries are in s_tab, its columns stored
+                const uint16_t next = start ? uint16_t(0) : __ldg(column + h);
+                rows_barrier<kBwdRows>();   // the last head's entries and columns are no longer read
+                if (!start) {
+                    if (has_entry) s_tab[tid] = bias_bits<T>(next);
+                    rows_barrier<kBwdRows>();
+                }
+                bias_fill<kBwdRows>(t, ids, s_tab);
                 for (int tile = 0; tile < nt; ++tile, ++g) {
                     if (tile % kChunkTiles == 0) {
-                        if (tile) rows_barrier();
                         const int c0 = (t0 + tile) * kTile;
-                        bias_columns256(t, c0, s.q_len, [&](int c) { return query_pos(p, s, c); });
-#pragma unroll
-                        for (int k = 0; k < kChunk / kBwdRows; ++k) {
-                            const int c = tid + k * kBwdRows;
-                            const bool in = c0 + c < s.q_len;   // no such query: p = 0
-                            s_lse[c] = in ? shift - lse_log2(lse[c0 + c]) : -INFINITY;
-                            s_delta[c] = in ? -delta[c0 + c] * rs : 0.f;
-                        }
-                        rows_barrier();
+                        const bool again = nt > kChunkTiles && (tile > 0 || !start);
+                        if (tile > 0) load_stats(c0);
+                        if (again) cols.load(c0, s.q_len, query_at);
+                        if (tile > 0) rows_barrier<kBwdRows>();
+                        if (again) cols.store(t, c0, s.q_len);
+                        store_stats(c0);
+                        rows_barrier<kBwdRows>();
                     }
-                    const int kind = t.kind[tile % kChunkTiles], c0 = (tile % kChunkTiles) * kTile;
+                    const int kind = tile_kind(t, tile % kChunkTiles), c0 = (tile % kChunkTiles) * kTile;
                     float x[32];
                     ok = ok && wait.warp(s_full, g & 1);
                     if (ok && warp_rows) {
@@ -890,8 +864,9 @@ __global__ void __launch_bounds__(kThreads, 3)
     // k_full, k_empty, q_full[3], s_full[3], a_full[2], done
     constexpr int kBars = 11;
     __shared__ __align__(8) uint64_t s_bar[kBars];
-    __shared__ uint16_t s_tab[kMaxBuckets];
-    __shared__ int s_kind[kChunkTiles], s_red[8];
+    __shared__ uint16_t s_tab[kMaxBuckets + 1];
+    __shared__ __align__(16) TileInfo s_tiles[kChunkTiles];
+    __shared__ int s_red[8];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
 
@@ -977,12 +952,22 @@ __global__ void __launch_bounds__(kThreads, 3)
         uint8_t* ids = extra + vec16_bytes(p.D, span);
         t.off = reinterpret_cast<int*>(ids + ids_bytes(p.D, span));
         float* s_lse = reinterpret_cast<float*>(t.off + kChunk);   // negated
-        t.kind = s_kind;
+        t.tiles = s_tiles;
+        uint8_t* map = ids + ((vec_entries(p.D, span) + 15) & ~15);
         const bool has_entry = tid < p.num_buckets;
         const uint16_t* column = p.table + static_cast<int64_t>(has_entry ? tid : 0) * p.H + h0;
-        uint16_t entry = __ldg(column);
-        bias_rows(t, p, 0, valid ? key_pos(p, s, row) : 0, valid, span, s_red);
-        bias_ids<-1>(t, p, ids, tid, 128);
+        // What the set-up needs of global memory, all under way at once.
+        const uint16_t entry = __ldg(column);
+        const int pos = valid ? key_pos(p, s, row) : 0;
+        auto query_at = [&](int c) { return query_pos(p, s, c); };
+        Columns<128> cols;
+        cols.load(0, s.q_len, query_at);
+        bias_map<128>(p, map, p.num_buckets);
+        if (has_entry) s_tab[tid] = bias_bits<T>(entry);
+        if (tid == p.num_buckets) s_tab[tid] = 0;
+        bias_rows<128>(t, p, pos, valid, span, s_red);
+        bias_ids<-1, 128>(t, map, ids, p.num_buckets);
+        cols.store(t, 0, s.q_len);
         const uint32_t tmem = start_rows(&s_tmem);
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         bool ok = true;
@@ -992,25 +977,36 @@ __global__ void __launch_bounds__(kThreads, 3)
             const float* lse = p.lse + h * p.lse_stride + s.q_start;
             const int64_t at = h * weight_stride + s.k_start + row;
             const float old = valid && prev != nullptr ? prev[at] : 0.f;
-            group_barrier(0);   // the last head's table and columns are no longer read
-            if (has_entry) s_tab[tid] = bias_bits<T>(entry);
-            if (i + 1 < nh) entry = __ldg(column + i + 1);
-            group_barrier(0);
-            bias_fill(t, ids, s_tab);
+            float l_next[kChunk / 128];   // on their way under the barriers and the fill
+            auto load_lse = [&](int c0) {
+#pragma unroll
+                for (int k = 0; k < kChunk / 128; ++k) l_next[k] = c0 + tid + k * 128 < s.q_len ? lse[c0 + tid + k * 128] : 0.f;
+            };
+            load_lse(0);
+            const uint16_t next = i == 0 ? uint16_t(0) : __ldg(column + i);
+            rows_barrier<128>();   // the last head's entries and columns are no longer read
+            if (i > 0) {
+                if (has_entry) s_tab[tid] = bias_bits<T>(next);
+                rows_barrier<128>();
+            }
+            bias_fill<128>(t, ids, s_tab);
             float sum_all = 0.f;
             for (int tile = 0; tile < nt; ++tile, ++g) {
                 if (tile % kChunkTiles == 0) {
-                    if (tile) group_barrier(0);
                     const int c0 = tile * kTile;
-                    if (i == 0 || nt > kChunkTiles) bias_columns(t, c0, s.q_len, [&](int c) { return query_pos(p, s, c); });
+                    const bool again = nt > kChunkTiles && (tile > 0 || i > 0);
+                    if (tile > 0) load_lse(c0);
+                    if (again) cols.load(c0, s.q_len, query_at);
+                    if (tile > 0) rows_barrier<128>();
+                    if (again) cols.store(t, c0, s.q_len);
 #pragma unroll
                     for (int k = 0; k < kChunk / 128; ++k) {
                         const int c = tid + k * 128;
-                        if (c0 + c < ((s.q_len + kTile - 1) & ~(kTile - 1))) s_lse[c] = c0 + c < s.q_len ? -lse_log2(lse[c0 + c]) : -INFINITY;
+                        s_lse[c] = c0 + c < s.q_len ? -lse_log2(l_next[k]) : -INFINITY;
                     }
-                    group_barrier(0);
+                    rows_barrier<128>();
                 }
-                const int kind = t.kind[tile % kChunkTiles], c0 = (tile % kChunkTiles) * kTile;
+                const int kind = tile_kind(t, tile % kChunkTiles), c0 = (tile % kChunkTiles) * kTile;
                 ok = ok && wait.warp(s_full(g), (g / 3) & 1);
                 if (ok && warp_rows) {
                     fence_after_sync();

@@ -55,8 +55,6 @@ enum TileKind { kGeneral = 0, kLeft = 1, kRight = 2, kConsecutive = 3, kClamped 
 
 __host__ __device__ constexpr int vec_entries(int D, int span) { return 2 * (D + span) + 1 + kVecPad; }
 
-constexpr uint8_t kNoBucket = 255;
-
 // ROWS rows of one head (base = its row 0), from row0 on, into a swizzled
 // tile, by one warp; rows at or past len are zero-filled without being read.
 template <int ROWS>
@@ -157,31 +155,54 @@ __device__ __forceinline__ uint16_t bias_bits(uint16_t x) {
     return x;
 }
 
+// What a tile of columns is for the rows of one warp.
+struct TileInfo {
+    int lo, hi;   // extremes of the columns' positions
+    int kind;     // kConsecutive, kGeneral or kClamped
+    int unused;
+};
+
 struct Bias16 {
-    uint16_t* vec;   // [2 (D + span) + 1 + pad], one head's entries
-    int* off;        // [kChunk] byte offsets into vec (kClamped: positions)
-    int* kind;       // [kChunkTiles]
+    uint16_t* vec;    // [2 (D + span) + 1 + pad], one head's entries
+    int* off;         // [kChunk] byte offsets into vec (kClamped: positions)
+    TileInfo* tiles;  // [kChunkTiles]
     int rmin, R, D, last;
+    int wlo, whi;     // extremes of the positions of this warp's rows
     bool near;
-    uint32_t row;    // byte offset of this thread's row
+    uint32_t row;     // byte offset of this thread's row
     int p_row;
 };
 
-// Barrier of one group's 128 row threads (w: the group).
-__device__ __forceinline__ void group_barrier(int w) { asm volatile("bar.sync %0, 128;" ::"r"(w + 1) : "memory"); }
+// Barrier of the NR (128 or 256) row threads.
+template <int NR>
+__device__ __forceinline__ void rows_barrier() {
+    asm volatile("bar.sync 1, %0;" ::"n"(NR) : "memory");
+}
 
-// Extremes of the group's row positions (s_red: 8 ints; a barrier inside).
-__device__ __forceinline__ void bias_rows(Bias16& t, const Problem& p, int w, int pos, bool valid, int span, int* s_red) {
-    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-    const int lo = __reduce_min_sync(0xffffffffu, valid ? pos : INT_MAX);
-    const int hi = __reduce_max_sync(0xffffffffu, valid ? pos : INT_MIN);
-    if (lane == 0) {
-        s_red[warp] = lo;
-        s_red[4 + warp] = hi;
+// The bucket map as bytes in shared memory (none: an entry outside the table).
+template <int NR>
+__device__ __forceinline__ void bias_map(const Problem& p, uint8_t* map, int none) {
+#pragma unroll 2
+    for (int x = threadIdx.x; x <= 2 * p.D; x += NR) {
+        const int b = bucket_of(p, x - p.D);
+        map[x] = static_cast<uint8_t>(b < 0 ? none : b);
     }
-    group_barrier(w);
+}
+// Extremes of the row positions (s_red: 2 * NR / 32 ints; a barrier inside,
+// which also completes the map).  With 256 threads each half holds all rows.
+template <int NR>
+__device__ __forceinline__ void bias_rows(Bias16& t, const Problem& p, int pos, bool valid, int span, int* s_red) {
+    constexpr int W = NR / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    t.wlo = __reduce_min_sync(0xffffffffu, valid ? pos : INT_MAX);
+    t.whi = __reduce_max_sync(0xffffffffu, valid ? pos : INT_MIN);
+    if (lane == 0) {
+        s_red[warp] = t.wlo;
+        s_red[W + warp] = t.whi;
+    }
+    rows_barrier<NR>();
     t.rmin = min(min(s_red[0], s_red[1]), min(s_red[2], s_red[3]));
-    const int rmax = max(max(s_red[4], s_red[5]), max(s_red[6], s_red[7]));
+    const int rmax = max(max(s_red[W], s_red[W + 1]), max(s_red[W + 2], s_red[W + 3]));
     const int64_t R = static_cast<int64_t>(rmax) - t.rmin;
     t.D = p.D;
     t.near = R <= span;
@@ -190,57 +211,65 @@ __device__ __forceinline__ void bias_rows(Bias16& t, const Problem& p, int w, in
     t.p_row = pos;
     t.row = valid && t.near ? 2u * static_cast<uint32_t>(t.R - (pos - t.rmin)) : 0u;
 }
-// The bucket of every entry (255: none), by n of the CTA's threads.
-template <int SIGN>
-__device__ __forceinline__ void bias_ids(const Bias16& t, const Problem& p, uint8_t* ids, int tid, int n) {
+// The bucket of every entry, once per CTA.  SIGN = 1: rows are queries, -1: keys.
+template <int SIGN, int NR>
+__device__ __forceinline__ void bias_ids(const Bias16& t, const uint8_t* map, uint8_t* ids, int none) {
 #pragma unroll 4
-    for (int x = tid; x <= t.last; x += n) ids[x] = static_cast<uint8_t>(bucket_of(p, SIGN * (x - t.D - t.R)));
-    for (int x = t.last + 1 + tid; x <= t.last + kVecPad; x += n) ids[x] = kNoBucket;
+    for (int x = threadIdx.x; x <= t.last; x += NR)
+        ids[x] = map[max(-t.D, min(t.D, SIGN * (x - t.D - t.R))) + t.D];
+    for (int x = t.last + 1 + threadIdx.x; x <= t.last + kVecPad; x += NR) ids[x] = static_cast<uint8_t>(none);   // past a partial tile's end
 }
-// One head's entries from its column of the table (tab), by the group.
+// One head's entries from its column of the table; tab[none] = 0.
+template <int NR>
 __device__ __forceinline__ void bias_fill(const Bias16& t, const uint8_t* ids, const uint16_t* tab) {
 #pragma unroll 4
-    for (int x = threadIdx.x & 127; x <= t.last + kVecPad; x += 128) {
-        const int b = ids[x];
-        t.vec[x] = b == kNoBucket ? uint16_t(0) : tab[b];
-    }
+    for (int x = threadIdx.x; x <= t.last + kVecPad; x += NR) t.vec[x] = tab[ids[x]];
 }
-// Offsets and kinds of columns [c0, c0 + kChunk), by the group; barriers around it are the caller's.
-template <class PosOf>
-__device__ __forceinline__ void bias_columns(const Bias16& t, int c0, int len, PosOf pos_of) {
-    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-    const int lo = -t.D, hi = t.R + t.D;
-    auto clamped = [&](int x) {
-        const int64_t d = static_cast<int64_t>(x) - t.rmin;
-        return d < lo ? lo : d > hi ? hi : static_cast<int>(d);
-    };
-    int pos[kChunkTiles / 4][2];   // all loads first
+// Positions of columns [c0, c0 + kChunk), loaded ahead of what needs them.
+template <int NR>
+struct Columns {
+    static constexpr int K = kChunkTiles / (NR / 32);   // tiles of a warp
+    int pos[K][2];
+    template <class PosOf>
+    __device__ __forceinline__ void load(int c0, int len, PosOf pos_of) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-    for (int k = 0; k < kChunkTiles / 4; ++k) {
-        const int c = c0 + (warp + k * 4) * kTile + lane;
-        pos[k][0] = c < len ? pos_of(c) : 0;
-        pos[k][1] = c + 32 < len ? pos_of(c + 32) : 0;
-    }
-#pragma unroll
-    for (int k = 0; k < kChunkTiles / 4; ++k) {
-        const int tile = warp + k * 4, c = c0 + tile * kTile + lane;
-        if (c0 + tile * kTile >= len) break;
-        const bool v0 = c < len, v1 = c + 32 < len;
-        const int o0 = clamped(pos[k][0]), o1 = clamped(pos[k][1]);
-        const int first = __shfl_sync(0xffffffffu, o0, 0);
-        const bool left = __all_sync(0xffffffffu, (!v0 || o0 == lo) && (!v1 || o1 == lo));
-        const bool right = __all_sync(0xffffffffu, (!v0 || o0 == hi) && (!v1 || o1 == hi));
-        const bool run = __all_sync(0xffffffffu, (!v0 || o0 == first + lane) && (!v1 || o1 == first + 32 + lane));
-        int* off = t.off + tile * kTile;
-        if (t.near) {
-            off[lane] = v0 ? 2 * (o0 - lo) : 0;
-            off[lane + 32] = v1 ? 2 * (o1 - lo) : 0;
-        } else {
-            off[lane] = pos[k][0];
-            off[lane + 32] = pos[k][1];
+        for (int k = 0; k < K; ++k) {
+            const int c = c0 + (warp + k * (NR / 32)) * kTile + lane;
+            pos[k][0] = c < len ? pos_of(c) : 0;
+            pos[k][1] = c + 32 < len ? pos_of(c + 32) : 0;
         }
-        if (lane == 0) t.kind[tile] = !t.near ? kClamped : left ? kLeft : right ? kRight : run ? kConsecutive : kGeneral;
     }
+    // Offsets and kinds; barriers around it are the caller's.
+    __device__ __forceinline__ void store(const Bias16& t, int c0, int len) const {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int lo = -t.D, hi = t.R + t.D;
+        auto clamped = [&](int x) {
+            const int64_t d = static_cast<int64_t>(x) - t.rmin;
+            return d < lo ? lo : d > hi ? hi : static_cast<int>(d);
+        };
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int tile = warp + k * (NR / 32), c = c0 + tile * kTile + lane;
+            if (c0 + tile * kTile >= len) break;
+            const bool v0 = c < len, v1 = c + 32 < len;
+            const int p0 = pos[k][0], p1 = pos[k][1], o0 = clamped(p0), o1 = clamped(p1);
+            const int first = __shfl_sync(0xffffffffu, o0, 0);
+            const bool run = __all_sync(0xffffffffu, (!v0 || o0 == first + lane) && (!v1 || o1 == first + 32 + lane));
+            const int pmin = __reduce_min_sync(0xffffffffu, min(v0 ? p0 : INT_MAX, v1 ? p1 : INT_MAX));
+            const int pmax = __reduce_max_sync(0xffffffffu, max(v0 ? p0 : INT_MIN, v1 ? p1 : INT_MIN));
+            int* off = t.off + tile * kTile;
+            off[lane] = !t.near ? p0 : v0 ? 2 * (o0 - lo) : 0;
+            off[lane + 32] = !t.near ? p1 : v1 ? 2 * (o1 - lo) : 0;
+            if (lane == 0) t.tiles[tile] = TileInfo{pmin, pmax, !t.near ? kClamped : run ? kConsecutive : kGeneral, 0};
+        }
+    }
+};
+// The kind of a tile for this warp: all its distances past one end of the map
+// (one bias for all), or what the columns allow.
+__device__ __forceinline__ int tile_kind(const Bias16& t, int tile) {
+    const int4 i = *reinterpret_cast<const int4*>(t.tiles + tile);
+    return pos_diff(i.y, t.wlo) <= -t.D ? kLeft : pos_diff(i.x, t.whi) >= t.D ? kRight : i.z;
 }
 // x = x * scale + bias for 32 columns from column c of a tile (not for kLeft, kRight).
 template <typename T>
@@ -296,7 +325,9 @@ constexpr int kFwdK = 3, kFwdV = 5;
 
 __host__ __device__ constexpr int fwd_fixed_bytes() { return 1024 + 2 * kRowBytes + (kFwdK + kFwdV) * kTileBytes + 4 * kChunk; }
 __host__ __device__ constexpr int vec16_bytes(int D, int span) { return 2 * ((vec_entries(D, span) + 7) & ~7); }
-__host__ __device__ constexpr int ids_bytes(int D, int span) { return (vec_entries(D, span) + 15) & ~15; }
+__host__ __device__ constexpr int ids_bytes(int D, int span) {   // and the bucket map
+    return ((vec_entries(D, span) + 15) & ~15) + ((2 * D + 1 + 15) & ~15);
+}
 __host__ __device__ constexpr int fwd_smem_bytes(int D, int span) {
     return fwd_fixed_bytes() + 2 * vec16_bytes(D, span) + ids_bytes(D, span);
 }
@@ -337,8 +368,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     // q_full[2], q_empty[2], k_full[3], v_full[5], s_full[3], p_full[4], pv_done[5], done
     constexpr int kBars = 25;
     __shared__ __align__(8) uint64_t s_bar[kBars];
-    __shared__ uint16_t s_tab[2][kMaxBuckets];
-    __shared__ int s_kind[kChunkTiles], s_red[8];
+    __shared__ uint16_t s_tab[2][kMaxBuckets + 1];
+    __shared__ __align__(16) TileInfo s_tiles[kChunkTiles];
+    __shared__ int s_red[8];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
 
@@ -465,16 +497,24 @@ __global__ void __launch_bounds__(kThreads, 2)
         uint8_t* ids = extra + 2 * vec16_bytes(p.D, span);
         t.vec = vec0;
         t.off = reinterpret_cast<int*>(ids + ids_bytes(p.D, span));
-        t.kind = s_kind;
+        t.tiles = s_tiles;
+        uint8_t* map = ids + ((vec_entries(p.D, span) + 15) & ~15);
         const bool has_entry = tid < p.num_buckets;   // of the table's column of a head
         const uint16_t* column = p.table + static_cast<int64_t>(has_entry ? tid : 0) * p.H + h0;
+        // What the set-up needs of global memory, all under way at once.
         const uint16_t entry = __ldg(column);
-        bias_rows(t, p, 0, valid ? query_pos(p, s, row) : 0, valid, span, s_red);
-        bias_ids<1>(t, p, ids, tid, 128);
-        bias_columns(t, 0, s.k_len, [&](int c) { return key_pos(p, s, c); });
+        const int pos = valid ? query_pos(p, s, row) : 0;
+        auto key_at = [&](int c) { return key_pos(p, s, c); };
+        Columns<128> cols;
+        cols.load(0, s.k_len, key_at);
+        bias_map<128>(p, map, p.num_buckets);
         if (has_entry) s_tab[0][tid] = bias_bits<T>(entry);
-        group_barrier(0);
-        bias_fill(t, ids, s_tab[0]);
+        if (tid == p.num_buckets) s_tab[0][tid] = s_tab[1][tid] = 0;
+        bias_rows<128>(t, p, pos, valid, span, s_red);
+        bias_ids<1, 128>(t, map, ids, p.num_buckets);
+        cols.store(t, 0, s.k_len);
+        rows_barrier<128>();
+        bias_fill<128>(t, ids, s_tab[0]);
         const uint32_t tmem = start_rows(&s_tmem);
 
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
@@ -509,20 +549,21 @@ __global__ void __launch_bounds__(kThreads, 2)
             // This head's entries are complete and the last head's no longer read after
             // this barrier; the next head's are filled in behind it.
             if (i + 1 < nh && has_entry) s_tab[(i + 1) & 1][tid] = bias_bits<T>(__ldg(column + i + 1));
-            group_barrier(0);
+            rows_barrier<128>();
             if (i + 1 < nh) {
                 t.vec = vec0 + ((i + 1) & 1) * vec_step;
-                bias_fill(t, ids, s_tab[(i + 1) & 1]);
+                bias_fill<128>(t, ids, s_tab[(i + 1) & 1]);
             }
             t.vec = vec0 + (i & 1) * vec_step;
             float m_ref = -INFINITY, l0 = 0.f, l1 = 0.f;
             for (int tile = 0; tile < nt; ++tile, ++g) {
                 if (tile % kChunkTiles == 0 && (tile > 0 || (i > 0 && nt > kChunkTiles))) {
-                    if (tile > 0) group_barrier(0);
-                    bias_columns(t, tile * kTile, s.k_len, [&](int c) { return key_pos(p, s, c); });
-                    group_barrier(0);
+                    cols.load(tile * kTile, s.k_len, key_at);
+                    if (tile > 0) rows_barrier<128>();
+                    cols.store(t, tile * kTile, s.k_len);
+                    rows_barrier<128>();
                 }
-                const int kind = t.kind[tile % kChunkTiles];
+                const int kind = tile_kind(t, tile % kChunkTiles);
                 const int* off = t.off + (tile % kChunkTiles) * kTile;
                 ok = ok && wait.warp(s_full(g), (g / 3) & 1);
                 if (ok && warp_rows) {
