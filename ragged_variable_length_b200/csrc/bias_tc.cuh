@@ -332,6 +332,16 @@ __host__ __device__ constexpr int fwd_smem_bytes(int D, int span) {
     return fwd_fixed_bytes() + 2 * vec16_bytes(D, span) + ids_bytes(D, span);
 }
 
+// One lane of a converged warp, chosen by the hardware: the compiler then knows
+// that the branch holds one thread, and keeps the MMAs' descriptors, which are
+// the same in all lanes, in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // The start of a CTA: the load warp sets up the barriers and begins at once,
 // the MMA warp takes the TMEM and waits for the barriers, the row threads join
 // when they have prepared the bias.
@@ -443,45 +453,51 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         cp_async_wait_all();
     } else if (warp == kTcMmaWarp) {
-        // ---------------- MMA issue (one thread) ----------------
-        const uint32_t tmem = start_mma(&s_tmem, kTmemCols);
-        if (lane == 0) {
-            const uint32_t idesc_qk = make_idesc(Cvt<T>::kFormat, 0, kTile), idesc_pv = make_idesc(Cvt<T>::kFormat, 1, 64);
-            int qi = 0, qt = 0;   // head and tile of the next scores
-            auto issue_qk = [&](uint32_t g) {
-                if (qt == 0 && !wait(q_full(qi), (qi >> 1) & 1)) return false;
-                if (!wait(k_full(g), (g / kFwdK) & 1)) return false;
-                fence_async_smem();   // cp.async wrote through the generic proxy
-                fence_after_sync();
-                const uint32_t sq = sQ + (qi & 1) * kRowBytes;
+        // ---------------- MMA issue (one elected thread; the warp waits as one) ----------------
+        const uint32_t tmem = uniform(start_mma(&s_tmem, kTmemCols));
+        const uint32_t n = uniform(total), per_head = uniform(nt);
+        const uint32_t idesc_qk = make_idesc(Cvt<T>::kFormat, 0, kTile), idesc_pv = make_idesc(Cvt<T>::kFormat, 1, 64);
+        const bool leader = elect_one();
+        uint32_t qi = 0, qt = 0;   // head and tile of the next scores
+        auto issue_qk = [&](uint32_t g) {
+            if (qt == 0 && !wait.warp(q_full(qi), (qi >> 1) & 1)) return false;
+            if (!wait.warp(k_full(g), (g / kFwdK) & 1)) return false;
+            fence_async_smem();   // cp.async wrote through the generic proxy
+            fence_after_sync();
+            const uint32_t sq = sQ + (qi & 1) * kRowBytes, sk = sK + (g % kFwdK) * kTileBytes, d = tmem + (g % 3) * kTile;
+            if (leader) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_f16(tmem + (g % 3) * kTile, make_sdesc(sq + ks * 32), make_sdesc(sK + (g % kFwdK) * kTileBytes + ks * 32),
-                            idesc_qk, ks > 0);
+                for (int ks = 0; ks < 4; ++ks) mma_f16(d, make_sdesc(sq + ks * 32), make_sdesc(sk + ks * 32), idesc_qk, ks > 0);
                 mma_commit(s_full(g));
-                if (++qt == nt) {
-                    mma_commit(q_empty(qi));
-                    qt = 0;
-                    ++qi;
-                }
-                return true;
-            };
-            bool ok = true;
-            for (uint32_t g = 0; ok && g < 3 && g < total; ++g) ok = issue_qk(g);
-            int t = 0;
-            for (uint32_t g = 0; ok && g < total; ++g) {
-                ok = wait(v_full(g), (g / kFwdV) & 1) && wait(p_full(g), (g >> 2) & 1);
-                if (!ok) break;
-                fence_async_smem();
-                fence_after_sync();
+                if (qt + 1 == per_head) mma_commit(q_empty(qi));
+            }
+            __syncwarp();
+            if (++qt == per_head) {
+                qt = 0;
+                ++qi;
+            }
+            return true;
+        };
+        bool ok = true;
+        for (uint32_t g = 0; ok && g < 3 && g < n; ++g) ok = issue_qk(g);
+        uint32_t t = 0;
+        for (uint32_t g = 0; ok && g < n; ++g) {
+            ok = wait.warp(v_full(g), (g / kFwdV) & 1) && wait.warp(p_full(g), (g >> 2) & 1);
+            if (!ok) break;
+            fence_async_smem();
+            fence_after_sync();
+            const uint32_t pa = tmem + (g % 3) * kTile, sv = sV + (g % kFwdV) * kTileBytes;
+            if (leader) {
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_f16_ts(tmem + o_col, tmem + (g % 3) * kTile + ks * 8,
-                               make_sdesc(sV + (g % kFwdV) * kTileBytes + ks * 2048), idesc_pv, (t > 0 || ks > 0) ? 1u : 0u);
+                    mma_f16_ts(tmem + o_col, pa + ks * 8, make_sdesc(sv + ks * 2048), idesc_pv, (t > 0 || ks > 0) ? 1u : 0u);
                 mma_commit(pv_done(g));
-                if (g + 3 < total) ok = issue_qk(g + 3);
-                if (++t == nt) t = 0;
             }
+            __syncwarp();
+            if (g + 3 < n) ok = issue_qk(g + 3);
+            if (++t == per_head) t = 0;
+        }
+        if (leader) {
             mma_commit(done);   // every MMA has finished before TMEM is freed
             mbar_wait(done, 0);
         }
