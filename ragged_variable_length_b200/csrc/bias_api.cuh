@@ -109,7 +109,7 @@ constexpr int bias_span(int D, int fixed, int bytes_per_entry) {
     const int span = (entries - 1 - ragged::bias::kVecPad) / 2 - D;
     return span < 256 ? ragged::bias::kSpan : span < ragged::bias::kSpan ? span : ragged::bias::kSpan;
 }
-constexpr int kBwdQSmemMax = ragged::bias::bwd_q_smem_bytes(ragged::bias::kMaxDistance, ragged::bias::kMaxBuckets, ragged::bias::kSpan);
+constexpr int kBwdQSmemMax = ragged::bias::bwd_q_smem_bytes(ragged::bias::kMaxDistance, ragged::bias::kMaxBuckets, ragged::bias::kSpan, 3);
 
 ragged_status check_workspace(const void* ws, int64_t have, int64_t need) {
     if (need > 0 && (ws == nullptr || have < need))
@@ -119,7 +119,7 @@ ragged_status check_workspace(const void* ws, int64_t have, int64_t need) {
     return RAGGED_OK;
 }
 
-DeviceFlags g_bias_fwd_smem[2], g_bias_bwd_q_smem[2], g_bias_bwd_kv_smem[2], g_bias_weight_smem[2];
+DeviceFlags g_bias_fwd_smem[2], g_bias_bwd_q_smem[2][2], g_bias_bwd_kv_smem[2], g_bias_weight_smem[2];
 template <typename T>
 constexpr int kTypeSlot = std::is_same<T, __half>::value ? 0 : 1;
 
@@ -154,27 +154,28 @@ int heads_per_cta(int64_t row_tiles, int64_t heads, int64_t col_tiles, int64_t s
 bool few_rows(const ragged::bias::Problem& p) {
     return static_cast<int64_t>(p.group) * p.max_q <= ragged::bias::kFewMaxRows;
 }
-// CTAs per (sequence, key / value head): what one wave of two per SM holds,
+// CTAs per (sequence, key / value head): what one wave of `per_sm` per SM holds,
 // each with at least one block of keys per warp.
-int few_splits(const ragged::bias::Problem& p, int limit) {
-    const int64_t base = static_cast<int64_t>(p.B) * p.Hkv, want = 2LL * sm_count() / base;
-    const int64_t most = (p.max_k + ragged::bias::kFewKeys * ragged::bias::kFewWarps - 1) / (ragged::bias::kFewKeys * ragged::bias::kFewWarps);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, most), limit)));
+int few_splits(const ragged::bias::Problem& p, int per_sm, int warps, int limit) {
+    const int64_t base = static_cast<int64_t>(p.B) * p.Hkv, want = static_cast<int64_t>(per_sm) * sm_count() / base;
+    const int64_t keys = static_cast<int64_t>(ragged::bias::kFewKeys) * warps;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, (p.max_k + keys - 1) / keys), limit)));
 }
-DeviceFlags g_few_smem[2][2], g_few_weight_smem[2][2];
+DeviceFlags g_few_smem[2][2][2], g_few_weight_smem[2][2][2];
 
-template <typename T, int MT>
+template <typename T, int MT, int NW>
 ragged_status launch_few(const ragged::bias::Problem& p, uint16_t* out, int64_t out_tok, cudaStream_t s) {
     using namespace ragged::bias;
-    auto kernel = bias_few_kernel<T, MT>;
-    ragged_status st = ensure_smem(kernel, few_smem_bytes<MT, false>(kMaxDistance, kMaxBuckets), g_few_smem[kTypeSlot<T>][MT - 1]);
+    auto kernel = bias_few_kernel<T, MT, NW>;
+    ragged_status st = ensure_smem(kernel, few_smem_bytes<MT, NW, false>(kMaxDistance, kMaxBuckets),
+                                   g_few_smem[kTypeSlot<T>][MT - 1][NW == kFewWarps]);
     if (st != RAGGED_OK) return st;
-    int splits = few_splits(p, kFewMaxSplits);
+    int splits = few_splits(p, NW == kFewWarps ? 2 : 4, NW, kFewMaxSplits);
     while (splits & (splits - 1)) splits &= splits - 1;   // cluster sizes are powers of two
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = bias_grid(splits, p.Hkv, p.B);
-    cfg.blockDim = dim3(kFewThreads);
-    cfg.dynamicSmemBytes = few_smem_bytes<MT, false>(p.D, p.num_buckets);
+    cfg.blockDim = dim3(32 * NW);
+    cfg.dynamicSmemBytes = few_smem_bytes<MT, NW, false>(p.D, p.num_buckets);
     cfg.stream = s;
     cudaLaunchAttribute cluster{};
     cluster.id = cudaLaunchAttributeClusterDimension;
@@ -184,22 +185,40 @@ ragged_status launch_few(const ragged::bias::Problem& p, uint16_t* out, int64_t 
     cfg.numAttrs = splits > 1 ? 1 : 0;
     return cuda_check(cudaLaunchKernelEx(&cfg, kernel, p, out, out_tok), "attention (few rows) launch");
 }
-
-template <typename T, int MT>
+template <typename T, int MT, int NW>
 ragged_status launch_few_weight(const ragged::bias::Problem& p, const float* prev, float* weight, int64_t stride, cudaStream_t s) {
     using namespace ragged::bias;
-    auto kernel = bias_few_weight_kernel<T, MT>;
-    ragged_status st = ensure_smem(kernel, few_smem_bytes<MT, true>(kMaxDistance, kMaxBuckets), g_few_weight_smem[kTypeSlot<T>][MT - 1]);
+    auto kernel = bias_few_weight_kernel<T, MT, NW>;
+    ragged_status st = ensure_smem(kernel, few_smem_bytes<MT, NW, true>(kMaxDistance, kMaxBuckets),
+                                   g_few_weight_smem[kTypeSlot<T>][MT - 1][NW == kFewWarps]);
     if (st != RAGGED_OK) return st;
-    kernel<<<bias_grid(few_splits(p, 1 << 16), p.Hkv, p.B), kFewThreads, few_smem_bytes<MT, true>(p.D, p.num_buckets), s>>>(p, prev, weight, stride);
+    const int splits = few_splits(p, NW == kFewWarps ? 2 : 8, NW, 1 << 16);
+    kernel<<<bias_grid(splits, p.Hkv, p.B), 32 * NW, few_smem_bytes<MT, NW, true>(p.D, p.num_buckets), s>>>(p, prev, weight, stride);
     return cuda_check(cudaGetLastError(), "attention weight (few rows) launch");
+}
+// By rows (one or two MMA tiles) and by the longest sequence.
+template <typename T>
+ragged_status launch_few_rows(const ragged::bias::Problem& p, uint16_t* out, int64_t out_tok, cudaStream_t s) {
+    using namespace ragged::bias;
+    const bool one = p.group * p.max_q <= 16;
+    if (p.max_k <= kFewShortKeys)
+        return one ? launch_few<T, 1, kFewShortWarps>(p, out, out_tok, s) : launch_few<T, 2, kFewShortWarps>(p, out, out_tok, s);
+    return one ? launch_few<T, 1, kFewWarps>(p, out, out_tok, s) : launch_few<T, 2, kFewWarps>(p, out, out_tok, s);
+}
+template <typename T>
+ragged_status launch_few_rows_weight(const ragged::bias::Problem& p, const float* prev, float* weight, int64_t stride, cudaStream_t s) {
+    using namespace ragged::bias;
+    const bool one = p.group * p.max_q <= 16;
+    if (p.max_k <= kFewShortKeys)
+        return one ? launch_few_weight<T, 1, kFewShortWarps>(p, prev, weight, stride, s)
+                   : launch_few_weight<T, 2, kFewShortWarps>(p, prev, weight, stride, s);
+    return one ? launch_few_weight<T, 1, kFewWarps>(p, prev, weight, stride, s) : launch_few_weight<T, 2, kFewWarps>(p, prev, weight, stride, s);
 }
 
 template <typename T>
 ragged_status launch_bias_fwd(const ragged::bias::Problem& p, uint16_t* out, int64_t out_tok, cudaStream_t s) {
     using namespace ragged::bias;
-    if (few_rows(p))
-        return p.group * p.max_q <= 16 ? launch_few<T, 1>(p, out, out_tok, s) : launch_few<T, 2>(p, out, out_tok, s);
+    if (few_rows(p)) return launch_few_rows<T>(p, out, out_tok, s);
     ragged_status st = ensure_smem(bias_fwd_kernel<T>, fwd_smem_bytes(kMaxDistance, kSpan), g_bias_fwd_smem[kTypeSlot<T>]);
     if (st != RAGGED_OK) return st;
     const int span = bias_span(p.D, fwd_fixed_bytes(), 5);
@@ -214,15 +233,19 @@ ragged_status launch_bias_fwd(const ragged::bias::Problem& p, uint16_t* out, int
 template <typename T>
 ragged_status launch_bias_bwd(const ragged::bias::Problem& p, ragged::bias::BwdArgs a, cudaStream_t s) {
     using namespace ragged::bias;
-    ragged_status st = ensure_smem(bias_bwd_q_kernel<T>, kBwdQSmemMax, g_bias_bwd_q_smem[kTypeSlot<T>]);
+    // Two K and V stages instead of three where many buckets' sums would not
+    // leave room for two CTAs per SM.
+    const int stages = bwd_q_fixed_bytes(p.num_buckets, 3) + 8192 <= kTwoPerSm ? 3 : 2;
+    auto q_kernel = stages == 3 ? bias_bwd_q_kernel<T, 3> : bias_bwd_q_kernel<T, 2>;
+    ragged_status st = ensure_smem(q_kernel, kBwdQSmemMax, g_bias_bwd_q_smem[kTypeSlot<T>][stages - 2]);
     if (st == RAGGED_OK) st = ensure_smem(bias_bwd_kv_kernel<T>, bwd_kv_smem_bytes(kMaxDistance, kSpan), g_bias_bwd_kv_smem[kTypeSlot<T>]);
     if (st != RAGGED_OK) return st;
     const int64_t avg_q = average_length(p.B, p.max_q, p.lse_stride), avg_k = std::max<int64_t>(1, p.max_k * avg_q / p.max_q);
     const int64_t slots = 2LL * sm_count();
-    a.span = bias_span(p.D, bwd_q_fixed_bytes(p.num_buckets), 3);
+    a.span = bias_span(p.D, bwd_q_fixed_bytes(p.num_buckets, stages), 3);
     a.heads = heads_per_cta(p.B * tiles128(avg_q), p.H, (avg_k + kTile - 1) / kTile, slots);
-    bias_bwd_q_kernel<T><<<bias_grid(a.q_tiles, (p.H + a.heads - 1) / a.heads, p.B), kBwdThreads,
-                           bwd_q_smem_bytes(p.D, p.num_buckets, a.span), s>>>(p, a);
+    q_kernel<<<bias_grid(a.q_tiles, (p.H + a.heads - 1) / a.heads, p.B), kBwdThreads,
+               bwd_q_smem_bytes(p.D, p.num_buckets, a.span, stages), s>>>(p, a);
     st = cuda_check(cudaGetLastError(), "query gradient launch");
     if (st != RAGGED_OK) return st;
     a.span = bias_span(p.D, bwd_kv_fixed_bytes(), 3);
@@ -245,9 +268,7 @@ template <typename T>
 ragged_status launch_bias_weight(const ragged::bias::Problem& p, const float* prev, float* weight, int64_t stride,
                                  cudaStream_t s) {
     using namespace ragged::bias;
-    if (few_rows(p))
-        return p.group * p.max_q <= 16 ? launch_few_weight<T, 1>(p, prev, weight, stride, s)
-                                       : launch_few_weight<T, 2>(p, prev, weight, stride, s);
+    if (few_rows(p)) return launch_few_rows_weight<T>(p, prev, weight, stride, s);
     ragged_status st = ensure_smem(bias_weight_kernel<T>, weight_smem_bytes(kMaxDistance, kSpan), g_bias_weight_smem[kTypeSlot<T>]);
     if (st != RAGGED_OK) return st;
     const int64_t avg_q = average_length(p.B, p.max_q, p.lse_stride), avg_k = std::max<int64_t>(1, p.max_k * avg_q / p.max_q);

@@ -127,11 +127,11 @@ __device__ __forceinline__ void probabilities(const Bias16& t, const Problem& p,
     }
 }
 
-__host__ __device__ constexpr int bwd_q_fixed_bytes(int num_buckets) {
-    return 1024 + kBwdStages * 2 * kTileBytes + (num_buckets + 1) * 4 * kBwdRows + 4 * kChunk;
+__host__ __device__ constexpr int bwd_q_fixed_bytes(int num_buckets, int stages) {
+    return 1024 + stages * 2 * kTileBytes + (num_buckets + 1) * 4 * kBwdRows + 4 * kChunk;
 }
-__host__ __device__ constexpr int bwd_q_smem_bytes(int D, int num_buckets, int span) {
-    return bwd_q_fixed_bytes(num_buckets) + vec16_bytes(D, span) + ids_bytes(D, span);
+__host__ __device__ constexpr int bwd_q_smem_bytes(int D, int num_buckets, int span, int stages) {
+    return bwd_q_fixed_bytes(num_buckets, stages) + vec16_bytes(D, span) + ids_bytes(D, span);
 }
 
 // Query rows: dQ, delta, and each tile's sums for the table's gradient.
@@ -142,10 +142,10 @@ __host__ __device__ constexpr int bwd_q_smem_bytes(int D, int num_buckets, int s
 // the time of one with A in shared memory, and the room goes to the table's
 // sums.  S of the next tile is computed while dS of this one is, dP of the
 // next one while its probabilities are.
-template <typename T>
+template <typename T, int STAGES>
 __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Problem p, const BwdArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    // kv_full[3], kv_done[3], qd_full, s_full, dp_full, a_full, b_full, dq_full, done
+    // kv_full[3], kv_done[3] (up to STAGES), qd_full, s_full, dp_full, a_full, b_full, dq_full, done
     constexpr int kBars = 13;
     __shared__ __align__(8) uint64_t s_bar[kBars];
     __shared__ uint16_t s_tab[kMaxBuckets + 1];
@@ -176,11 +176,11 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
 
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t sRing = (raw + 1023u) & ~1023u;   // stage: K, then V
-    float* acc = reinterpret_cast<float*>(smem_raw + (sRing - raw) + kBwdStages * 2 * kTileBytes);   // [buckets + 1][256]
-    auto stage = [&](uint32_t g) { return sRing + (g % kBwdStages) * 2 * kTileBytes; };
+    float* acc = reinterpret_cast<float*>(smem_raw + (sRing - raw) + STAGES * 2 * kTileBytes);   // [buckets + 1][256]
+    auto stage = [&](uint32_t g) { return sRing + (g % STAGES) * 2 * kTileBytes; };
     const uint32_t bar0 = smem_addr(&s_bar[0]);
-    auto kv_full = [&](uint32_t g) { return bar0 + 8u * (g % kBwdStages); };
-    auto kv_done = [&](uint32_t g) { return bar0 + 8u * (3 + g % kBwdStages); };
+    auto kv_full = [&](uint32_t g) { return bar0 + 8u * (g % STAGES); };
+    auto kv_done = [&](uint32_t g) { return bar0 + 8u * (3 + g % STAGES); };
     const uint32_t qd_full = bar0 + 48, s_full = bar0 + 56, dp_full = bar0 + 64, a_full = bar0 + 72, b_full = bar0 + 80, dq_full = bar0 + 88, done = bar0 + 96;
     constexpr uint32_t dp_col = kTile, dq_col = 2 * kTile, q_col = 3 * kTile, do_col = 3 * kTile + 32;
     const Wait wait{&s_fail};
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
             const uint16_t* kb = p.k + s.k_start * p.kv_tok + z;
             const uint16_t* vb = p.v + s.k_start * p.kv_tok + z;
             for (int t = 0; t < nt; ++t, ++g) {
-                if (g >= kBwdStages) ok = wait.warp(kv_done(g), (g / kBwdStages - 1) & 1);
+                if (g >= STAGES) ok = wait.warp(kv_done(g), (g / STAGES - 1) & 1);
                 if (!ok) break;
                 load_rows<kTile>(stage(g), kb, p.kv_tok, t * kTile, s.k_len, lane);
                 load_rows<kTile>(stage(g) + kTileBytes, vb, p.kv_tok, t * kTile, s.k_len, lane);
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
             bool ok = true;
             uint32_t g = 0;
             for (int i = 0; ok && i < nh; ++i) {
-                ok = wait(qd_full, i & 1) && wait(kv_full(g), (g / kBwdStages) & 1);
+                ok = wait(qd_full, i & 1) && wait(kv_full(g), (g / STAGES) & 1);
                 if (!ok) break;
                 fence_async_smem();
                 fence_after_sync();
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                 for (int t = 0; t < nt; ++t, ++g) {
                     const bool more = t + 1 < nt;
                     if (more) {
-                        ok = wait(kv_full(g + 1), ((g + 1) / kBwdStages) & 1);
+                        ok = wait(kv_full(g + 1), ((g + 1) / STAGES) & 1);
                         if (!ok) break;
                         fence_async_smem();
                     }

@@ -22,8 +22,11 @@
 namespace ragged {
 namespace bias {
 
-constexpr int kFewWarps = 8;
-constexpr int kFewThreads = 32 * kFewWarps;
+// Warps of a CTA: few where the longest sequence is short, so that many CTAs
+// share an SM (200 sequences of 4 to 6 tokens, 8 heads: 33 us with eight warps,
+// which a ring each for long sequences takes 100 KB for).
+constexpr int kFewWarps = 8, kFewShortWarps = 2;
+constexpr int kFewShortKeys = 128;
 constexpr int kFewKeys = 16;          // keys per block
 constexpr int kFewStages = 3;         // ring of a warp: two blocks in flight beside the current one
 constexpr int kFewMaxRows = 32;
@@ -35,10 +38,16 @@ template <int MT, bool WEIGHT>
 __host__ __device__ constexpr int few_stage_bytes() {   // keys, then values or the weights so far, then positions
     return kFewKeys * 128 + (WEIGHT ? MT * 16 * kFewKeys * 4 : kFewKeys * 128) + kFewKeys * 4;
 }
-template <int MT, bool WEIGHT>
+// The bucket map is staged for long sequences only: a short one meets few distances.
+template <int MT, int NW>
+__host__ __device__ constexpr int few_map_bytes(int D) { return NW == kFewWarps ? (2 * D + 1 + 15) & ~15 : 0; }
+template <int MT, int NW, bool WEIGHT>
+__host__ __device__ constexpr int few_ring_bytes() {   // at least what the warps' states take at the end
+    return WEIGHT || kFewStages * few_stage_bytes<MT, WEIGHT>() > MT * 16 * 256 ? NW * kFewStages * few_stage_bytes<MT, WEIGHT>() : NW * MT * 16 * 256;
+}
+template <int MT, int NW, bool WEIGHT>
 __host__ __device__ constexpr int few_smem_bytes(int D, int num_buckets) {
-    return kFewWarps * kFewStages * few_stage_bytes<MT, WEIGHT>() + MT * 16 * 128 + ((2 * D + 1 + 15) & ~15) +
-           4 * num_buckets * MT * 16;
+    return few_ring_bytes<MT, NW, WEIGHT>() + MT * 16 * 128 + few_map_bytes<MT, NW>(D) + 4 * num_buckets * MT * 16;
 }
 
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, int src_bytes) {
@@ -68,8 +77,10 @@ __device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t round
 
 // What both kernels set up: the sequence, this warp's key blocks, the query
 // fragments, the rows' positions and the bias in shared memory.
-template <typename T, int MT, bool WEIGHT>
+template <typename T, int MT, int NW, bool WEIGHT>
 struct Few {
+    static constexpr int kThreadsF = 32 * NW;
+    static constexpr bool kMap = NW == kFewWarps;
     static constexpr int kStage = few_stage_bytes<MT, WEIGHT>();
     Seq s;
     int z, rows, warp, lane, g, c2;   // g: row in a tile, c2: first of this lane's two columns
@@ -100,23 +111,24 @@ struct Few {
     // What the scores need (the first blocks are on their way meanwhile).
     __device__ __forceinline__ void setup(const Problem& p, uint8_t* smem) {
         const int tid = threadIdx.x;
-        uint8_t* sq = smem + kFewWarps * kFewStages * kStage;
+        uint8_t* sq = smem + few_ring_bytes<MT, NW, WEIGHT>();
         uint8_t* m = sq + MT * 16 * 128;
-        float* t = reinterpret_cast<float*>(m + ((2 * p.D + 1 + 15) & ~15));
+        float* t = reinterpret_cast<float*>(m + few_map_bytes<MT, NW>(p.D));
         map = m;
         tab = t;
-        for (int i = tid; i < MT * 16 * 8; i += kFewThreads) {
+        for (int i = tid; i < MT * 16 * 8; i += kThreadsF) {
             const int r = i >> 3, c = i & 7;
             uint4 w = make_uint4(0, 0, 0, 0);
             if (r < rows)
                 w = __ldg(reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(s.q_start + query_of(r)) * p.q_tok + head_of(p, r) * p.q_head) + c);
             *reinterpret_cast<uint4*>(sq + mma_attn::swz(r, c)) = w;
         }
-        for (int i = tid; i < p.num_buckets * MT * 16; i += kFewThreads) {
+        for (int i = tid; i < p.num_buckets * MT * 16; i += kThreadsF) {
             const int b = i / (MT * 16), r = i - b * (MT * 16);
             t[i] = r < rows ? bias_log2<T>(__ldg(p.table + static_cast<int64_t>(b) * p.H + head_of(p, r))) : 0.f;
         }
-        for (int i = tid; i <= 2 * p.D; i += kFewThreads) m[i] = static_cast<uint8_t>(bucket_of(p, i - p.D));   // -1: 255
+        if constexpr (kMap)
+            for (int i = tid; i <= 2 * p.D; i += kThreadsF) m[i] = static_cast<uint8_t>(bucket_of(p, i - p.D));   // -1: 255
         q_min = INT_MAX;
         q_max = INT_MIN;
         for (int i = 0; i < s.q_len; ++i) {
@@ -140,14 +152,15 @@ struct Few {
                 mma_attn::ldmatrix_x4(qf[t2][ks], sQ + mma_attn::swz(t2 * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), 2 * ks + (lane >> 4)));
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                left[t2][k] = entry(t2 * 16 + g + 8 * k, 0);
-                right[t2][k] = entry(t2 * 16 + g + 8 * k, 2 * p.D);
+                left[t2][k] = entry(p, t2 * 16 + g + 8 * k, -p.D);
+                right[t2][k] = entry(p, t2 * 16 + g + 8 * k, p.D);
             }
         }
     }
-    __device__ __forceinline__ float entry(int row, int index) const {
-        const int b = map[index];
-        return b == 255 ? 0.f : tab[b * (MT * 16) + row];
+    // Bias of a row for a clamped distance.
+    __device__ __forceinline__ float entry(const Problem& p, int row, int d) const {
+        const int b = kMap ? static_cast<int8_t>(map[d + p.D]) : bucket_of(p, d);
+        return b < 0 ? 0.f : tab[b * (MT * 16) + row];
     }
     __device__ __forceinline__ uint32_t stage(int n) const { return ring + (n % kFewStages) * kStage; }
     // One block of keys (and values, positions) into stage n of this warp's ring.
@@ -217,7 +230,7 @@ struct Few {
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const int d = max(-p.D, min(p.D, pos_diff(pk, pq[t][k])));
-                            x[t][i][2 * k + j] = fmaf(x[t][i][2 * k + j], p.scale_log2, entry(t * 16 + g + 8 * k, d + p.D));
+                            x[t][i][2 * k + j] = fmaf(x[t][i][2 * k + j], p.scale_log2, entry(p, t * 16 + g + 8 * k, d));
                         }
                 }
         }
@@ -234,23 +247,23 @@ struct Few {
 };
 
 // grid (splits, Hkv, B), cluster (splits, 1, 1)
-template <typename T, int MT>
-__global__ void __launch_bounds__(kFewThreads) bias_few_kernel(const Problem p, uint16_t* __restrict__ out, int64_t out_tok) {
+template <typename T, int MT, int NW>
+__global__ void __launch_bounds__(32 * NW) bias_few_kernel(const Problem p, uint16_t* __restrict__ out, int64_t out_tok) {
     extern __shared__ __align__(128) uint8_t few_smem[];
-    __shared__ float s_m[kFewWarps][MT * 16], s_l[kFewWarps][MT * 16];
+    __shared__ float s_m[NW][MT * 16], s_l[NW][MT * 16];
     __shared__ float s_mc[MT * 16], s_lc[MT * 16];
     const int splits = gridDim.x, rank = blockIdx.x;
-    Few<T, MT, false> f;
+    Few<T, MT, NW, false> f;
     f.z = blockIdx.y;
     if (!read_pair(p, blockIdx.z, f.s) || f.s.q_len == 0) return;   // the same for the whole cluster
     f.begin(p, few_smem);
     const int blocks = (f.s.k_len + kFewKeys - 1) / kFewKeys;
-    const int per = (blocks + splits * kFewWarps - 1) / (splits * kFewWarps);   // of one warp
+    const int per = (blocks + splits * NW - 1) / (splits * NW);   // of one warp
     // A CTA's blocks are one run of keys; its warps take them in turn.
-    const int first = min(blocks, rank * per * kFewWarps) + f.warp, end = min(blocks, (rank + 1) * per * kFewWarps);
+    const int first = min(blocks, rank * per * NW) + f.warp, end = min(blocks, (rank + 1) * per * NW);
 #pragma unroll
     for (int n = 0; n < kFewStages - 1; ++n) {
-        if (first + n * kFewWarps < end) f.load(p, n, (first + n * kFewWarps) * kFewKeys);
+        if (first + n * NW < end) f.load(p, n, (first + n * NW) * kFewKeys);
         cp_async_commit();
     }
     f.setup(p, few_smem);
@@ -265,10 +278,10 @@ __global__ void __launch_bounds__(kFewThreads) bias_few_kernel(const Problem p, 
             for (int j = 0; j < 4; ++j) o[t][i][j] = 0.f;
     }
     int n = 0;
-    for (int blk = first; blk < end; blk += kFewWarps, ++n) {
+    for (int blk = first; blk < end; blk += NW, ++n) {
         cp_async_wait<kFewStages - 2>();
         __syncwarp();
-        const int ahead = blk + (kFewStages - 1) * kFewWarps;
+        const int ahead = blk + (kFewStages - 1) * NW;
         if (ahead < end) f.load(p, n + kFewStages - 1, ahead * kFewKeys);
         cp_async_commit();
         float x[MT][2][4];
@@ -349,15 +362,15 @@ __global__ void __launch_bounds__(kFewThreads) bias_few_kernel(const Problem p, 
         }
     __syncthreads();
     const int rows = f.rows;
-    for (int i = threadIdx.x; i < rows * 64; i += kFewThreads) {
+    for (int i = threadIdx.x; i < rows * 64; i += (32 * NW)) {
         const int r = i >> 6, d = i & 63;
         float top = s_m[0][r];
 #pragma unroll
-        for (int w = 1; w < kFewWarps; ++w) top = fmaxf(top, s_m[w][r]);
+        for (int w = 1; w < NW; ++w) top = fmaxf(top, s_m[w][r]);
         const float ref = top == -INFINITY ? 0.f : top;
         float acc = 0.f, sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) {
+        for (int w = 0; w < NW; ++w) {
             const float a = mma_attn::fast_exp2(s_m[w][r] - ref);
             acc = fmaf(a, so[(w * MT * 16 + r) * 64 + d], acc);
             sum = fmaf(a, s_l[w][r], sum);
@@ -370,7 +383,7 @@ __global__ void __launch_bounds__(kFewThreads) bias_few_kernel(const Problem p, 
     }
     if (splits > 1) cluster_sync();
     else __syncthreads();
-    for (int i = rank * kFewThreads + threadIdx.x; i < rows * 32; i += splits * kFewThreads) {
+    for (int i = rank * (32 * NW) + threadIdx.x; i < rows * 32; i += splits * (32 * NW)) {
         const int r = i >> 5, d = (i & 31) * 2;
         float a0, a1, sum, top;
         if (splits == 1) {
@@ -408,23 +421,23 @@ __global__ void __launch_bounds__(kFewThreads) bias_few_kernel(const Problem p, 
 }
 
 // weight[h, j] = prev[h, j] + sum_i exp(s[i, j] - lse_i).  grid (splits, Hkv, B)
-template <typename T, int MT>
-__global__ void __launch_bounds__(kFewThreads)
+template <typename T, int MT, int NW>
+__global__ void __launch_bounds__(32 * NW)
     bias_few_weight_kernel(const Problem p, const float* prev, float* weight, int64_t weight_stride) {
     extern __shared__ __align__(128) uint8_t few_smem[];
-    __shared__ float s_p[kFewWarps][MT * 16][kFewKeys + 1];
+    __shared__ float s_p[NW][MT * 16][kFewKeys + 1];
     const int splits = gridDim.x, rank = blockIdx.x;
-    Few<T, MT, true> f;
+    Few<T, MT, NW, true> f;
     f.z = blockIdx.y;
     if (!read_pair(p, blockIdx.z, f.s) || f.s.k_len == 0) return;
     const int blocks = (f.s.k_len + kFewKeys - 1) / kFewKeys;
-    const int per = (blocks + splits * kFewWarps - 1) / (splits * kFewWarps);
-    const int begin = min(blocks, rank * per * kFewWarps), end = min(blocks, (rank + 1) * per * kFewWarps);
+    const int per = (blocks + splits * NW - 1) / (splits * NW);
+    const int begin = min(blocks, rank * per * NW), end = min(blocks, (rank + 1) * per * NW);
     if (begin >= end) return;
     const int64_t at = f.z * p.group * weight_stride + f.s.k_start;
     if (f.s.q_len == 0) {   // nothing to add
         for (int h = 0; h < p.group; ++h)
-            for (int j = begin * kFewKeys + threadIdx.x; j < min(end * kFewKeys, f.s.k_len); j += kFewThreads)
+            for (int j = begin * kFewKeys + threadIdx.x; j < min(end * kFewKeys, f.s.k_len); j += (32 * NW))
                 weight[at + h * weight_stride + j] = prev != nullptr ? prev[at + h * weight_stride + j] : 0.f;
         return;
     }
@@ -441,7 +454,7 @@ __global__ void __launch_bounds__(kFewThreads)
     };
 #pragma unroll
     for (int n = 0; n < kFewStages - 1; ++n) {
-        if (first + n * kFewWarps < end) load(n, first + n * kFewWarps);
+        if (first + n * NW < end) load(n, first + n * NW);
         cp_async_commit();
     }
     f.setup(p, few_smem);
@@ -454,10 +467,10 @@ __global__ void __launch_bounds__(kFewThreads)
             lse[t][k] = r < f.rows ? lse_log2(__ldg(p.lse + f.head_of(p, r) * p.lse_stride + f.s.q_start + f.query_of(r))) : INFINITY;
         }
     int n = 0;
-    for (int blk = first; blk < end; blk += kFewWarps, ++n) {
+    for (int blk = first; blk < end; blk += NW, ++n) {
         cp_async_wait<kFewStages - 2>();
         __syncwarp();
-        const int ahead = blk + (kFewStages - 1) * kFewWarps;
+        const int ahead = blk + (kFewStages - 1) * NW;
         if (ahead < end) load(n + kFewStages - 1, ahead);
         cp_async_commit();
         float x[MT][2][4];

@@ -74,6 +74,14 @@ def test_queries_against_a_longer_cache(lens_q, lens_k, H, Hkv, dtype, where):
     compare(s, run_all(s))
 
 
+@pytest.mark.parametrize("where", ["none", "sorted", "shuffled", "far", "equal"])
+@pytest.mark.parametrize("H,Hkv,D,nb", [(2, 2, 1024, 32), (4, 1, 16, 50), (3, 3, 0, 1), (2, 1, 200, 64)])
+@pytest.mark.parametrize("lens_q,lens_k", [([7, 3, 12], [7, 3, 12]), ([2, 8, 1, 0], [128, 16, 3, 5])], ids=str)
+def test_short_sequences(lens_q, lens_k, H, Hkv, D, nb, where):
+    s = ref.problem(lens_q, lens_k, H, Hkv, F16 if nb % 4 else BF16, nb, D, where=where, layout="rows", seed=D)
+    compare(s, run_all(s))
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_long_sequence(dtype):
     s = ref.problem([2049, 100], [2049, 100], 1, 1, dtype, 32, 128)
