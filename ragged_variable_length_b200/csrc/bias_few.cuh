@@ -91,7 +91,8 @@ struct Few {
     uint32_t ring;
     const uint8_t* map;
     const float* tab;                 // [num_buckets][MT * 16]
-    const uint16_t *kb, *vb;
+    const uint16_t* kb;
+    int64_t v_off;                    // from a key's row to its value's, elements
 
     __device__ __forceinline__ int head_of(const Problem& p, int row) const { return z * p.group + row / s.q_len; }
     __device__ __forceinline__ int query_of(int row) const { return row % s.q_len; }
@@ -106,7 +107,7 @@ struct Few {
         ring = smem_addr(smem) + warp * kFewStages * kStage;
         const int64_t head = z * p.kv_head;
         kb = p.k + s.k_start * p.kv_tok + head;
-        vb = p.v + s.k_start * p.kv_tok + head;
+        v_off = static_cast<int64_t>(reinterpret_cast<intptr_t>(p.v) - reinterpret_cast<intptr_t>(p.k)) / 2;
     }
     // What the scores need (the first blocks are on their way meanwhile).
     __device__ __forceinline__ void setup(const Problem& p, uint8_t* smem) {
@@ -165,20 +166,32 @@ struct Few {
     __device__ __forceinline__ uint32_t stage(int n) const { return ring + (n % kFewStages) * kStage; }
     // One block of keys (and values, positions) into stage n of this warp's ring.
     __device__ __forceinline__ void load(const Problem& p, int n, int key0) const {
-        const uint32_t st = stage(n);
         const int r = lane >> 3, c = lane & 7;
+        const uint32_t st = stage(n), even = st + mma_attn::swz(r, c), odd = st + mma_attn::swz(r + 4, c);
+        const uint16_t* k = kb + static_cast<int64_t>(key0 + r) * p.kv_tok + c * 8;
+        const int64_t four = 4 * p.kv_tok;
+        if (key0 + kFewKeys <= s.k_len) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = key0 + r + 4 * i;
-            const bool in = row < s.k_len;
-            const int64_t off = static_cast<int64_t>(in ? row : 0) * p.kv_tok + c * 8;
-            cp_async_16(st + mma_attn::swz(r + 4 * i, c), kb + off, in ? 16 : 0);
-            if constexpr (!WEIGHT) cp_async_16(st + kFewKeys * 128 + mma_attn::swz(r + 4 * i, c), vb + off, in ? 16 : 0);
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t dst = ((i & 1) ? odd : even) + (i >> 1) * 1024;
+                cp_async_16(dst, k, 16);
+                if constexpr (!WEIGHT) cp_async_16(dst + kFewKeys * 128, k + v_off, 16);
+                k += four;
+            }
+            if (p.pos_k != nullptr && lane < kFewKeys)
+                cp_async_4(st + kStage - kFewKeys * 4 + 4 * lane, p.pos_k + s.k_start + key0 + lane, 4);
+            return;
         }
-        if (p.pos_k != nullptr && lane < kFewKeys) {
-            const int row = min(key0 + lane, s.k_len - 1);   // past the end: a position of the block
-            cp_async_4(st + kStage - kFewKeys * 4 + 4 * lane, p.pos_k + s.k_start + row, 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // past the end: zeros
+            const bool in = key0 + r + 4 * i < s.k_len;
+            const uint32_t dst = ((i & 1) ? odd : even) + (i >> 1) * 1024;
+            cp_async_16(dst, in ? k : kb, in ? 16 : 0);
+            if constexpr (!WEIGHT) cp_async_16(dst + kFewKeys * 128, in ? k + v_off : kb, in ? 16 : 0);
+            k += four;
         }
+        if (p.pos_k != nullptr && lane < kFewKeys)   // past the end: a position of the block
+            cp_async_4(st + kStage - kFewKeys * 4 + 4 * lane, p.pos_k + s.k_start + min(key0 + lane, s.k_len - 1), 4);
     }
     // Scores in base 2 of block n (keys from key0): x[tile][8 keys][row g: 2 columns, row g + 8: 2 columns].
     __device__ __forceinline__ void scores(const Problem& p, int n, int key0, float (&x)[MT][2][4]) const {
@@ -446,11 +459,11 @@ __global__ void __launch_bounds__(32 * NW)
     // The weights so far travel with the keys: [head][16 keys] of a stage, where there are any.
     auto load = [&](int n, int blk) {
         f.load(p, n, blk * kFewKeys);
-        if (prev != nullptr)
-            for (int i = f.lane; i < p.group * kFewKeys; i += 32) {
-                const int h = i / kFewKeys, j = blk * kFewKeys + i % kFewKeys;
-                cp_async_4(f.stage(n) + kFewKeys * 128 + 4 * i, prev + at + h * weight_stride + min(j, f.s.k_len - 1), 4);
-            }
+        if (prev != nullptr) {
+            const float* src = prev + at + (f.lane >> 4) * weight_stride + min(blk * kFewKeys + (f.lane & 15), f.s.k_len - 1);
+            uint32_t dst = f.stage(n) + kFewKeys * 128 + 4 * f.lane;
+            for (int h = f.lane >> 4; h < p.group; h += 2, src += 2 * weight_stride, dst += 128) cp_async_4(dst, src, 4);
+        }
     };
 #pragma unroll
     for (int n = 0; n < kFewStages - 1; ++n) {
@@ -484,16 +497,20 @@ __global__ void __launch_bounds__(32 * NW)
                     s_p[f.warp][t * 16 + f.g + 8 * (j >> 1)][i * 8 + f.c2 + (j & 1)] = mma_attn::fast_exp2(x[t][i][j] - lse[t][j >> 1]);
         __syncwarp();
         // Key lane % 16 of heads lane / 16, + 2, ...: this block's sums over the queries, in their order.
-        const int key = f.lane & 15, j = blk * kFewKeys + key;
-        if (j < f.s.k_len)
-            for (int h = f.lane >> 4; h < p.group; h += 2) {
-                float sum = 0.f;
-                for (int q = 0; q < f.s.q_len; ++q) sum += s_p[f.warp][h * f.s.q_len + q][key];
+        const int key = f.lane & 15, h0 = f.lane >> 4, j = blk * kFewKeys + key;
+        if (j < f.s.k_len) {
+            float* dst = weight + at + h0 * weight_stride + j;
+            const float* sp = &s_p[f.warp][h0 * f.s.q_len][key];
+            uint32_t old_at = f.stage(n) + kFewKeys * 128 + 4 * f.lane;
+            const int skip = f.s.q_len * (kFewKeys + 1);
+            for (int h = h0; h < p.group; h += 2, dst += 2 * weight_stride, sp += 2 * skip, old_at += 128) {
+                float sum = sp[0];
+                for (int q = 1; q < f.s.q_len; ++q) sum += sp[q * (kFewKeys + 1)];
                 float old = 0.f;
-                if (prev != nullptr)
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(old) : "r"(f.stage(n) + kFewKeys * 128 + 4 * (h * kFewKeys + key)) : "memory");
-                weight[at + h * weight_stride + j] = old + sum;
+                if (prev != nullptr) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(old) : "r"(old_at) : "memory");
+                *dst = old + sum;
             }
+        }
         __syncwarp();   // the stage and s_p may be overwritten
     }
     cp_async_wait<0>();
