@@ -250,18 +250,31 @@ ragged_status launch_bias_bwd(const ragged::bias::Problem& p, ragged::bias::BwdA
     if (st != RAGGED_OK) return st;
     a.span = bias_span(p.D, bwd_kv_fixed_bytes(), 3);
     a.heads = a.parts > 1 ? 1 : heads_per_cta(p.B * tiles128(avg_k), p.Hkv, (avg_q + kTile - 1) / kTile * p.group, slots);
-    bias_bwd_kv_kernel<T><<<bias_grid(tiles128(p.max_k) * a.parts, (p.Hkv + a.heads - 1) / a.heads, p.B), kBwdThreads,
-                            bwd_kv_smem_bytes(p.D, a.span), s>>>(p, a);
-    st = cuda_check(cudaGetLastError(), "key and value gradient launch");
-    if (st != RAGGED_OK) return st;
-    if (a.parts > 1) {
-        const int64_t blocks = std::min<int64_t>((static_cast<int64_t>(p.max_k) * p.Hkv * 16 + 255) / 256, 8LL * sm_count());
-        bias_bwd_parts_kernel<T><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(p.B)), 256, 0, s>>>(p, a);
-        st = cuda_check(cudaGetLastError(), "key and value gradient sum launch");
-        if (st != RAGGED_OK) return st;
+    cudaLaunchConfig_t cfg{};
+    // The table's sums go to CTAs of this launch where a column or a slice of its
+    // grid has enough of them (32,768 values each) and not too many.
+    const int64_t columns = tiles128(p.max_k) * a.parts, groups = (p.Hkv + a.heads - 1) / a.heads;
+    const int64_t values = static_cast<int64_t>(p.num_buckets) * p.H * p.B * a.q_tiles, most = std::max<int64_t>(32, columns * groups * p.B / 16);
+    auto fits = [&](int64_t ctas) { return ctas * 32768 >= values && ctas <= most; };
+    a.table_in = p.B < 65535 && fits(columns * groups) ? kSlice : fits(groups * p.B) ? kColumn : kOwnLaunch;
+    cfg.gridDim = bias_grid(columns + (a.table_in == kColumn), static_cast<int>(groups), p.B + (a.table_in == kSlice));
+    cfg.blockDim = dim3(kBwdThreads);
+    cfg.dynamicSmemBytes = bwd_kv_smem_bytes(p.D, a.span);
+    cfg.stream = s;
+    cudaLaunchAttribute early{};   // may start before the query kernel has ended; waits for it itself
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    st = cuda_check(cudaLaunchKernelEx(&cfg, bias_bwd_kv_kernel<T>, p, a), "key and value gradient launch");
+    if (st == RAGGED_OK && a.table_in == kOwnLaunch) {
+        bias_bwd_table_kernel<T><<<static_cast<unsigned>((p.num_buckets * static_cast<int64_t>(p.H) + 7) / 8), 256, 0, s>>>(p, a);
+        st = cuda_check(cudaGetLastError(), "table gradient launch");
     }
-    bias_bwd_table_kernel<T><<<bias_grid(p.num_buckets, p.H, 1), 256, 0, s>>>(p, a);
-    return cuda_check(cudaGetLastError(), "table gradient launch");
+    if (st != RAGGED_OK || a.parts == 1) return st;
+    const int64_t blocks = std::min<int64_t>((static_cast<int64_t>(p.max_k) * p.Hkv * 16 + 255) / 256, 8LL * sm_count());
+    bias_bwd_parts_kernel<T><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(p.B)), 256, 0, s>>>(p, a);
+    return cuda_check(cudaGetLastError(), "key and value gradient sum launch");
 }
 
 template <typename T>

@@ -38,6 +38,10 @@ constexpr int kPExp = 14, kSExp = 6;
 // 2^e for |e| up to 126.
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
+// Where the table's gradient is summed up: by a launch of its own, or by CTAs
+// of the key-row kernel beyond the last key tile, or beyond the last sequence.
+enum TableIn { kOwnLaunch = 0, kColumn = 1, kSlice = 2 };
+
 struct BwdArgs {
     const uint16_t* out;
     const uint16_t* dout;
@@ -48,13 +52,14 @@ struct BwdArgs {
     int64_t dq_tok, dq_head, dkv_tok, dkv_head;
     float* delta;     // [H, lse_stride]
     int* tile_exp;    // [B][H][query tiles][4 warps]: exponent of the largest |dO|
-    float* partial;   // [B][H][query tiles][num_buckets]
+    float* partial;   // [H][num_buckets][B][query tiles]
     uint16_t* dtable;
     int q_tiles;
     int span, heads;  // of a launch: positions of its expanded table, heads per CTA
     // Key rows in parts (where the grid would not fill the GPU): queries of a
     // part, and the parts' fp32 sums [part][B * key rows][Hkv][dK, dV][64].
     int parts;
+    int table_in;        // the key-row kernel's CTAs for the table, if any
     float* part_sums;
     int64_t part_rows;   // key rows per sequence, a multiple of 128
 };
@@ -82,6 +87,13 @@ __device__ __forceinline__ void finish_cta256(const uint32_t* s_tmem, uint32_t c
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*s_tmem), "r"(cols) : "memory");
     }
 }
+// The key-row kernel is launched while the query-row kernel still runs: its
+// CTAs come up as the other's last ones leave, prepare what does not depend on
+// it, and wait here for its end before they read delta, the exponents or the
+// tiles' sums.  (Bounded waits of the other warps meanwhile last a second.)
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // 32 of a row's 64 fp32 columns at taddr, times f, rounded and stored.
 template <typename T>
 __device__ __forceinline__ void store_tmem_half(uint32_t taddr, float f, uint16_t* dst, bool valid) {
@@ -155,15 +167,16 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
 
+    let_next_start();
     const int q0 = blockIdx.x * kQTile, h0 = blockIdx.y * a.heads, b = blockIdx.z;
     const int nh = min(a.heads, p.H - h0);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t item0 = (static_cast<int64_t>(b) * p.H + h0) * a.q_tiles + blockIdx.x;   // + i * q_tiles
+    const int64_t sums = static_cast<int64_t>(p.B) * a.q_tiles, sum0 = static_cast<int64_t>(b) * a.q_tiles + blockIdx.x;
     Seq s;
     const bool any = read_pair(p, b, s) && q0 < s.q_len;
     if (!any || s.k_len == 0) {   // nothing for the table; queries without keys get no gradient
-        for (int i = tid; i < nh * p.num_buckets; i += kBwdThreads)
-            a.partial[(item0 + static_cast<int64_t>(i / p.num_buckets) * a.q_tiles) * p.num_buckets + i % p.num_buckets] = 0.f;
+        for (int i = tid; i < nh * p.num_buckets; i += kBwdThreads) a.partial[(h0 * p.num_buckets + i) * sums + sum0] = 0.f;
         if (any)
             for (int i = tid; i < nh * kQTile; i += kBwdThreads) {
                 const int r = q0 + i % kQTile;
@@ -331,7 +344,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                     }
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if (lane == 0) a.partial[(item0 + static_cast<int64_t>(i) * a.q_tiles) * p.num_buckets + n] = sum;
+                    if (lane == 0) a.partial[((h0 + i) * p.num_buckets + n) * sums + sum0] = sum;
                 }
             }
             if (more) bias_fill<kBwdRows>(t, ids, s_tab);
@@ -483,8 +496,30 @@ __host__ __device__ constexpr int bwd_kv_smem_bytes(int D, int span) {
     return bwd_kv_fixed_bytes() + vec16_bytes(D, span) + ids_bytes(D, span);
 }
 
+// dtable[n, h] = sum of the tiles' sums, in a fixed order: entries id, id + n_ids,
+// ... by the CTA's warps.
+template <typename T>
+__device__ __forceinline__ void table_gradient(const Problem& p, const BwdArgs& a, int id, int n_ids) {
+    const int lane = threadIdx.x & 31, warps = blockDim.x / 32, n = p.B * a.q_tiles, all = p.num_buckets * p.H;
+    for (int e = id * warps + (threadIdx.x >> 5); e < all; e += n_ids * warps) {
+        const float* src = a.partial + static_cast<int64_t>(e) * n;
+        float x = 0.f;
+#pragma unroll 4
+        for (int i = lane; i < n; i += 32) x += __ldcg(src + i);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        const int h = e / p.num_buckets;
+        if (lane == 0) a.dtable[static_cast<int64_t>(e - h * p.num_buckets) * p.H + h] = from_float<T>(x);
+    }
+}
+template <typename T>
+__global__ void __launch_bounds__(256) bias_bwd_table_kernel(const Problem p, const BwdArgs a) {
+    table_gradient<T>(p, a, blockIdx.x, gridDim.x);
+}
+
 // Key rows: dK and dV, over the query tiles of every query head of a key head.
-// grid (key tiles * parts, groups of key heads, B), two CTAs per SM.
+// grid (key tiles * parts, groups of key heads, B), two CTAs per SM, and a
+// column or a slice of CTAs that sums up the table's gradient.
 //
 // TMEM (256 columns): S^T and dP^T (each half replaced in place by its P^T,
 // dS^T), dK and dV.
@@ -500,6 +535,14 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
 
+    // One column, or one slice, of CTAs more: the table's gradient.
+    if (a.table_in == kColumn ? blockIdx.x == gridDim.x - 1 : a.table_in == kSlice && blockIdx.z == gridDim.z - 1) {
+        wait_for_last();
+        const int other = a.table_in == kSlice ? blockIdx.x : blockIdx.z, others = a.table_in == kSlice ? gridDim.x : gridDim.z;
+        table_gradient<T>(p, a, blockIdx.y + gridDim.y * other, gridDim.y * others);
+        return;
+    }
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) wait_for_last();   // this grid never ends before the other
     const int part = blockIdx.x % a.parts, k0 = (blockIdx.x / a.parts) * kQTile, z0 = blockIdx.y * a.heads, b = blockIdx.z;
     const int nz = min(a.heads, p.Hkv - z0);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -650,6 +693,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
         cols.store(t, t0 * kTile, s.q_len);
         const uint32_t tmem = start_rows256(&s_tmem);
         const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        wait_for_last();   // delta and the exponents
         bool ok = true;
         uint32_t g = 0;
         const float shift = kScaled<T> ? static_cast<float>(kPExp) : 0.f;
@@ -820,27 +864,6 @@ __global__ void __launch_bounds__(256) bias_bwd_parts_kernel(const Problem p, co
         }
         uint16_t* dst = (c < 8 ? a.dk : a.dv) + (s.k_start + row) * a.dkv_tok + z * a.dkv_head + (c & 7) * 8;
         *reinterpret_cast<uint4*>(dst) = make_uint4(Cvt<T>::pack(v[0], v[1]), Cvt<T>::pack(v[2], v[3]), Cvt<T>::pack(v[4], v[5]), Cvt<T>::pack(v[6], v[7]));
-    }
-}
-
-// dtable[n, h] = sum of the tiles' sums, in a fixed order.  grid (num_buckets, H)
-template <typename T>
-__global__ void __launch_bounds__(256) bias_bwd_table_kernel(const Problem p, const BwdArgs a) {
-    __shared__ float s_sum[8];
-    const int n = blockIdx.x, h = blockIdx.y, tiles = a.q_tiles;
-    float x = 0.f;
-    for (int i = threadIdx.x; i < p.B * tiles; i += 256) {
-        const int b = i / tiles, t = i - b * tiles;
-        x += a.partial[((static_cast<int64_t>(b) * p.H + h) * tiles + t) * p.num_buckets + n];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = x;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        x = 0.f;
-        for (int w = 0; w < 8; ++w) x += s_sum[w];
-        a.dtable[static_cast<int64_t>(n) * p.H + h] = from_float<T>(x);
     }
 }
 
