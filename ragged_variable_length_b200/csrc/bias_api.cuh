@@ -88,11 +88,12 @@ int64_t bwd_parts(const ragged_bias_attn* a) {
 }
 // Workspace of the backward pass: delta [H, lse_stride] floats, four exponents per
 // (sequence, head, query tile), the tiles' sums for the table's gradient
-// [B, H, query tiles, num_buckets], and the parts' sums of dK and dV.
+// [H, num_buckets, B, query tiles], an exponent per (sequence, key head, key tile),
+// and the parts' sums of dK and dV.
 int64_t bwd_delta_floats(const ragged_bias_attn* a) { return (a->H * a->lse_stride + 3) & ~int64_t(3); }
 int64_t bwd_items(const ragged_bias_attn* a) { return a->B * a->H * tiles128(a->max_seqlen_q); }
 int64_t bwd_small_floats(const ragged_bias_attn* a) {
-    return (bwd_delta_floats(a) + bwd_items(a) * (4 + a->num_buckets) + 3) & ~int64_t(3);
+    return (bwd_delta_floats(a) + bwd_items(a) * (4 + a->num_buckets) + a->B * a->Hkv * tiles128(a->max_seqlen_k) + 3) & ~int64_t(3);
 }
 int64_t bwd_workspace(const ragged_bias_attn* a) {
     const int64_t parts = bwd_parts(a);
@@ -244,13 +245,25 @@ ragged_status launch_bias_bwd(const ragged::bias::Problem& p, ragged::bias::BwdA
     const int64_t slots = 2LL * sm_count();
     a.span = bias_span(p.D, bwd_q_fixed_bytes(p.num_buckets, stages), 3);
     a.heads = heads_per_cta(p.B * tiles128(avg_q), p.H, (avg_k + kTile - 1) / kTile, slots);
-    q_kernel<<<bias_grid(a.q_tiles, (p.H + a.heads - 1) / a.heads, p.B), kBwdThreads,
-               bwd_q_smem_bytes(p.D, p.num_buckets, a.span, stages), s>>>(p, a);
-    st = cuda_check(cudaGetLastError(), "query gradient launch");
+    cudaLaunchAttribute early{};   // the kernel may start before the one ahead of it has ended, and waits for it itself
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kBwdThreads);
+    cfg.stream = s;
+    cfg.attrs = &early;
+    if (kScaled<T>) {
+        bias_bwd_value_kernel<T><<<bias_grid(a.k_tiles, p.Hkv, p.B), 256, 0, s>>>(p, a);
+        st = cuda_check(cudaGetLastError(), "value exponent launch");
+        if (st != RAGGED_OK) return st;
+        cfg.numAttrs = 1;
+    }
+    cfg.gridDim = bias_grid(a.q_tiles, (p.H + a.heads - 1) / a.heads, p.B);
+    cfg.dynamicSmemBytes = bwd_q_smem_bytes(p.D, p.num_buckets, a.span, stages);
+    st = cuda_check(cudaLaunchKernelEx(&cfg, q_kernel, p, a), "query gradient launch");
     if (st != RAGGED_OK) return st;
     a.span = bias_span(p.D, bwd_kv_fixed_bytes(), 3);
     a.heads = a.parts > 1 ? 1 : heads_per_cta(p.B * tiles128(avg_k), p.Hkv, (avg_q + kTile - 1) / kTile * p.group, slots);
-    cudaLaunchConfig_t cfg{};
     // The table's sums go to CTAs of this launch where a column or a slice of its
     // grid has enough of them (32,768 values each) and not too many.
     const int64_t columns = tiles128(p.max_k) * a.parts, groups = (p.Hkv + a.heads - 1) / a.heads;
@@ -258,13 +271,7 @@ ragged_status launch_bias_bwd(const ragged::bias::Problem& p, ragged::bias::BwdA
     auto fits = [&](int64_t ctas) { return ctas * 32768 >= values && ctas <= most; };
     a.table_in = p.B < 65535 && fits(columns * groups) ? kSlice : fits(groups * p.B) ? kColumn : kOwnLaunch;
     cfg.gridDim = bias_grid(columns + (a.table_in == kColumn), static_cast<int>(groups), p.B + (a.table_in == kSlice));
-    cfg.blockDim = dim3(kBwdThreads);
     cfg.dynamicSmemBytes = bwd_kv_smem_bytes(p.D, a.span);
-    cfg.stream = s;
-    cudaLaunchAttribute early{};   // may start before the query kernel has ended; waits for it itself
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &early;
     cfg.numAttrs = 1;
     st = cuda_check(cudaLaunchKernelEx(&cfg, bias_bwd_kv_kernel<T>, p, a), "key and value gradient launch");
     if (st == RAGGED_OK && a.table_in == kOwnLaunch) {
@@ -430,6 +437,8 @@ ragged_status ragged_attn_bias_bwd(const ragged_bias_attn* a, const void* out, i
     g.delta = ws;
     g.tile_exp = reinterpret_cast<int*>(ws + bwd_delta_floats(a));
     g.partial = ws + bwd_delta_floats(a) + 4 * bwd_items(a);
+    g.v_exp = reinterpret_cast<int*>(g.partial + bwd_items(a) * a->num_buckets);
+    g.k_tiles = static_cast<int>(tiles128(a->max_seqlen_k));
     g.dtable = static_cast<uint16_t*>(dtable);
     g.q_tiles = static_cast<int>(tiles128(a->max_seqlen_q));
     g.parts = static_cast<int>(bwd_parts(a));

@@ -15,9 +15,11 @@
 //
 // dS and P are rounded to the 16-bit type to be operands of the next product.
 // In f16 they would lose what lies below 2^-14: probabilities of long rows,
-// and gradients far below 1.  Both are therefore scaled by powers of two, which
-// the accumulators undo exactly: P by 2^14, dS by 2^(6 - e) with e the exponent
-// of the largest |dO| of the row (dQ), or of all rows that a key meets (dK).
+// and gradients far below 1; and a large V would push dS past 65504.  Both are
+// therefore scaled by powers of two, which the accumulators undo exactly: P by
+// 2^14, dS by 2^(14 - e - f).  2^e is above the norm of the row's dO (dQ), or
+// of every dO that a key meets (dK), 2^f above the norm of every row of V:
+// |dP| and |delta| are below 2^(e + f), so |dS| stays below 2^15.
 #pragma once
 
 #include "bias_tc.cuh"
@@ -29,14 +31,17 @@ constexpr int kBwdRows = 256;                   // row threads
 constexpr int kBwdThreads = kBwdRows + 64;      // and the MMA and load warps
 constexpr int kBwdMmaWarp = 8, kBwdLoadWarp = 9;
 constexpr int kBwdStages = 3;
-constexpr int kNoExp = -1000;                   // a row (or tile) of zero gradients
+constexpr int kNoExp = -1000;                   // of rows that are zero, or not finite
 
 template <typename T>
 constexpr bool kScaled = std::is_same<T, __half>::value;
-constexpr int kPExp = 14, kSExp = 6;
+constexpr int kPExp = 14, kSExp = 14;
 
 // 2^e for |e| up to 126.
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+// e with |x| < 2^e for a row x whose squares add up to ss.
+__device__ __forceinline__ int norm_exp(float ss) { return ss > 0.f && ss < INFINITY ? (ilogbf(ss) >> 1) + 1 : kNoExp; }
 
 // Where the table's gradient is summed up: by a launch of its own, or by CTAs
 // of the key-row kernel beyond the last key tile, or beyond the last sequence.
@@ -51,10 +56,11 @@ struct BwdArgs {
     uint16_t* dv;
     int64_t dq_tok, dq_head, dkv_tok, dkv_head;
     float* delta;     // [H, lse_stride]
-    int* tile_exp;    // [B][H][query tiles][4 warps]: exponent of the largest |dO|
+    int* tile_exp;    // [B][H][query tiles][4 warps]: exponent e of the rows of dO, plus f (f16)
+    int* v_exp;       // [B][Hkv][key tiles]: exponent f of the rows of V (f16)
     float* partial;   // [H][num_buckets][B][query tiles]
     uint16_t* dtable;
-    int q_tiles;
+    int q_tiles, k_tiles;
     int span, heads;  // of a launch: positions of its expanded table, heads per CTA
     // Key rows in parts (where the grid would not fill the GPU): queries of a
     // part, and the parts' fp32 sums [part][B * key rows][Hkv][dK, dV][64].
@@ -146,6 +152,52 @@ __host__ __device__ constexpr int bwd_q_smem_bytes(int D, int num_buckets, int s
     return bwd_q_fixed_bytes(num_buckets, stages) + vec16_bytes(D, span) + ids_bytes(D, span);
 }
 
+// Exponent f of each tile of 128 rows of V (f16 only).  grid (key tiles, Hkv, B);
+// eight threads per row.  One read of V, which the next kernel finds in L2.
+template <typename T>
+__global__ void __launch_bounds__(256) bias_bwd_value_kernel(const Problem p, const BwdArgs a) {
+    __shared__ int s_top[8];
+    let_next_start();
+    const int k0 = blockIdx.x * kQTile, z = blockIdx.y, b = blockIdx.z;
+    Seq s;
+    if (!read_pair(p, b, s) || k0 >= s.k_len) return;
+    const int r0 = k0 + (threadIdx.x >> 3), lane = threadIdx.x & 31;
+    const uint16_t* src = p.v + (s.k_start + r0) * p.kv_tok + z * p.kv_head + (threadIdx.x & 7) * 8;
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = r0 + 32 * i < s.k_len ? __ldg(reinterpret_cast<const uint4*>(src + 32 * i * p.kv_tok)) : make_uint4(0, 0, 0, 0);
+    int top = kNoExp;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t xs[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        float ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float x0 = to_float<T>(static_cast<uint16_t>(xs[k])), x1 = to_float<T>(static_cast<uint16_t>(xs[k] >> 16));
+            ss = fmaf(x0, x0, fmaf(x1, x1, ss));
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        top = max(top, norm_exp(ss));
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) s_top[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) top = max(top, s_top[k]);
+    a.v_exp[(static_cast<int64_t>(b) * p.Hkv + z) * a.k_tiles + blockIdx.x] = top;
+}
+// Of every row of V of a sequence and key head, by one warp.
+__device__ __forceinline__ int value_exp(const Problem& p, const BwdArgs& a, int b, int z, int k_len) {
+    const int* src = a.v_exp + (static_cast<int64_t>(b) * p.Hkv + z) * a.k_tiles;
+    int top = kNoExp;
+    for (int i = threadIdx.x & 31; i < (k_len + kQTile - 1) / kQTile; i += 32) top = max(top, __ldcg(src + i));
+    top = __reduce_max_sync(0xffffffffu, top);
+    return top == kNoExp ? 0 : top;
+}
+
 // Query rows: dQ, delta, and each tile's sums for the table's gradient.
 // grid (query tiles, groups of heads, B), two CTAs per SM where the table is small.
 //
@@ -161,9 +213,9 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
     constexpr int kBars = 13;
     __shared__ __align__(8) uint64_t s_bar[kBars];
     __shared__ uint16_t s_tab[kMaxBuckets + 1];
-    __shared__ float s_delta[2][kQTile], s_undo[kQTile];
+    __shared__ float s_delta[2][kQTile], s_norm[2][kQTile], s_undo[kQTile];
     __shared__ __align__(16) TileInfo s_tiles[kChunkTiles];
-    __shared__ int s_red[16], s_exp[2][kQTile];
+    __shared__ int s_red[16];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
 
@@ -175,6 +227,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
     const int64_t sums = static_cast<int64_t>(p.B) * a.q_tiles, sum0 = static_cast<int64_t>(b) * a.q_tiles + blockIdx.x;
     Seq s;
     const bool any = read_pair(p, b, s) && q0 < s.q_len;
+    if (kScaled<T> && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) wait_for_last();   // never ends before the value kernel
     if (!any || s.k_len == 0) {   // nothing for the table; queries without keys get no gradient
         for (int i = tid; i < nh * p.num_buckets; i += kBwdThreads) a.partial[(h0 * p.num_buckets + i) * sums + sum0] = 0.f;
         if (any)
@@ -366,7 +419,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                 w[4 * c + 3] = qw[c].w;
             }
             tmem_st16_u(t_lane + q_col + half * 16, w);
-            float d = 0.f, big = 0.f;
+            float d = 0.f, ss = 0.f;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const uint32_t ys[4] = {dw[c].x, dw[c].y, dw[c].z, dw[c].w}, xs[4] = {ow[c].x, ow[c].y, ow[c].z, ow[c].w};
@@ -376,7 +429,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                     const float d0 = to_float<T>(static_cast<uint16_t>(ys[k])), d1 = to_float<T>(static_cast<uint16_t>(ys[k] >> 16));
                     d = fmaf(to_float<T>(static_cast<uint16_t>(xs[k])), d0, d);
                     d = fmaf(to_float<T>(static_cast<uint16_t>(xs[k] >> 16)), d1, d);
-                    if constexpr (kScaled<T>) big = fmaxf(big, fmaxf(fabsf(d0), fabsf(d1)));
+                    if constexpr (kScaled<T>) ss = fmaf(d0, d0, fmaf(d1, d1, ss));
                 }
             }
             tmem_st16_u(t_lane + do_col + half * 16, w);
@@ -384,10 +437,11 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
             fence_before_sync();
             mbar_arrive(qd_full);
             s_delta[half][r] = d;
-            if constexpr (kScaled<T>) s_exp[half][r] = big > 0.f && big < INFINITY ? ilogbf(big) + 1 : kNoExp;
+            if constexpr (kScaled<T>) s_norm[half][r] = ss;
             rows_barrier<kBwdRows>();   // entries, deltas and cleared sums are there
         };
         change(-1, true);
+        if constexpr (kScaled<T>) wait_for_last();   // the value kernel's exponents
         for (int i = 0; i < nh; ++i) {
             const int h = h0 + i;
             const float delta = s_delta[0][r] + s_delta[1][r];
@@ -395,8 +449,10 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
             float rs = 1.f;   // dS is kept times rs
             undo = 1.f;
             if constexpr (kScaled<T>) {
-                const int e = max(s_exp[0][r], s_exp[1][r]);
+                int e = norm_exp(s_norm[0][r] + s_norm[1][r]);
+                const int f = value_exp(p, a, b, h / p.group, s.k_len);
                 if (e != kNoExp) {
+                    e += f;
                     rs = pow2(kSExp - e);
                     undo = pow2(e - kSExp);
                 }
@@ -690,7 +746,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
         if (tid == p.num_buckets) s_tab[tid] = 0;
         bias_rows<kBwdRows>(t, p, pos, valid, a.span, s_red);
         bias_ids<-1, kBwdRows>(t, map, ids, p.num_buckets);
-        cols.store(t, t0 * kTile, s.q_len);
+        cols.store<true>(t, t0 * kTile, s.q_len);
         const uint32_t tmem = start_rows256(&s_tmem);
         const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         wait_for_last();   // delta and the exponents
@@ -784,7 +840,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
                         if (tile > 0) load_stats(c0);
                         if (again) cols.load(c0, s.q_len, query_at);
                         if (tile > 0) rows_barrier<kBwdRows>();
-                        if (again) cols.store(t, c0, s.q_len);
+                        if (again) cols.store<true>(t, c0, s.q_len);
                         store_stats(c0);
                         rows_barrier<kBwdRows>();
                     }
@@ -990,7 +1046,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         if (tid == p.num_buckets) s_tab[tid] = 0;
         bias_rows<128>(t, p, pos, valid, span, s_red);
         bias_ids<-1, 128>(t, map, ids, p.num_buckets);
-        cols.store(t, 0, s.q_len);
+        cols.store<true>(t, 0, s.q_len);
         const uint32_t tmem = start_rows(&s_tmem);
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         bool ok = true;
@@ -1021,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 3)
                     if (tile > 0) load_lse(c0);
                     if (again) cols.load(c0, s.q_len, query_at);
                     if (tile > 0) rows_barrier<128>();
-                    if (again) cols.store(t, c0, s.q_len);
+                    if (again) cols.store<true>(t, c0, s.q_len);
 #pragma unroll
                     for (int k = 0; k < kChunk / 128; ++k) {
                         const int c = tid + k * 128;

@@ -240,7 +240,11 @@ struct Columns {
             pos[k][1] = c + 32 < len ? pos_of(c + 32) : 0;
         }
     }
-    // Offsets and kinds; barriers around it are the caller's.
+    // Offsets and kinds; barriers around it are the caller's.  Places past the last
+    // column: with REPEAT they get its bias, so that an entry of the table that
+    // no pair uses, which may be anything, stays out of sight of kernels that
+    // only add -inf there; without, the caller masks them.
+    template <bool REPEAT = false>
     __device__ __forceinline__ void store(const Bias16& t, int c0, int len) const {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         const int lo = -t.D, hi = t.R + t.D;
@@ -251,16 +255,24 @@ struct Columns {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int tile = warp + k * (NR / 32), c = c0 + tile * kTile + lane;
-            if (c0 + tile * kTile >= len) break;
+            if (c0 + tile * kTile >= len) break;   // the whole warp
             const bool v0 = c < len, v1 = c + 32 < len;
-            const int p0 = pos[k][0], p1 = pos[k][1], o0 = clamped(p0), o1 = clamped(p1);
+            int p0 = pos[k][0], p1 = pos[k][1];
+            if constexpr (REPEAT) {
+                const int end = min(len - c0 - tile * kTile, kTile) - 1;
+                const int p_end = __shfl_sync(0xffffffffu, end < 32 ? p0 : p1, end & 31);
+                if (!v0) p0 = p_end;
+                if (!v1) p1 = p_end;
+            }
+            const int o0 = clamped(p0), o1 = clamped(p1);
             const int first = __shfl_sync(0xffffffffu, o0, 0);
-            const bool run = __all_sync(0xffffffffu, (!v0 || o0 == first + lane) && (!v1 || o1 == first + 32 + lane));
+            const bool any0 = !REPEAT && !v0, any1 = !REPEAT && !v1;   // places whose bias does not matter
+            const bool run = __all_sync(0xffffffffu, (any0 || o0 == first + lane) && (any1 || o1 == first + 32 + lane));
             const int pmin = __reduce_min_sync(0xffffffffu, min(v0 ? p0 : INT_MAX, v1 ? p1 : INT_MAX));
             const int pmax = __reduce_max_sync(0xffffffffu, max(v0 ? p0 : INT_MIN, v1 ? p1 : INT_MIN));
             int* off = t.off + tile * kTile;
-            off[lane] = !t.near ? p0 : v0 ? 2 * (o0 - lo) : 0;
-            off[lane + 32] = !t.near ? p1 : v1 ? 2 * (o1 - lo) : 0;
+            off[lane] = !t.near ? p0 : !any0 ? 2 * (o0 - lo) : 0;
+            off[lane + 32] = !t.near ? p1 : !any1 ? 2 * (o1 - lo) : 0;
             if (lane == 0) t.tiles[tile] = TileInfo{pmin, pmax, !t.near ? kClamped : run ? kConsecutive : kGeneral, 0};
         }
     }

@@ -15,6 +15,8 @@ relative to that.
   out  : u |out|  (the result)  +  sum_j p_j |v_j| (u + EPS32)  +  n SUB max|v|
   delta: sum_c |do_c| err(out_c) + EPS32 sum_c |do_c out_c|
   dS   : |dS| u + P (err(delta) + EPS32 (|dP| + |delta|)) with |dP| <= sum |do v|
+         (f16: dS 2^(14 - e - f) is rounded, 2^e and 2^f at most twice the largest norms of the rows of dO and V,
+         so SUB of it is at most SUB 2^-12 max|do| max|v|)
   dq   : u |dq| + scale sum_j err(dS) |k|;  dk, dv alike;  dtable: u |dtable| + sum err(dS) without its rounding
 """
 import torch
@@ -82,7 +84,7 @@ def attention(s, dout=None):
             ds = p * (dp - delta)
             ed = (do.abs() * eo).sum(1, keepdim=True) + EPS32 * (do * out).abs().sum(1, keepdim=True)
             es32 = p * (ed + EPS32 * (do.abs() @ v.abs().T + delta.abs()))
-            es = es32 + u * ds.abs() + sub * 2.0 ** -6 * do.abs().amax()
+            es = es32 + u * ds.abs() + sub * 2.0 ** -12 * do.norm(dim=1).amax() * v.norm(dim=1).amax()
             ep = (u + EPS32) * p + sub * 2.0 ** -14
             r["dq"][0][i, h] = ds @ k * s["scale"]
             r["dq"][1][i, h] = es @ k.abs() * s["scale"]

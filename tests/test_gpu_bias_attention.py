@@ -153,6 +153,31 @@ def test_gradient_scale(size):
     compare(s, run_all(s))
 
 
+@pytest.mark.parametrize("v_size,do_size", [(2.0 ** 7, 1.0), (2.0 ** 12, 2.0 ** -12), (2.0 ** 12, 2.0 ** -4), (2.0 ** -8, 1.0), (2.0 ** -4, 2.0 ** 8)])
+@pytest.mark.parametrize("H,Hkv,lens", [(1, 1, [700, 129]), (4, 2, [33, 1, 300])])
+def test_value_scale(v_size, do_size, H, Hkv, lens):
+    """f16: large values must not push a product's operand past 65504, nor small ones lose it."""
+    s = ref.problem(lens, lens, H, Hkv, F16, 32, 128, where="sorted", layout="rows")
+    s["v"].mul_(v_size)
+    s["dout"] = (s["dout"].float() * do_size).half()
+    compare(s, run_all(s))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("lens_q,where", [([37, 20, 65], "none"), ([37, 20, 65], "sorted"), ([1, 5, 2], "none"), ([1, 5, 2], "sorted")])
+def test_table_entry_that_no_pair_uses(dtype, bad, lens_q, where):
+    """A tile's places without a column must not see it."""
+    s = ref.problem(lens_q, [37, 20, 65], 2, 1, dtype, 64, 1024, where=where, layout="rows")
+    used = torch.cat([ref.scores(s, b, 0)[1].flatten() for b in range(3)]).unique()
+    unused = torch.ones(64, dtype=torch.bool)
+    unused[used] = False
+    assert unused.sum() > 10
+    s["table"][unused] = bad
+    good = dict(s, table=torch.where(unused[:, None], torch.zeros_like(s["table"]), s["table"]))
+    compare(good, run_all(s))
+
+
 def test_gradients_against_differences():
     """d sum(out dout) / dx by central differences of the definition, at random elements of every input."""
     lens = [9, 21]
