@@ -402,7 +402,7 @@ RAGGED_API ragged_status ragged_pipeline_graph_destroy(ragged_pipeline_graph *gr
  *                    RAGGED_MAX_TOKENS; a sequence longer than its bound is
  *                    skipped and RAGGED_DEV_BAD_SEQLENS is set.
  *   B                0 .. 65535 sequences;  H 1 .. 65534, a multiple of Hkv;
- *                    head_dim 64;  scale positive and finite.
+ *                    head_dim 64;  scale positive, at most 1e38.
  *   dtype            RAGGED_F16 or RAGGED_BF16: q, k, v, out, the gradients,
  *                    table and dtable.  Scores, softmax and sums are fp32.
  *   table            device [num_buckets, H], contiguous; 1 <= num_buckets <= 64.
@@ -410,7 +410,7 @@ RAGGED_API ragged_status ragged_pipeline_graph_destroy(ragged_pipeline_graph *gr
  *                    <= 1024 (ragged_rel_buckets gives one).  An entry outside
  *                    [0, num_buckets) sets RAGGED_DEV_BAD_BUCKETS; its pairs
  *                    get no bias and pass no gradient to the table.
- *   pos_q, pos_k     device int32 per row (any order, magnitudes up to 2^30),
+ *   pos_q, pos_k     device int32 per row, in any order, from -2^30 to 2^30 - 1;
  *                    or NULL: key j of a sequence is at position j, and its
  *                    queries are the last ones: query i at i + L_k - L_q.
  *   lse              device float; lse[h * lse_stride + t].  Written by
@@ -449,7 +449,7 @@ RAGGED_API ragged_status ragged_rel_buckets(int64_t num_buckets, int64_t max_dis
 /*
  * ragged_attn_bias_fwd - writes out (element (t, h, c) at out[t *
  * out_tok_stride + h * 64 + c], out_tok_stride >= H * 64, 16-byte aligned) and
- * lse.  workspace: device scratch of the size that
+ * lse, which must not overlap the inputs.  workspace: device scratch of the size that
  * ragged_attn_bias_fwd_workspace reports (0: may be NULL), 16-byte aligned, of
  * this call alone until its work has finished; nothing in it is kept.
  */
@@ -466,7 +466,8 @@ RAGGED_API ragged_status ragged_attn_bias_fwd(const ragged_bias_attn *problem, v
  * (dk and dv summed over the query heads of their head; dtable over the whole
  * batch).  Every sum is taken in a fixed order.  dq, dk and dv have strides of
  * their own (dk and dv share theirs) and cover the rows of the sequences only;
- * dtable is [num_buckets, H], contiguous.  workspace as above.
+ * dtable is [num_buckets, H], contiguous.  The gradients must not overlap the
+ * inputs or one another.  workspace as above.
  */
 RAGGED_API ragged_status ragged_attn_bias_bwd_workspace(const ragged_bias_attn *problem, int64_t *bytes);
 RAGGED_API ragged_status ragged_attn_bias_bwd(const ragged_bias_attn *problem, const void *out, int64_t out_tok_stride,
@@ -497,7 +498,8 @@ RAGGED_API ragged_status ragged_attn_weight(const ragged_bias_attn *problem, con
  *   rows          device rows of row_bytes (a multiple of 16), 16-byte aligned;
  *                 or NULL with rows_out NULL: only the selection.
  *   weight        device float [H, weight_stride], as ragged_attn_weight writes.
- *   tokens        rows of the input (at least cu_seqlens[B]).
+ *   tokens        rows of the input; a sequence that ends past them keeps nothing
+ *                 and sets RAGGED_DEV_BAD_SEQLENS.
  *   cu_seqlens    device int32 [B + 1], 0 <= B <= 65535;  1 <= max_seqlen <=
  *                 RAGGED_MAX_TOKENS bounds every L_b (a longer sequence keeps
  *                 nothing and sets RAGGED_DEV_BAD_SEQLENS).

@@ -34,8 +34,8 @@ ragged_status check_bias_problem(const ragged_bias_attn* a, bool need_v, ragged:
     for (int64_t n : longest)
         if (n < 1 || n > RAGGED_MAX_TOKENS)
             return fail(RAGGED_ERR_INVALID_ARG, "max_seqlen = %lld outside [1, %d]", (long long)n, RAGGED_MAX_TOKENS);
-    if (!(a->scale > 0.f) || a->scale > 3.0e38f)
-        return fail(RAGGED_ERR_INVALID_ARG, "scale must be a positive finite number");
+    if (!(a->scale > 0.f) || a->scale > 1.0e38f)   // times log2 e it stays finite
+        return fail(RAGGED_ERR_INVALID_ARG, "scale must be positive and at most 1e38");
     if (a->num_buckets < 1 || a->num_buckets > ragged::bias::kMaxBuckets)
         return fail(RAGGED_ERR_UNSUPPORTED, "num_buckets = %lld outside [1, %d]", (long long)a->num_buckets,
                     ragged::bias::kMaxBuckets);

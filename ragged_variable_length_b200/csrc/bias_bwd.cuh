@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         __syncwarp();
         start_loads();
-        bool ok = true;
+        bool ok = !test_hook(1);
         uint32_t g = 0;
         for (int i = 0; ok && i < nh; ++i) {
             const int64_t z = static_cast<int64_t>((h0 + i) / p.group) * p.kv_head;
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         __syncwarp();
         start_loads();
-        bool ok = true;
+        bool ok = !test_hook(1);
         uint32_t g = 0;
         for (int i = 0; ok && i < nz && nt > 0; ++i) {
             const int z = z0 + i;
@@ -981,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         __syncwarp();
         start_loads();
-        bool ok = true;
+        bool ok = !test_hook(1);
         uint32_t g = 0;
         for (int i = 0; ok && i < nh; ++i) {
             const int h = h0 + i;

@@ -44,7 +44,7 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 // Tokens that sequence b keeps (0 for one that must be skipped).
 __device__ __forceinline__ int kept_of(const Args& a, int b, bool flag) {
     const int start = __ldg(a.cu + b), len = __ldg(a.cu + b + 1) - start;
-    if (start < 0 || len < 0 || len > a.max_seqlen) {
+    if (start < 0 || len < 0 || len > a.max_seqlen || static_cast<int64_t>(start) + len > a.tokens) {
         if (flag) raise_status(RAGGED_DEV_BAD_SEQLENS);
         return 0;
     }
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(256) keys_kernel(const Args a) {
     const int b = blockIdx.y, m = kept_of(a, b, false);
     const int start = __ldg(a.cu + b), len = __ldg(a.cu + b + 1) - start;
     const int t = blockIdx.x * 256 + threadIdx.x;
-    if (m > 0 && m < len && t < len && start + t < a.tokens) a.keys[start + t] = token_key(a, start, len, t);
+    if (m > 0 && m < len && t < len) a.keys[start + t] = token_key(a, start, len, t);
 }
 
 // ... the selection, one CTA per sequence with the keys in registers, ...
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kLongThreads) long_kernel(const Args a) {
 #pragma unroll
         for (int i = 0; i < KEYS; ++i) {
             const int t = i * NT + tid;
-            key[i] = t < len && start + t < a.tokens ? a.keys[start + t] : 0u;
+            key[i] = t < len ? a.keys[start + t] : 0u;
         }
     }
     const int before = kept_before<NT>(a, b, s_red);

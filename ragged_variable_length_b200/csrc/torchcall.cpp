@@ -180,6 +180,13 @@ Tensor result(PyObject* o, const Tensor& like, const char* what) {
     return t;
 }
 
+// A result is written while the inputs are still read, and while other results are written.
+void apart(const Tensor& result, std::initializer_list<const Tensor*> others, const char* what) {
+    for (const Tensor* t : others)
+        TORCH_CHECK_VALUE(result.numel() == 0 || t->numel() == 0 || t->data_ptr() != result.data_ptr(), what,
+                          " must not share its memory with an input or another result");
+}
+
 // q, k, v, shared..., out, lse -> (out, lse)
 PyObject* bias_fwd(PyObject*, PyObject* const* o, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -188,6 +195,7 @@ PyObject* bias_fwd(PyObject*, PyObject* const* o, Py_ssize_t n) {
     TORCH_CHECK_VALUE(q.dim() == 3, "q must be [Tq, H, head_dim]");
     const Tensor out = result(o[3 + kShared], q, "out");
     TORCH_CHECK_VALUE(rows_of_heads(out), "out must be [T, H, head_dim] with contiguous heads");
+    apart(out, {&q, &k, &v}, "out");
     const Tensor lse = o[4 + kShared] == Py_None ? empty({q.size(1), q.size(0)}, q, at::kFloat) : tensor(o[4 + kShared], "lse");
     Problem p(q, k, v, o + 3, lse);
     p.dev.add(out);
@@ -211,16 +219,20 @@ PyObject* bias_bwd(PyObject*, PyObject* const* o, Py_ssize_t n) {
     TORCH_CHECK_VALUE(out.sizes() == q.sizes() && out.scalar_type() == q.scalar_type() && q.dim() == 3 && rows_of_heads(out),
                       "out must be [T, H, head_dim] with contiguous heads");
     TORCH_CHECK_VALUE(dout.sizes() == q.sizes() && dout.scalar_type() == q.scalar_type(), "dout must have the shape and dtype of out");
-    Problem p(q, k, v, o + 6, lse);
-    p.dev.add(dout);
-    p.dev.add(out);
     const Tensor& table = tensor(o[6 + 4], "table");
-    if (!rows_of_heads(dout) || reinterpret_cast<uintptr_t>(dout.data_ptr()) % 16 != 0 || row_stride(dout) % 8 != 0)
-        dout = dout.detach().clone(at::MemoryFormat::Contiguous);   // a broadcast or transposed gradient
     const Tensor dq = result(given[0], q, "dq"), dk = result(given[1], k, "dk"), dv = result(given[2], v, "dv");
     const Tensor dtable = result(given[3], table, "dtable");
     TORCH_CHECK_VALUE(dk.numel() == 0 || dk.strides() == dv.strides(), "dk and dv must have the same strides");
+    apart(dq, {&q, &k, &v, &out, &dout, &dk, &dv}, "dq");
+    apart(dk, {&q, &k, &v, &out, &dout, &dv}, "dk");
+    apart(dv, {&q, &k, &v, &out, &dout}, "dv");
+    apart(dtable, {&table}, "dtable");
     TORCH_CHECK_VALUE(dtable.is_contiguous(), "dtable must be contiguous with the shape and dtype of table");
+    Problem p(q, k, v, o + 6, lse);
+    p.dev.add(dout);
+    p.dev.add(out);
+    if (!rows_of_heads(dout) || reinterpret_cast<uintptr_t>(dout.data_ptr()) % 16 != 0 || row_stride(dout) % 8 != 0)
+        dout = dout.detach().clone(at::MemoryFormat::Contiguous);   // a broadcast or transposed gradient
     for (const Tensor* t : {&dq, &dk, &dv, &dtable}) p.dev.add(*t);
     int64_t bytes = 0;
     ragged_status s = g_lib.bwd_workspace(&p.a, &bytes);

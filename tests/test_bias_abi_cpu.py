@@ -33,7 +33,7 @@ PROBLEMS = [
     (dict(Hkv=0), BAD, "Hkv"), (dict(H=70000, Hkv=70000), BAD, "H ="), (dict(head_dim=128), UNSUPPORTED, "head_dim"), (dict(dtype=7), BAD, "dtype"),
     (dict(dtype=rv.RAGGED_F32), UNSUPPORTED, "f16 and bf16"), (dict(max_seqlen_q=0), BAD, "max_seqlen"), (dict(max_seqlen_k=0), BAD, "max_seqlen"),
     (dict(max_seqlen_k=rv.RAGGED_MAX_TOKENS + 1), BAD, "max_seqlen"), (dict(scale=0.0), BAD, "scale"), (dict(scale=-1.0), BAD, "scale"),
-    (dict(scale=math.nan), BAD, "scale"), (dict(scale=math.inf), BAD, "scale"), (dict(num_buckets=0), UNSUPPORTED, "num_buckets"),
+    (dict(scale=math.nan), BAD, "scale"), (dict(scale=math.inf), BAD, "scale"), (dict(scale=2e38), BAD, "scale"), (dict(num_buckets=0), UNSUPPORTED, "num_buckets"),
     (dict(num_buckets=65), UNSUPPORTED, "num_buckets"), (dict(max_distance=-1), UNSUPPORTED, "max_distance"),
     (dict(max_distance=1025), UNSUPPORTED, "max_distance"), (dict(q=None), BAD, "NULL"), (dict(k=None), BAD, "NULL"),
     (dict(cu_seqlens_q=None), BAD, "NULL"), (dict(cu_seqlens_k=None), BAD, "NULL"), (dict(table=None), BAD, "NULL"), (dict(buckets=None), BAD, "NULL"),
@@ -202,6 +202,16 @@ def test_gradient_weight_and_eviction_refuse_tensors(lib):
     for kw, needle in ((dict(dout=a["q"][:7]), "dout"), (dict(out=a["k"]), "out"), (dict(lse=torch.zeros(4, 9)), "lse"), (dict(), "current CUDA device")):
         with pytest.raises(ValueError, match=needle):
             rv.ragged_attn_bias_bwd(**dict(bwd, **kw))
+    other = dict(bwd, out=torch.zeros_like(a["q"]), dout=torch.zeros_like(a["q"]))
+    for kw, needle in ((dict(dq=a["q"]), "dq"), (dict(dk=a["v"]), "dk"), (dict(dv=a["k"]), "dv"), (dict(dtable=a["table"]), "dtable"),
+                       (dict(dk=torch.zeros_like(a["k"])), "CUDA device")):
+        with pytest.raises(ValueError, match=needle):
+            rv.ragged_attn_bias_bwd(**dict(other, **kw))
+    both = torch.zeros_like(a["k"])
+    with pytest.raises(ValueError, match="dk must not share"):
+        rv.ragged_attn_bias_bwd(**dict(other, dk=both, dv=both))
+    with pytest.raises(ValueError, match="out must not share"):
+        rv.ragged_attn_bias_fwd(**_tensors(out=a["q"], q=a["q"]))
     with pytest.raises(ValueError, match="current CUDA device"):
         rv.ragged_attn_weight(q=a["q"], k=a["k"], **rest)
     w, cu, budget = torch.zeros(2, 9), torch.zeros(3, dtype=I32), torch.zeros(2, dtype=I32)
