@@ -78,7 +78,9 @@ int64_t average_length(int64_t B, int64_t longest, int64_t rows) {
 }
 
 // Parts that a key row's queries are split into, where key tiles and heads
-// alone leave SMs without work and each CTA has many query tiles to walk.
+// alone leave SMs without work and each CTA has many query tiles to walk.  (2
+// sequences of 3,279 to 4,099, 8 over 2 heads: 332 + 5 us for the key rows and
+// the parts' sum, 515 us in one part.)
 int64_t bwd_parts(const ragged_bias_attn* a) {
     const int64_t avg_q = average_length(a->B, a->max_seqlen_q, a->lse_stride);
     const int64_t avg_k = std::max<int64_t>(1, a->max_seqlen_k * avg_q / a->max_seqlen_q);
@@ -103,14 +105,15 @@ int64_t fwd_workspace(const ragged_bias_attn*) { return 0; }
 
 // Positions that a kernel's expanded table covers: what two CTAs per SM leave
 // room for next to `fixed` bytes, unless that is too little to be of use (many
-// buckets, or a far-reaching map): then one CTA.
+// buckets, or a far-reaching map): then one CTA.  (64 sequences of 173 to 403
+// tokens, D = 512, where two CTAs leave 150 positions: 118 us either way.)
 constexpr int kTwoPerSm = (228 * 1024) / 2 - 1024 - 3072;   // less the reserved and the static part
 constexpr int bias_span(int D, int fixed, int bytes_per_entry) {
     const int entries = (kTwoPerSm - fixed - 64 - (2 * D + 16)) / bytes_per_entry;
     const int span = (entries - 1 - ragged::bias::kVecPad) / 2 - D;
     return span < 256 ? ragged::bias::kSpan : span < ragged::bias::kSpan ? span : ragged::bias::kSpan;
 }
-constexpr int kBwdQSmemMax = ragged::bias::bwd_q_smem_bytes(ragged::bias::kMaxDistance, ragged::bias::kMaxBuckets, ragged::bias::kSpan, 3);
+constexpr int kBwdQSmemMax = ragged::bias::bwd_q_smem_bytes(ragged::bias::kMaxDistance, ragged::bias::kMaxBuckets, ragged::bias::kSpan);
 
 ragged_status check_workspace(const void* ws, int64_t have, int64_t need) {
     if (need > 0 && (ws == nullptr || have < need))
@@ -120,7 +123,7 @@ ragged_status check_workspace(const void* ws, int64_t have, int64_t need) {
     return RAGGED_OK;
 }
 
-DeviceFlags g_bias_fwd_smem[2], g_bias_bwd_q_smem[2][2], g_bias_bwd_kv_smem[2], g_bias_weight_smem[2];
+DeviceFlags g_bias_fwd_smem[2], g_bias_bwd_q_smem[2], g_bias_bwd_kv_smem[2], g_bias_weight_smem[2];
 template <typename T>
 constexpr int kTypeSlot = std::is_same<T, __half>::value ? 0 : 1;
 
@@ -151,7 +154,10 @@ int heads_per_cta(int64_t row_tiles, int64_t heads, int64_t col_tiles, int64_t s
 
 // Few query rows per key / value head go to the kernels that share one 16- or
 // 32-row MMA tile among them: the 128-row tiles would be mostly empty, and
-// read the keys once per query head.
+// read the keys once per query head.  (32 sequences of 4,096 to 8,192 keys, 16
+// over 4 heads, 4 and 8 queries, so 16 and 32 rows: 42 and 68 us, against 205
+// us either way; weights of 32 rows 78 against 184.  More rows do not fit these
+// kernels' registers.)
 bool few_rows(const ragged::bias::Problem& p) {
     return static_cast<int64_t>(p.group) * p.max_q <= ragged::bias::kFewMaxRows;
 }
@@ -197,12 +203,22 @@ ragged_status launch_few_weight(const ragged::bias::Problem& p, const float* pre
     kernel<<<bias_grid(splits, p.Hkv, p.B), 32 * NW, few_smem_bytes<MT, NW, true>(p.D, p.num_buckets), s>>>(p, prev, weight, stride);
     return cuda_check(cudaGetLastError(), "attention weight (few rows) launch");
 }
-// By rows (one or two MMA tiles) and by the longest sequence.
+// Two warps per CTA instead of eight where there are more groups than one wave
+// of eight warps (two CTAs per SM) holds, the more the longer they are.
+// (Attention of one query, 16 over 4 heads, with two and with eight warps: 296
+// groups of up to 128 keys 11.6 and 7.2 us; 400 of up to 60 9.9 and 11.1, of up
+// to 128 12.8 and 11.9, of up to 512 20 and 17; 1,024 of up to 128 15 and 22, of
+// up to 512 29 and 35, of up to 1,024 47 and 47, of up to 2,048 77 and 72.)
+bool few_short(const ragged::bias::Problem& p) {
+    const int64_t groups = static_cast<int64_t>(p.B) * p.Hkv, wave = 2LL * sm_count();
+    return groups > wave && p.max_k <= ragged::bias::kFewShortKeys && p.max_k * wave <= 160 * groups;
+}
+// By rows (one or two MMA tiles), and by the number and length of the sequences.
 template <typename T>
 ragged_status launch_few_rows(const ragged::bias::Problem& p, uint16_t* out, int64_t out_tok, cudaStream_t s) {
     using namespace ragged::bias;
     const bool one = p.group * p.max_q <= 16;
-    if (p.max_k <= kFewShortKeys)
+    if (few_short(p))
         return one ? launch_few<T, 1, kFewShortWarps>(p, out, out_tok, s) : launch_few<T, 2, kFewShortWarps>(p, out, out_tok, s);
     return one ? launch_few<T, 1, kFewWarps>(p, out, out_tok, s) : launch_few<T, 2, kFewWarps>(p, out, out_tok, s);
 }
@@ -210,7 +226,7 @@ template <typename T>
 ragged_status launch_few_rows_weight(const ragged::bias::Problem& p, const float* prev, float* weight, int64_t stride, cudaStream_t s) {
     using namespace ragged::bias;
     const bool one = p.group * p.max_q <= 16;
-    if (p.max_k <= kFewShortKeys)
+    if (few_short(p))
         return one ? launch_few_weight<T, 1, kFewShortWarps>(p, prev, weight, stride, s)
                    : launch_few_weight<T, 2, kFewShortWarps>(p, prev, weight, stride, s);
     return one ? launch_few_weight<T, 1, kFewWarps>(p, prev, weight, stride, s) : launch_few_weight<T, 2, kFewWarps>(p, prev, weight, stride, s);
@@ -234,16 +250,12 @@ ragged_status launch_bias_fwd(const ragged::bias::Problem& p, uint16_t* out, int
 template <typename T>
 ragged_status launch_bias_bwd(const ragged::bias::Problem& p, ragged::bias::BwdArgs a, cudaStream_t s) {
     using namespace ragged::bias;
-    // Two K and V stages instead of three where many buckets' sums would not
-    // leave room for two CTAs per SM.
-    const int stages = bwd_q_fixed_bytes(p.num_buckets, 3) + 8192 <= kTwoPerSm ? 3 : 2;
-    auto q_kernel = stages == 3 ? bias_bwd_q_kernel<T, 3> : bias_bwd_q_kernel<T, 2>;
-    ragged_status st = ensure_smem(q_kernel, kBwdQSmemMax, g_bias_bwd_q_smem[kTypeSlot<T>][stages - 2]);
+    ragged_status st = ensure_smem(bias_bwd_q_kernel<T>, kBwdQSmemMax, g_bias_bwd_q_smem[kTypeSlot<T>]);
     if (st == RAGGED_OK) st = ensure_smem(bias_bwd_kv_kernel<T>, bwd_kv_smem_bytes(kMaxDistance, kSpan), g_bias_bwd_kv_smem[kTypeSlot<T>]);
     if (st != RAGGED_OK) return st;
     const int64_t avg_q = average_length(p.B, p.max_q, p.lse_stride), avg_k = std::max<int64_t>(1, p.max_k * avg_q / p.max_q);
     const int64_t slots = 2LL * sm_count();
-    a.span = bias_span(p.D, bwd_q_fixed_bytes(p.num_buckets, stages), 3);
+    a.span = bias_span(p.D, bwd_q_fixed_bytes(p.num_buckets), 3);
     a.heads = heads_per_cta(p.B * tiles128(avg_q), p.H, (avg_k + kTile - 1) / kTile, slots);
     cudaLaunchAttribute early{};   // the kernel may start before the one ahead of it has ended, and waits for it itself
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -259,13 +271,15 @@ ragged_status launch_bias_bwd(const ragged::bias::Problem& p, ragged::bias::BwdA
         cfg.numAttrs = 1;
     }
     cfg.gridDim = bias_grid(a.q_tiles, (p.H + a.heads - 1) / a.heads, p.B);
-    cfg.dynamicSmemBytes = bwd_q_smem_bytes(p.D, p.num_buckets, a.span, stages);
-    st = cuda_check(cudaLaunchKernelEx(&cfg, q_kernel, p, a), "query gradient launch");
+    cfg.dynamicSmemBytes = bwd_q_smem_bytes(p.D, p.num_buckets, a.span);
+    st = cuda_check(cudaLaunchKernelEx(&cfg, bias_bwd_q_kernel<T>, p, a), "query gradient launch");
     if (st != RAGGED_OK) return st;
     a.span = bias_span(p.D, bwd_kv_fixed_bytes(), 3);
     a.heads = a.parts > 1 ? 1 : heads_per_cta(p.B * tiles128(avg_k), p.Hkv, (avg_q + kTile - 1) / kTile * p.group, slots);
     // The table's sums go to CTAs of this launch where a column or a slice of its
-    // grid has enough of them (32,768 values each) and not too many.
+    // grid has enough of them (32,768 values each) and not too many: 28 instead of
+    // 31 us for 4 sequences of 79 to 197 tokens; 462 instead of 299 us where few
+    // CTAs had to sum for 352 short ones.
     const int64_t columns = tiles128(p.max_k) * a.parts, groups = (p.Hkv + a.heads - 1) / a.heads;
     const int64_t values = static_cast<int64_t>(p.num_buckets) * p.H * p.B * a.q_tiles, most = std::max<int64_t>(32, columns * groups * p.B / 16);
     auto fits = [&](int64_t ctas) { return ctas * 32768 >= values && ctas <= most; };

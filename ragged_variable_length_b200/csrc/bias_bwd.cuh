@@ -7,7 +7,18 @@
 //
 // Two kernels, so that every sum has a fixed order and no sum needs atomics:
 // one with query rows (dQ, delta, the table), one with key rows (dK, dV,
-// transposed scores).  Each recomputes S and dP, 7 products instead of 5.
+// transposed scores).  Each recomputes S and dP, 7 products instead of 5.  In
+// f16 a small kernel before them reads the size of V (below).
+//
+// delta is formed from O as it was stored, so the half step of O's rounding is
+// in dS, P (dO . err O), and shows in the table's gradient, which sums dS in
+// fp32: 3e-4 of its size in f16, 3e-3 in bf16, against 2e-4 and 2e-3 for sums
+// from an unrounded O, which nobody keeps.
+//
+// Measured, both kernels and the sums: 64 sequences of 173 to 403 tokens, 12
+// heads, bf16, positions with gaps: 376 us (memory and products allow 40); 2
+// of 3,279 to 4,099, 8 over 2 heads, f16: 444 us (117); 4 of 79 to 197, 6
+// heads, f16: 29 us.
 //
 // Both have eight row warps: two threads share a row, one for each half of a
 // tile's 64 columns (nothing is reduced along a row but the table's sums, which
@@ -30,7 +41,7 @@ namespace bias {
 constexpr int kBwdRows = 256;                   // row threads
 constexpr int kBwdThreads = kBwdRows + 64;      // and the MMA and load warps
 constexpr int kBwdMmaWarp = 8, kBwdLoadWarp = 9;
-constexpr int kBwdStages = 3;
+constexpr int kBwdQStages = 2, kBwdStages = 3;   // of the kernels below; three for the first were no faster
 constexpr int kNoExp = -1000;                   // of rows that are zero, or not finite
 
 template <typename T>
@@ -145,15 +156,16 @@ __device__ __forceinline__ void probabilities(const Bias16& t, const Problem& p,
     }
 }
 
-__host__ __device__ constexpr int bwd_q_fixed_bytes(int num_buckets, int stages) {
-    return 1024 + stages * 2 * kTileBytes + (num_buckets + 1) * 4 * kBwdRows + 4 * kChunk;
+__host__ __device__ constexpr int bwd_q_fixed_bytes(int num_buckets) {
+    return 1024 + kBwdQStages * 2 * kTileBytes + (num_buckets + 1) * 4 * kBwdRows + 4 * kChunk;
 }
-__host__ __device__ constexpr int bwd_q_smem_bytes(int D, int num_buckets, int span, int stages) {
-    return bwd_q_fixed_bytes(num_buckets, stages) + vec16_bytes(D, span) + ids_bytes(D, span);
+__host__ __device__ constexpr int bwd_q_smem_bytes(int D, int num_buckets, int span) {
+    return bwd_q_fixed_bytes(num_buckets) + vec16_bytes(D, span) + ids_bytes(D, span);
 }
 
 // Exponent f of each tile of 128 rows of V (f16 only).  grid (key tiles, Hkv, B);
-// eight threads per row.  One read of V, which the next kernel finds in L2.
+// eight threads per row.  Bound by that one read of V (2.7 us for 2 MB, 30 us
+// for 190 MB), of which the next kernel finds in L2 what fits there.
 template <typename T>
 __global__ void __launch_bounds__(256) bias_bwd_value_kernel(const Problem p, const BwdArgs a) {
     __shared__ int s_top[8];
@@ -199,6 +211,12 @@ __device__ __forceinline__ int value_exp(const Problem& p, const BwdArgs& a, int
 }
 
 // Query rows: dQ, delta, and each tile's sums for the table's gradient.
+//
+// The table's sums have a column of shared memory per thread, so that no two
+// threads meet and the order is fixed; each element is one read-modify-write
+// there, after the read of its bucket.  They bound the kernel: 2,470 of a
+// tile's 4,400 cycles where the distances are inside the map, 470 where one sum
+// in a register serves the whole tile.
 // grid (query tiles, groups of heads, B), two CTAs per SM where the table is small.
 //
 // TMEM (256 columns): S, dP (each half replaced in place by its dS), dQ, and
@@ -206,10 +224,10 @@ __device__ __forceinline__ int value_exp(const Problem& p, const BwdArgs& a, int
 // the time of one with A in shared memory, and the room goes to the table's
 // sums.  S of the next tile is computed while dS of this one is, dP of the
 // next one while its probabilities are.
-template <typename T, int STAGES>
+template <typename T>
 __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Problem p, const BwdArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    // kv_full[3], kv_done[3] (up to STAGES), qd_full, s_full, dp_full, a_full, b_full, dq_full, done
+    // kv_full[2], kv_done[2], qd_full, s_full, dp_full, a_full, b_full, dq_full, done
     constexpr int kBars = 13;
     __shared__ __align__(8) uint64_t s_bar[kBars];
     __shared__ uint16_t s_tab[kMaxBuckets + 1];
@@ -242,11 +260,11 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
 
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t sRing = (raw + 1023u) & ~1023u;   // stage: K, then V
-    float* acc = reinterpret_cast<float*>(smem_raw + (sRing - raw) + STAGES * 2 * kTileBytes);   // [buckets + 1][256]
-    auto stage = [&](uint32_t g) { return sRing + (g % STAGES) * 2 * kTileBytes; };
+    float* acc = reinterpret_cast<float*>(smem_raw + (sRing - raw) + kBwdQStages * 2 * kTileBytes);   // [buckets + 1][256]
+    auto stage = [&](uint32_t g) { return sRing + (g % kBwdQStages) * 2 * kTileBytes; };
     const uint32_t bar0 = smem_addr(&s_bar[0]);
-    auto kv_full = [&](uint32_t g) { return bar0 + 8u * (g % STAGES); };
-    auto kv_done = [&](uint32_t g) { return bar0 + 8u * (3 + g % STAGES); };
+    auto kv_full = [&](uint32_t g) { return bar0 + 8u * (g % kBwdQStages); };
+    auto kv_done = [&](uint32_t g) { return bar0 + 8u * (3 + g % kBwdQStages); };
     const uint32_t qd_full = bar0 + 48, s_full = bar0 + 56, dp_full = bar0 + 64, a_full = bar0 + 72, b_full = bar0 + 80, dq_full = bar0 + 88, done = bar0 + 96;
     constexpr uint32_t dp_col = kTile, dq_col = 2 * kTile, q_col = 3 * kTile, do_col = 3 * kTile + 32;
     const Wait wait{&s_fail};
@@ -264,7 +282,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
             const uint16_t* kb = p.k + s.k_start * p.kv_tok + z;
             const uint16_t* vb = p.v + s.k_start * p.kv_tok + z;
             for (int t = 0; t < nt; ++t, ++g) {
-                if (g >= STAGES) ok = wait.warp(kv_done(g), (g / STAGES - 1) & 1);
+                if (g >= kBwdQStages) ok = wait.warp(kv_done(g), (g / kBwdQStages - 1) & 1);
                 if (!ok) break;
                 load_rows<kTile>(stage(g), kb, p.kv_tok, t * kTile, s.k_len, lane);
                 load_rows<kTile>(stage(g) + kTileBytes, vb, p.kv_tok, t * kTile, s.k_len, lane);
@@ -283,7 +301,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
             bool ok = true;
             uint32_t g = 0;
             for (int i = 0; ok && i < nh; ++i) {
-                ok = wait(qd_full, i & 1) && wait(kv_full(g), (g / STAGES) & 1);
+                ok = wait(qd_full, i & 1) && wait(kv_full(g), (g / kBwdQStages) & 1);
                 if (!ok) break;
                 fence_async_smem();
                 fence_after_sync();
@@ -294,7 +312,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                 for (int t = 0; t < nt; ++t, ++g) {
                     const bool more = t + 1 < nt;
                     if (more) {
-                        ok = wait(kv_full(g + 1), ((g + 1) / STAGES) & 1);
+                        ok = wait(kv_full(g + 1), ((g + 1) / kBwdQStages) & 1);
                         if (!ok) break;
                         fence_async_smem();
                     }
@@ -578,7 +596,8 @@ __global__ void __launch_bounds__(256) bias_bwd_table_kernel(const Problem p, co
 // column or a slice of CTAs that sums up the table's gradient.
 //
 // TMEM (256 columns): S^T and dP^T (each half replaced in place by its P^T,
-// dS^T), dK and dV.
+// dS^T), dK and dV.  Bound by the row warps' instructions, as the forward pass.
+// A table column of shared memory less, so three stages of Q and dO fit.
 template <typename T>
 __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Problem p, const BwdArgs a) {
     extern __shared__ uint8_t smem_raw[];
@@ -926,7 +945,10 @@ __global__ void __launch_bounds__(256) bias_bwd_parts_kernel(const Problem p, co
 // ---------------------------------------------------------------------------
 // weight[h, j] = prev[h, j] + sum_i exp(s[i, j] - lse_i): key rows, transposed
 // scores, summed along each thread's row.  grid (key tiles, groups of heads,
-// B), three CTAs per SM; TMEM: two score buffers.
+// B), three CTAs per SM; TMEM: two score buffers.  Bound by the row warps'
+// instructions.  512 sequences of 79 to 118 tokens, 6 heads, f16: 60 us, 352 of
+// up to 36, 12 heads: 39, 11 of up to 2,878, 48 heads: 105; with two CTAs and
+// more registers 53, 48 and 120.  The reads alone are 12 us of the first.
 // ---------------------------------------------------------------------------
 
 constexpr int kWeightStages = 3;

@@ -13,6 +13,11 @@
 //
 // P is split into two 16-bit parts (value and residual) for P V, which costs
 // nothing next to the loads and leaves the result with its own rounding only.
+//
+// Measured: 32 sequences of 4,096 to 8,192 keys, one query, 16 over 4 heads,
+// bf16: 40 us, 5.5 TB/s of keys and values; their weights, with those so far
+// read and written: 38 us.  One sequence of 577, 12 heads, f16: 7.2 and 5.1 us,
+// a launch and two dependent reads.
 #pragma once
 
 #include <limits.h>
@@ -22,11 +27,11 @@
 namespace ragged {
 namespace bias {
 
-// Warps of a CTA: few where the longest sequence is short, so that many CTAs
-// share an SM (200 sequences of 4 to 6 tokens, 8 heads: 33 us with eight warps,
-// which a ring each for long sequences takes 100 KB for).
+// Warps of a CTA: few for many short sequences, so that many CTAs share an SM
+// (200 sequences of 4 to 6 tokens, 8 heads: 18 us, 33 us with eight warps, whose
+// rings take 100 KB).
 constexpr int kFewWarps = 8, kFewShortWarps = 2;
-constexpr int kFewShortKeys = 128;
+constexpr int kFewShortKeys = 512;
 constexpr int kFewKeys = 16;          // keys per block
 constexpr int kFewStages = 3;         // ring of a warp: two blocks in flight beside the current one
 constexpr int kFewMaxRows = 32;
@@ -38,7 +43,7 @@ template <int MT, bool WEIGHT>
 __host__ __device__ constexpr int few_stage_bytes() {   // keys, then values or the weights so far, then positions
     return kFewKeys * 128 + (WEIGHT ? MT * 16 * kFewKeys * 4 : kFewKeys * 128) + kFewKeys * 4;
 }
-// The bucket map is staged for long sequences only: a short one meets few distances.
+// The bucket map is staged by eight warps only: a short sequence meets few distances.
 template <int MT, int NW>
 __host__ __device__ constexpr int few_map_bytes(int D) { return NW == kFewWarps ? (2 * D + 1 + 15) & ~15 : 0; }
 template <int MT, int NW, bool WEIGHT>
