@@ -107,7 +107,7 @@ int64_t fwd_workspace(const ragged_bias_attn*) { return 0; }
 // room for next to `fixed` bytes, unless that is too little to be of use (many
 // buckets, or a far-reaching map): then one CTA.  (64 sequences of 173 to 403
 // tokens, D = 512, where two CTAs leave 150 positions: 118 us either way.)
-constexpr int kTwoPerSm = (228 * 1024) / 2 - 1024 - 3072;   // less the reserved and the static part
+constexpr int kTwoPerSm = 114 * 1024 - 1024 - 3 * 1024;   // less the reserved and the static part
 constexpr int bias_span(int D, int fixed, int bytes_per_entry) {
     const int entries = (kTwoPerSm - fixed - 64 - (2 * D + 16)) / bytes_per_entry;
     const int span = (entries - 1 - ragged::bias::kVecPad) / 2 - D;
@@ -312,7 +312,7 @@ ragged_status launch_bias_weight(const ragged::bias::Problem& p, const float* pr
     return cuda_check(cudaGetLastError(), "attention weight launch");
 }
 
-// x^a * y^b >= u^c * v^d in whole numbers (up to 64 factors below 2^16 each).
+// Products of up to 64 factors below 2^16, compared in whole numbers.
 struct BigUint {
     uint32_t w[72] = {1};
     int n = 1;

@@ -40,7 +40,6 @@ namespace bias {
 using namespace tc05;   // tcgen05 / mbarrier / packed-fp32 wrappers
 
 constexpr int kThreads = 192;         // 4 element-wise warps, MMA warp, load warp
-constexpr int kRowWarps = 4;
 constexpr int kTcMmaWarp = 4, kTcLoadWarp = 5;
 constexpr int kTile = 64;             // columns per tile
 constexpr int kTileBytes = kTile * 128;
@@ -338,7 +337,7 @@ __device__ __forceinline__ void bias_add(const Bias16& t, int kind, const int* o
 // (exponentials 900 to 1,300 of them) and more where the entries are gathered.
 // Measured: 64 sequences of 173 to 403 tokens, 12 heads, bf16, positions with
 // gaps: 104 us, the least that memory and products allow is 18; 2 of 4,914 to
-// 8,191, 12 over 4 heads: 580 us, 430 TFLOP/s; 4 of 79 to 118, 6 heads, f16:
+// 8,191, 12 over 4 heads: 580 us, 437 TFLOP/s; 4 of 79 to 118, 6 heads, f16:
 // 8.0 us, of which most is the launch and one chain of dependent reads.
 //
 // Tried against this: eight row warps that share each tile (half the columns
