@@ -9,7 +9,7 @@
 // the selection is exact and in integers.  Measured: 32 sequences of 4,096 to
 // 8,192 tokens, half of them kept, rows of 1 KB, 16 heads: keys 4.6 us,
 // selection 12.5 us (one CTA per sequence, its keys in registers), copy 40.5 us
-// (4.9 TB/s read and written); 4 of 79 to 197, rows of 2,304 bytes: 8.4 us in
+// (5.4 TB/s read and written); 4 of 79 to 197, rows of 2,304 bytes: 8.4 us in
 // one launch.  A selection by bisection of the key range took 41 to 64 us, one
 // shared by a cluster's CTAs no less than one CTA's.
 #pragma once

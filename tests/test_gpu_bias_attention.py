@@ -82,6 +82,16 @@ def test_short_sequences(lens_q, lens_k, H, Hkv, D, nb, where):
     compare(s, run_all(s))
 
 
+@pytest.mark.parametrize("where", ["none", "sorted", "shuffled", "far"])
+@pytest.mark.parametrize("H,Hkv,D,nb,longest", [(2, 2, 128, 32, 8), (8, 2, 1024, 64, 8), (2, 2, 16, 50, 30), (4, 2, 200, 7, 1)])
+def test_many_short_sequences(H, Hkv, D, nb, longest, where):
+    """More groups than the GPU has room for at a time: a few queries against up to 100 keys each, some without either."""
+    lens_q = [(7 * i) % (longest + 1) for i in range(170)]
+    lens_k = [(n + 37 * i) % 101 if i % 3 else n for i, n in enumerate(lens_q)]
+    s = ref.problem(lens_q, lens_k, H, Hkv, F16 if nb % 4 else BF16, nb, D, where=where, layout="rows", seed=D)
+    compare(s, run_all(s, want=("out", "lse", "weight")))
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_long_sequence(dtype):
     s = ref.problem([2049, 100], [2049, 100], 1, 1, dtype, 32, 128)
