@@ -139,9 +139,10 @@ dim3 bias_grid(int64_t tiles, int heads, int B) {
 // to 118, 6 heads: 86, 74, 70, 88, 65 us with 1, 2, 3, 4, 6.)
 int heads_per_cta(int64_t row_tiles, int64_t heads, int64_t col_tiles, int64_t slots) {
     constexpr double kSetup = 4, kHead = 1;
+    constexpr int64_t kMost = 64;   // a CTA of the longest sequences then takes some 50 ms, well within the next kernel's waits
     int best = 1;
     double best_cost = 1e300;
-    for (int n = 1; n <= heads; ++n) {
+    for (int n = 1; n <= std::min<int64_t>(heads, kMost); ++n) {
         const double waves = static_cast<double>(row_tiles * ((heads + n - 1) / n)) / static_cast<double>(slots);
         const double cost = (std::max(1.0, waves) + 0.5) * (kSetup + n * (kHead + static_cast<double>(col_tiles)));
         if (cost < best_cost) {

@@ -92,6 +92,14 @@ def test_many_short_sequences(H, Hkv, D, nb, longest, where):
     compare(s, run_all(s, want=("out", "lse", "weight")))
 
 
+@pytest.mark.parametrize("H,Hkv,dtype", [(300, 300, F16), (300, 100, BF16)])
+def test_many_heads(H, Hkv, dtype):
+    """More heads than a CTA walks over."""
+    lens = [3, 40, 0, 130]
+    s = ref.problem(lens, lens, H, Hkv, dtype, 32, 128, where="sorted", layout="rows")
+    compare(s, run_all(s))
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_long_sequence(dtype):
     s = ref.problem([2049, 100], [2049, 100], 1, 1, dtype, 32, 128)
