@@ -535,6 +535,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                         // Addresses first: a load of the next one could not pass a store to the sums.
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
+                            if (left <= q * 16) break;   // no columns left
                             uint32_t at[16];
                             if (kind == kConsecutive) {
                                 const uint8_t* id = id_row + (off[0] >> 1) + half * 32 + q * 16;
