@@ -17,7 +17,7 @@
 //
 // Measured, both kernels and the sums: 64 sequences of 173 to 403 tokens, 12
 // heads, bf16, positions with gaps: 376 us (memory and products allow 40); 2
-// of 3,279 to 4,099, 8 over 2 heads, f16: 444 us (117); 4 of 79 to 197, 6
+// of 3,279 to 4,099, 8 over 2 heads, f16: 441 us (117); 4 of 79 to 197, 6
 // heads, f16: 29 us.
 //
 // Both have eight row warps: two threads share a row, one for each half of a
