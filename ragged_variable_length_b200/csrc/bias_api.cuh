@@ -139,7 +139,7 @@ dim3 bias_grid(int64_t tiles, int heads, int B) {
 // to 118, 6 heads: 86, 74, 70, 88, 65 us with 1, 2, 3, 4, 6.)
 int heads_per_cta(int64_t row_tiles, int64_t heads, int64_t col_tiles, int64_t slots) {
     constexpr double kSetup = 4, kHead = 1;
-    constexpr int64_t kMost = 64;   // a CTA of the longest sequences then takes some 50 ms, well within the next kernel's waits
+    constexpr int64_t kMost = 64;   // the set-up is then a 16th of a tile's time per head
     int best = 1;
     double best_cost = 1e300;
     for (int n = 1; n <= std::min<int64_t>(heads, kMost); ++n) {

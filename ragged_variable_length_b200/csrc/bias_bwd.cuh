@@ -107,7 +107,9 @@ __device__ __forceinline__ void finish_cta256(const uint32_t* s_tmem, uint32_t c
 // The key-row kernel is launched while the query-row kernel still runs: its
 // CTAs come up as the other's last ones leave, prepare what does not depend on
 // it, and wait here for its end before they read delta, the exponents or the
-// tiles' sums.  (Bounded waits of the other warps meanwhile last a second.)
+// tiles' sums.  The load and MMA warps wait here as well before their first
+// bounded wait for the row warps: that limit is for this kernel's own work, and
+// the other kernel may run for longer.  So for the value kernel.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -282,6 +284,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
             const uint16_t* kb = p.k + s.k_start * p.kv_tok + z;
             const uint16_t* vb = p.v + s.k_start * p.kv_tok + z;
             for (int t = 0; t < nt; ++t, ++g) {
+                if (kScaled<T> && g == kBwdQStages) wait_for_last();
                 if (g >= kBwdQStages) ok = wait.warp(kv_done(g), (g / kBwdQStages - 1) & 1);
                 if (!ok) break;
                 load_rows<kTile>(stage(g), kb, p.kv_tok, t * kTile, s.k_len, lane);
@@ -309,6 +312,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                 mma_commit(s_full);
                 product(dp_col, do_col, stage(g) + kTileBytes);
                 mma_commit(dp_full);
+                if (kScaled<T> && i == 0) wait_for_last();
                 for (int t = 0; t < nt; ++t, ++g) {
                     const bool more = t + 1 < nt;
                     if (more) {
@@ -663,6 +667,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
         uint32_t g = 0;
         for (int i = 0; ok && i < nz && nt > 0; ++i) {
             const int z = z0 + i;
+            if (i == 1) wait_for_last();
             if (i > 0) ok = wait.warp(kv_empty, (i - 1) & 1);
             if (!ok) break;
             const int64_t at = s.k_start * p.kv_tok + z * p.kv_head;
@@ -673,6 +678,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
                 const uint16_t* qb = p.q + s.q_start * p.q_tok + h * p.q_head;
                 const uint16_t* db = a.dout + s.q_start * a.dout_tok + h * 64;
                 for (int t = t0; t < t1; ++t, ++g) {
+                    if (g == kBwdStages) wait_for_last();
                     if (g >= kBwdStages) ok = wait.warp(q_done(g), (g / kBwdStages - 1) & 1);
                     if (!ok) break;
                     load_rows<kTile>(stage(g), qb, p.q_tok, t * kTile, s.q_len, lane);
@@ -708,6 +714,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
                 product(dp_col, sV, stage(g) + kTileBytes);
                 mma_commit(dp_full);
                 if (per_head == 1) mma_commit(kv_empty);   // the head's last product with K and V
+                if (i == 0) wait_for_last();
                 for (uint32_t n = 0; n < per_head; ++n, ++g) {
                     const bool more = n + 1 < per_head;
                     if (more) {

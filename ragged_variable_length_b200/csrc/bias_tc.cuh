@@ -73,7 +73,11 @@ __device__ __forceinline__ void load_rows(uint32_t s_tile, const uint16_t* base,
 // hint the polls of the MMA and load warps took more issue slots than the
 // element-wise work (60 % of all instructions).
 constexpr uint32_t kWaitNs = 4000;
-constexpr uint32_t kWaitLimit = 1u << 18;   // about a second
+// A wait gives up by time, because the hint is an upper limit: a poll may come
+// back at once.  2^18 full sleeps are about a second; the polls have a limit
+// too, which is past that even at 20 cycles each.
+constexpr uint32_t kWaitLimit = 1u << 18;
+constexpr uint32_t kWaitPolls = 1u << 28;
 
 __device__ __forceinline__ bool mbar_try(uint32_t mbar, uint32_t parity) {
     uint32_t done;
@@ -91,10 +95,12 @@ struct Wait {
     int* s_fail;
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {   // one thread
         if (mbar_try(bar, parity)) return true;
-        const uint32_t limit = min(spin_limit(), kWaitLimit);
-        for (uint32_t i = 0; i < limit; ++i) {
+        const int64_t limit = static_cast<int64_t>(min(spin_limit(), kWaitLimit)) * (2 * kWaitNs);   // cycles, at up to 2 GHz
+        const int64_t start = clock64();
+        for (uint32_t i = 0; i < kWaitPolls; ++i) {
             if (mbar_try(bar, parity)) return true;
             if (*reinterpret_cast<volatile int*>(s_fail)) return false;
+            if (clock64() - start > limit) break;
         }
         atomicExch(s_fail, 1);
         return false;
