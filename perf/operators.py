@@ -283,11 +283,15 @@ def run(s):
         return _plain_evict(s) if s["op"] == "evict" else _plain_attention(s)
     import ragged_variable_length_b200 as rv
 
+    def places(p, rows):  # two equal draws at a sequence's cut leave a place too many; the calls take one per row
+        return p if p is None or p.shape[0] == rows else p[:rows]
+
+    pos_k = places(s["pos_k"], s["T"])
     if s["op"] == "evict":
         rows, cu, src, weight, pos = rv.ragged_evict(s["rows"], s["weight"], s["cu_k"], s["max_k"], s["budget"], sinks=s["sinks"],
-                                                     recents=s["recents"], pos=s["pos_k"], total=s["kept"])
+                                                     recents=s["recents"], pos=pos_k, total=s["kept"])
         return {"rows": rows, "cu": cu, "src": src, "weight": weight, "pos": pos}
-    where = dict(pos_q=s["pos_q"], pos_k=s["pos_k"])
+    where = dict(pos_q=places(s["pos_q"], s["q"].shape[0]), pos_k=pos_k)
     seq = (s["cu_q"], s["cu_k"], s["max_q"], s["max_k"], s["table"], s["buckets"])
     out, lse = rv.ragged_attn_bias_fwd(s["q"], s["k"], s["v"], *seq, **where)
     if s["op"] == "attend":
