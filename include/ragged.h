@@ -389,7 +389,11 @@ RAGGED_API ragged_status ragged_pipeline_graph_destroy(ragged_pipeline_graph *gr
  * keep their bias: pos is what ragged_pack's src_idx (modulo L_full) or
  * ragged_evict's pos_out gives.  A query row whose sequence has no keys, or
  * whose scores are all -inf, gets out = 0 and lse = -inf, and passes no
- * gradient.  Rows past the last sequence are neither read nor written.
+ * gradient.  Finite table entries of any size are numbers like others (a row
+ * whose keys all carry -1e9 keeps its softmax), over scores as fp32 holds them;
+ * gradients and weights of rows with |lse| above 512 form the logarithm of the
+ * row's sum again, from plain products, which takes many times longer.  Rows past
+ * the last sequence are neither read nor written.
  *
  *   q                device; element (t, h, c) at q[t * q_tok_stride + h *
  *                    q_head_stride + c].  16-byte aligned, as are both strides

@@ -88,14 +88,14 @@ int64_t bwd_parts(const ragged_bias_attn* a) {
     const int64_t tiles = (avg_q + ragged::bias::kTile - 1) / ragged::bias::kTile;
     return std::max<int64_t>(1, std::min<int64_t>({8, 2LL * sm_count() / ctas, tiles / 4, tiles * (a->H / a->Hkv) / 16}));
 }
-// Workspace of the backward pass: delta [H, lse_stride] floats, four exponents per
+// Workspace of the backward pass: delta and the far rows' sums [H, lse_stride] floats, four exponents per
 // (sequence, head, query tile), the tiles' sums for the table's gradient
 // [H, num_buckets, B, query tiles], an exponent per (sequence, key head, key tile),
 // and the parts' sums of dK and dV.
 int64_t bwd_delta_floats(const ragged_bias_attn* a) { return (a->H * a->lse_stride + 3) & ~int64_t(3); }
 int64_t bwd_items(const ragged_bias_attn* a) { return a->B * a->H * tiles128(a->max_seqlen_q); }
 int64_t bwd_small_floats(const ragged_bias_attn* a) {
-    return (bwd_delta_floats(a) + bwd_items(a) * (4 + a->num_buckets) + a->B * a->Hkv * tiles128(a->max_seqlen_k) + 3) & ~int64_t(3);
+    return (2 * bwd_delta_floats(a) + bwd_items(a) * (4 + a->num_buckets) + a->B * a->Hkv * tiles128(a->max_seqlen_k) + 3) & ~int64_t(3);
 }
 int64_t bwd_workspace(const ragged_bias_attn* a) {
     const int64_t parts = bwd_parts(a);
@@ -450,8 +450,9 @@ ragged_status ragged_attn_bias_bwd(const ragged_bias_attn* a, const void* out, i
     g.dkv_tok = dkv_tok_stride;
     g.dkv_head = a->Hkv > 1 ? dkv_head_stride : 0;
     g.delta = ws;
-    g.tile_exp = reinterpret_cast<int*>(ws + bwd_delta_floats(a));
-    g.partial = ws + bwd_delta_floats(a) + 4 * bwd_items(a);
+    g.log_sum = ws + bwd_delta_floats(a);
+    g.tile_exp = reinterpret_cast<int*>(ws + 2 * bwd_delta_floats(a));
+    g.partial = ws + 2 * bwd_delta_floats(a) + 4 * bwd_items(a);
     g.v_exp = reinterpret_cast<int*>(g.partial + bwd_items(a) * a->num_buckets);
     g.k_tiles = static_cast<int>(tiles128(a->max_seqlen_k));
     g.dtable = static_cast<uint16_t*>(dtable);

@@ -67,6 +67,7 @@ struct BwdArgs {
     uint16_t* dv;
     int64_t dq_tok, dq_head, dkv_tok, dkv_head;
     float* delta;     // [H, lse_stride]
+    float* log_sum;   // [H, lse_stride]: row_log_sum of the far rows, nothing elsewhere
     int* tile_exp;    // [B][H][query tiles][4 warps]: exponent e of the rows of dO, plus f (f16)
     int* v_exp;       // [B][Hkv][key tiles]: exponent f of the rows of V (f16)
     float* partial;   // [H][num_buckets][B][query tiles]
@@ -124,15 +125,19 @@ __device__ __forceinline__ void store_tmem_half(uint32_t taddr, float f, uint16_
     if (valid) store_half_row(dst, w);
 }
 
-// p = 2^(x - lse) of the 32 columns from column c of a tile (x: scores before
-// scale and bias); the negated lse is a row's (nl) or the tile's columns' (neg_lse).
+// p = exp(s - lse) of the 32 columns from column c of a tile (x: scores before
+// scale and bias).  The negated lse in base 2 is a row's (nl) or the tile's
+// columns' (neg_lse); of far ones it is the logarithm of their sum only, and
+// the tile is of kFarKind, which takes off their largest scores (mu, mu_cols).
+// (As a kind of tile that costs no other tile anything; a step between the bias
+// and the exponentials cost 3 to 10 % of the kernels.)
 template <typename T>
 __device__ __forceinline__ void probabilities(const Bias16& t, const Problem& p, int kind, const int* off, int c,
-                                              const float* neg_lse, float nl, float (&x)[32]) {
+                                              const float* neg_lse, float nl, const float* mu_cols, float mu, float (&x)[32]) {
     const bool flat = kind == kLeft || kind == kRight;
     const float scale = flat ? p.scale_log2 : kLog2e;
     const float add = flat ? to_float<T>(t.vec[kind == kLeft ? 0 : t.last]) * kLog2e : 0.f;
-    if (!flat) bias_add<T>(t, kind, off, c, p.scale, x);
+    if (!flat) bias_add<T, true>(t, kind, off, c, p.scale, x, mu_cols, mu);
     const uint64_t sc2 = f2(scale, scale), add2 = f2(add, add);
     if (neg_lse == nullptr) {
         const uint64_t c2 = f2(add + nl, add + nl);
@@ -383,7 +388,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
         };
         load_row(h0);
         bias_map<kBwdRows>(p, map, p.num_buckets);
-        if (has_entry) s_tab[tid] = bias_bits<T>(entry);
+        if (has_entry) s_tab[tid] = entry;
         if (tid == p.num_buckets) s_tab[tid] = 0;
         for (int n = 0; n <= p.num_buckets; ++n) acc[n * kBwdRows + tid] = 0.f;
         bias_rows<kBwdRows>(t, p, pos, valid, a.span, s_red);
@@ -406,7 +411,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                 if (half == 0) s_undo[r] = valid ? undo : 0.f;
                 if (more) {
                     load_row(h0 + i + 1);
-                    if (has_entry) s_tab[tid] = bias_bits<T>(__ldg(column + i + 1));
+                    if (has_entry) s_tab[tid] = __ldg(column + i + 1);
                 }
                 rows_barrier<kBwdRows>();   // sums complete, the last head's entries no longer read
                 for (int n = warp; n < p.num_buckets; n += 8) {   // each thread's sums, unscaled, in a fixed order
@@ -481,7 +486,18 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                 const int top = __reduce_max_sync(0xffffffffu, e);
                 if (half == 0 && lane == 0) a.tile_exp[(item0 + static_cast<int64_t>(i) * a.q_tiles) * 4 + warp] = top;
             }
-            const float nl = valid ? -lse_log2(lse) : -INFINITY;
+            float nl = valid ? -lse_log2(lse) : -INFINITY, mu = 0.f;
+            uint32_t todo = __ballot_sync(0xffffffffu, valid && is_far(lse));
+            const bool far = todo != 0;
+            for (; todo != 0; todo &= todo - 1) {
+                const int src = __ffs(todo) - 1;
+                const float ls = row_log_sum<T>(p, s, q0 + (warp & 3) * 32 + src, h);
+                if (lane == src) {
+                    mu = lse - ls;
+                    nl = -ls * kLog2e;
+                    if (half == 0) a.log_sum[h * p.lse_stride + t_row] = ls;
+                }
+            }
             const uint64_t r2 = f2(rs, rs), nd2 = f2(-delta * rs, -delta * rs);
             far_left = far_right = 0.f;
             for (int tile = 0; tile < nt; ++tile, ++g) {
@@ -491,7 +507,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                     cols.store(t, tile * kTile, s.k_len);
                     rows_barrier<kBwdRows>();
                 }
-                const int kind = tile_kind(t, tile % kChunkTiles);
+                const int kind = far ? kFarKind : tile_kind(t, tile % kChunkTiles);
                 const int* off = t.off + (tile % kChunkTiles) * kTile;
                 const int left = s.k_len - tile * kTile - half * 32;   // columns of this half
                 float x[32];
@@ -503,7 +519,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                 fence_before_sync();
                 mbar_arrive(a_full);
                 if (ok && warp_rows) {
-                    probabilities<T>(t, p, kind, off, half * 32, nullptr, nl, x);
+                    probabilities<T>(t, p, kind, off, half * 32, nullptr, nl, nullptr, mu, x);
                     if (left < 32) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
@@ -545,7 +561,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                                 const uint8_t* id = id_row + (off[0] >> 1) + half * 32 + q * 16;
 #pragma unroll
                                 for (int c = 0; c < 16; ++c) at[c] = id[c];
-                            } else if (kind == kGeneral) {
+                            } else if (kind == kGeneral || (kind == kFarKind && t.near)) {
 #pragma unroll
                                 for (int c = 0; c < 4; ++c) {
                                     const int4 o = *reinterpret_cast<const int4*>(off + half * 32 + q * 16 + 4 * c);
@@ -570,7 +586,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
     finish_cta256(&s_tmem, kTmemCols, warp, &s_fail);
 }
 
-__host__ __device__ constexpr int bwd_kv_fixed_bytes() { return 1024 + 2 * kRowBytes + kBwdStages * 2 * kTileBytes + 12 * kChunk; }
+__host__ __device__ constexpr int bwd_kv_fixed_bytes() { return 1024 + 2 * kRowBytes + kBwdStages * 2 * kTileBytes + 16 * kChunk; }
 __host__ __device__ constexpr int bwd_kv_smem_bytes(int D, int span) {
     return bwd_kv_fixed_bytes() + vec16_bytes(D, span) + ids_bytes(D, span);
 }
@@ -758,6 +774,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
         t.off = reinterpret_cast<int*>(ids + ids_bytes(p.D, a.span));
         float* s_lse = reinterpret_cast<float*>(t.off + kChunk);   // negated
         float* s_delta = s_lse + kChunk;
+        float* s_mu = s_delta + kChunk;
         t.tiles = s_tiles;
         uint8_t* map = ids + ((vec_entries(p.D, a.span) + 15) & ~15);
         const bool has_entry = tid < p.num_buckets;
@@ -769,7 +786,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
         Columns<kBwdRows> cols;
         cols.load(t0 * kTile, s.q_len, query_at);
         bias_map<kBwdRows>(p, map, p.num_buckets);
-        if (has_entry) s_tab[tid] = bias_bits<T>(entry);
+        if (has_entry) s_tab[tid] = entry;
         if (tid == p.num_buckets) s_tab[tid] = 0;
         bias_rows<kBwdRows>(t, p, pos, valid, a.span, s_red);
         bias_ids<-1, kBwdRows>(t, map, ids, p.num_buckets);
@@ -842,24 +859,30 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
                         d_next[k] = c < s.q_len ? delta[c] : 0.f;
                     }
                 };
-                auto store_stats = [&](int c0) {
+                auto store_stats = [&](int c0) {   // whether one of them is far
+                    bool any = false;
 #pragma unroll
                     for (int k = 0; k < kChunk / kBwdRows; ++k) {
                         const int c = tid + k * kBwdRows;
-                        const bool in = c0 + c < s.q_len;   // no such query: p = 0
-                        s_lse[c] = in ? shift - lse_log2(l_next[k]) : -INFINITY;
+                        const bool in = c0 + c < s.q_len, far = in && is_far(l_next[k]);   // no such query: p = 0
+                        const float ls = far ? a.log_sum[h * p.lse_stride + s.q_start + c0 + c] : 0.f;
+                        s_lse[c] = !in ? -INFINITY : shift - (far ? ls * kLog2e : lse_log2(l_next[k]));
+                        s_mu[c] = far ? l_next[k] - ls : 0.f;
                         s_delta[c] = in ? -d_next[k] * rs : 0.f;
+                        any |= far;
                     }
+                    return any;
                 };
                 load_stats(t0 * kTile);
                 const bool start = h == z0 * p.group;   // the first head's entries are in s_tab, its columns stored
                 const uint16_t next = start ? uint16_t(0) : __ldg(column + h);
                 rows_barrier<kBwdRows>();   // the last head's entries and columns are no longer read
                 if (!start) {
-                    if (has_entry) s_tab[tid] = bias_bits<T>(next);
+                    if (has_entry) s_tab[tid] = next;
                     rows_barrier<kBwdRows>();
                 }
                 bias_fill<kBwdRows>(t, ids, s_tab);
+                bool far = false;
                 for (int tile = 0; tile < nt; ++tile, ++g) {
                     if (tile % kChunkTiles == 0) {
                         const int c0 = (t0 + tile) * kTile;
@@ -868,16 +891,15 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_kv_kernel(const Probl
                         if (again) cols.load(c0, s.q_len, query_at);
                         if (tile > 0) rows_barrier<kBwdRows>();
                         if (again) cols.store<true>(t, c0, s.q_len);
-                        store_stats(c0);
-                        rows_barrier<kBwdRows>();
+                        far = rows_any<kBwdRows>(store_stats(c0));
                     }
-                    const int kind = tile_kind(t, tile % kChunkTiles), c0 = (tile % kChunkTiles) * kTile;
+                    const int kind = far ? kFarKind : tile_kind(t, tile % kChunkTiles), c0 = (tile % kChunkTiles) * kTile;
                     float x[32];
                     ok = ok && wait.warp(s_full, g & 1);
                     if (ok && warp_rows) {
                         fence_after_sync();
                         tmem_ld32(t_lane + half * 32, x);
-                        probabilities<T>(t, p, kind, t.off + c0, half * 32, s_lse + c0, 0.f, x);
+                        probabilities<T>(t, p, kind, t.off + c0, half * 32, s_lse + c0, 0.f, s_mu + c0, 0.f, x);
                         uint32_t w[16];
 #pragma unroll
                         for (int c = 0; c < 16; ++c) w[c] = Cvt<T>::pack(x[2 * c], x[2 * c + 1]);
@@ -963,7 +985,26 @@ constexpr int kWeightStages = 3;
 constexpr uint32_t kWeightTmem = 128;
 
 __host__ __device__ constexpr int weight_smem_bytes(int D, int span) {
-    return 1024 + kRowBytes + kWeightStages * kTileBytes + 8 * kChunk + vec16_bytes(D, span) + ids_bytes(D, span);
+    return 1024 + kRowBytes + kWeightStages * kTileBytes + 12 * kChunk + vec16_bytes(D, span) + ids_bytes(D, span);
+}
+
+// The statistics of a chunk's far queries, each warp those of its own threads'
+// columns.  Every key tile forms them again: there is no place to keep them.
+template <typename T>
+__device__ __forceinline__ void far_columns(const Problem& p, const Seq& s, int h, int c0, float* s_lse, float* s_mu) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int c = threadIdx.x; c < kChunk; c += 128) {
+        const float l = c0 + c < s.q_len ? p.lse[h * p.lse_stride + s.q_start + c0 + c] : 0.f;
+        for (uint32_t todo = __ballot_sync(0xffffffffu, is_far(l)); todo != 0; todo &= todo - 1) {
+            const int src = __ffs(todo) - 1;
+            const float ls = row_log_sum<T>(p, s, c0 + c - lane + src, h);
+            if (lane == src) {
+                s_lse[c] = -ls * kLog2e;
+                s_mu[c] = l - ls;
+            }
+        }
+    }
 }
 
 template <typename T>
@@ -1061,6 +1102,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         uint8_t* ids = extra + vec16_bytes(p.D, span);
         t.off = reinterpret_cast<int*>(ids + ids_bytes(p.D, span));
         float* s_lse = reinterpret_cast<float*>(t.off + kChunk);   // negated
+        float* s_mu = s_lse + kChunk;
         t.tiles = s_tiles;
         uint8_t* map = ids + ((vec_entries(p.D, span) + 15) & ~15);
         const bool has_entry = tid < p.num_buckets;
@@ -1072,7 +1114,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         Columns<128> cols;
         cols.load(0, s.q_len, query_at);
         bias_map<128>(p, map, p.num_buckets);
-        if (has_entry) s_tab[tid] = bias_bits<T>(entry);
+        if (has_entry) s_tab[tid] = entry;
         if (tid == p.num_buckets) s_tab[tid] = 0;
         bias_rows<128>(t, p, pos, valid, span, s_red);
         bias_ids<-1, 128>(t, map, ids, p.num_buckets);
@@ -1095,11 +1137,12 @@ __global__ void __launch_bounds__(kThreads, 3)
             const uint16_t next = i == 0 ? uint16_t(0) : __ldg(column + i);
             rows_barrier<128>();   // the last head's entries and columns are no longer read
             if (i > 0) {
-                if (has_entry) s_tab[tid] = bias_bits<T>(next);
+                if (has_entry) s_tab[tid] = next;
                 rows_barrier<128>();
             }
             bias_fill<128>(t, ids, s_tab);
             float sum_all = 0.f;
+            bool far = false;
             for (int tile = 0; tile < nt; ++tile, ++g) {
                 if (tile % kChunkTiles == 0) {
                     const int c0 = tile * kTile;
@@ -1108,14 +1151,18 @@ __global__ void __launch_bounds__(kThreads, 3)
                     if (again) cols.load(c0, s.q_len, query_at);
                     if (tile > 0) rows_barrier<128>();
                     if (again) cols.store<true>(t, c0, s.q_len);
+                    bool mine = false;
 #pragma unroll
                     for (int k = 0; k < kChunk / 128; ++k) {
                         const int c = tid + k * 128;
                         s_lse[c] = c0 + c < s.q_len ? -lse_log2(l_next[k]) : -INFINITY;
+                        s_mu[c] = 0.f;
+                        mine |= c0 + c < s.q_len && is_far(l_next[k]);
                     }
-                    rows_barrier<128>();
+                    if (__any_sync(0xffffffffu, mine)) far_columns<T>(p, s, h, c0, s_lse, s_mu);
+                    far = rows_any<128>(mine);
                 }
-                const int kind = tile_kind(t, tile % kChunkTiles), c0 = (tile % kChunkTiles) * kTile;
+                const int kind = far ? kFarKind : tile_kind(t, tile % kChunkTiles), c0 = (tile % kChunkTiles) * kTile;
                 ok = ok && wait.warp(s_full(g), (g / 3) & 1);
                 if (ok && warp_rows) {
                     fence_after_sync();
@@ -1128,7 +1175,7 @@ __global__ void __launch_bounds__(kThreads, 3)
                             fence_before_sync();
                             mbar_arrive(a_full(g));
                         }
-                        probabilities<T>(t, p, kind, t.off + c0, hf * 32, s_lse + c0, 0.f, x);
+                        probabilities<T>(t, p, kind, t.off + c0, hf * 32, s_lse + c0, 0.f, s_mu + c0, 0.f, x);
 #pragma unroll
                         for (int c = 0; c < 16; ++c) sum = f2_add(sum, f2(x[2 * c], x[2 * c + 1]));
                     }

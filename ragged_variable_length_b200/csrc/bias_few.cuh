@@ -126,7 +126,7 @@ struct Few {
         }
         for (int i = tid; i < p.num_buckets * MT * 16; i += kThreadsF) {
             const int b = i / (MT * 16), r = i - b * (MT * 16);
-            t[i] = r < rows ? bias_log2<T>(__ldg(p.table + static_cast<int64_t>(b) * p.H + head_of(p, r))) : 0.f;
+            t[i] = r < rows ? to_float<T>(__ldg(p.table + static_cast<int64_t>(b) * p.H + head_of(p, r))) : 0.f;
         }
         if constexpr (kMap)
             for (int i = tid; i <= 2 * p.D; i += kThreadsF) m[i] = static_cast<uint8_t>(bucket_of(p, i - p.D));   // -1: 255
@@ -193,7 +193,7 @@ struct Few {
         if (p.pos_k != nullptr && lane < kFewKeys)   // past the end: a position of the block
             cp_async_4(st + kStage - kFewKeys * 4 + 4 * lane, p.pos_k + s.k_start + min(key0 + lane, s.k_len - 1), 4);
     }
-    // Scores in base 2 of block n (keys from key0): x[tile][8 keys][row g: 2 columns, row g + 8: 2 columns].
+    // Scores of block n (keys from key0): x[tile][8 keys][row g: 2 columns, row g + 8: 2 columns].
     __device__ __forceinline__ void scores(const Problem& p, int n, int key0, float (&x)[MT][2][4]) const {
         const uint32_t st = stage(n);
 #pragma unroll
@@ -230,7 +230,7 @@ struct Few {
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) x[t][i][2 * k + j] = fmaf(x[t][i][2 * k + j], p.scale_log2, e);
+                        for (int j = 0; j < 2; ++j) x[t][i][2 * k + j] = fmaf(x[t][i][2 * k + j], p.scale, e);
                 }
         } else {
 #pragma unroll
@@ -243,7 +243,7 @@ struct Few {
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const int d = max(-p.D, min(p.D, pos_diff(pk, pq[t][k])));
-                            x[t][i][2 * k + j] = fmaf(x[t][i][2 * k + j], p.scale_log2, entry(p, t * 16 + g + 8 * k, d));
+                            x[t][i][2 * k + j] = fmaf(x[t][i][2 * k + j], p.scale, entry(p, t * 16 + g + 8 * k, d));
                         }
                 }
         }
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(32 * NW) bias_few_kernel(const Problem p, uint
             bool grow = false;
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-                grow |= fmaxf(fmaxf(x[t][0][2 * k], x[t][0][2 * k + 1]), fmaxf(x[t][1][2 * k], x[t][1][2 * k + 1])) > m[t][k] + 8.f;
+                grow |= fmaxf(fmaxf(x[t][0][2 * k], x[t][0][2 * k + 1]), fmaxf(x[t][1][2 * k], x[t][1][2 * k + 1])) > m[t][k] + 8.f * kLn2;
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(32 * NW) bias_few_kernel(const Problem p, uint
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
                     const float next = fmaxf(m[t][k], v);
-                    const float alpha = next == -INFINITY ? 1.f : mma_attn::fast_exp2(m[t][k] - next);
+                    const float alpha = next == -INFINITY ? 1.f : mma_attn::fast_exp2((m[t][k] - next) * kLog2e);
                     m[t][k] = next;
                     l[t][k] *= alpha;
 #pragma unroll
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(32 * NW) bias_few_kernel(const Problem p, uint
                 const float ref = m[t][k] == -INFINITY ? 0.f : m[t][k];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float a = mma_attn::fast_exp2(x[t][i][2 * k] - ref), b = mma_attn::fast_exp2(x[t][i][2 * k + 1] - ref);
+                    const float a = mma_attn::fast_exp2((x[t][i][2 * k] - ref) * kLog2e), b = mma_attn::fast_exp2((x[t][i][2 * k + 1] - ref) * kLog2e);
                     l[t][k] += a + b;
                     const uint32_t w = mma_attn::Mma<T>::pack(a, b);
                     hi[t][2 * i + k] = w;
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(32 * NW) bias_few_kernel(const Problem p, uint
     }
     cp_async_wait<0>();
     __syncthreads();
-    // The warps' states, then the CTA's, then the cluster's: out = sum 2^(m - M) o / sum 2^(m - M) l.
+    // The warps' states, then the CTA's, then the cluster's: out = sum e^(m - M) o / sum e^(m - M) l.
     float* so = reinterpret_cast<float*>(few_smem);   // [warp][row][64], over the rings
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(32 * NW) bias_few_kernel(const Problem p, uint
         float acc = 0.f, sum = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float a = mma_attn::fast_exp2(s_m[w][r] - ref);
+            const float a = mma_attn::fast_exp2((s_m[w][r] - ref) * kLog2e);
             acc = fmaf(a, so[(w * MT * 16 + r) * 64 + d], acc);
             sum = fmaf(a, s_l[w][r], sum);
         }
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(32 * NW) bias_few_kernel(const Problem p, uint
 #pragma unroll
             for (int c = 0; c < kFewMaxSplits; ++c)
                 if (c < splits) {
-                    const float w = mma_attn::fast_exp2(mc[c] - ref);
+                    const float w = mma_attn::fast_exp2((mc[c] - ref) * kLog2e);
                     sum = fmaf(w, cluster_read(&s_lc[r], c), sum);
                     a0 = fmaf(w, cluster_read(so + r * 64 + d, c), a0);
                     a1 = fmaf(w, cluster_read(so + r * 64 + d + 1, c), a1);
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(32 * NW) bias_few_kernel(const Problem p, uint
         const int h = f.head_of(p, r);
         const int64_t t = f.s.q_start + f.query_of(r);
         *reinterpret_cast<uint32_t*>(out + t * out_tok + h * 64 + d) = empty ? 0u : mma_attn::Mma<T>::pack(a0 * inv, a1 * inv);
-        if (d == 0) p.lse[h * p.lse_stride + t] = empty ? -INFINITY : (top + log2f(sum)) * kLn2;
+        if (d == 0) p.lse[h * p.lse_stride + t] = empty ? -INFINITY : fmaf(log2f(sum), kLn2, top);
     }
     if (splits > 1) cluster_sync();   // this CTA's shared memory has been read
 }
@@ -439,6 +439,7 @@ __global__ void __launch_bounds__(32 * NW)
     bias_few_weight_kernel(const Problem p, const float* prev, float* weight, int64_t weight_stride) {
     extern __shared__ __align__(128) uint8_t few_smem[];
     __shared__ float s_p[NW][MT * 16][kFewKeys + 1];
+    __shared__ float s_log_sum[MT * 16];   // of the far rows
     const int splits = gridDim.x, rank = blockIdx.x;
     Few<T, MT, NW, true> f;
     f.z = blockIdx.y;
@@ -471,14 +472,38 @@ __global__ void __launch_bounds__(32 * NW)
         cp_async_commit();
     }
     f.setup(p, few_smem);
-    float lse[MT][2];
+    auto lse_of = [&](int r) { return r < f.rows ? __ldg(p.lse + f.head_of(p, r) * p.lse_stride + f.s.q_start + f.query_of(r)) : -INFINITY; };
+    float nl[MT][2], mu[MT][2];
+    bool far = false;
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int r = t * 16 + f.g + 8 * k;
-            lse[t][k] = r < f.rows ? lse_log2(__ldg(p.lse + f.head_of(p, r) * p.lse_stride + f.s.q_start + f.query_of(r))) : INFINITY;
+            const float l = lse_of(t * 16 + f.g + 8 * k);
+            nl[t][k] = -lse_log2(l);
+            mu[t][k] = 0.f;
+            far |= is_far(l);
         }
+    far = __any_sync(0xffffffffu, far);   // every warp sees all rows
+    if (far) {
+#pragma unroll 1
+        for (int r = f.warp; r < f.rows; r += NW) {
+            if (!is_far(lse_of(r))) continue;
+            const float ls = row_log_sum<T>(p, f.s, f.query_of(r), f.head_of(p, r));
+            if (f.lane == 0) s_log_sum[r] = ls;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int r = t * 16 + f.g + 8 * k;
+                const float l = lse_of(r);
+                if (!is_far(l)) continue;
+                nl[t][k] = -s_log_sum[r] * kLog2e;
+                mu[t][k] = l - s_log_sum[r];
+            }
+    }
     int n = 0;
     for (int blk = first; blk < end; blk += NW, ++n) {
         cp_async_wait<kFewStages - 2>();
@@ -488,13 +513,21 @@ __global__ void __launch_bounds__(32 * NW)
         cp_async_commit();
         float x[MT][2][4];
         f.scores(p, n, blk * kFewKeys, x);
+        if (far) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[t][i][j] = fminf(x[t][i][j] - mu[t][j >> 1], mu[t][j >> 1] != 0.f ? 0.f : INFINITY);
+        }
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    s_p[f.warp][t * 16 + f.g + 8 * (j >> 1)][i * 8 + f.c2 + (j & 1)] = mma_attn::fast_exp2(x[t][i][j] - lse[t][j >> 1]);
+                    s_p[f.warp][t * 16 + f.g + 8 * (j >> 1)][i * 8 + f.c2 + (j & 1)] = mma_attn::fast_exp2(fmaf(x[t][i][j], kLog2e, nl[t][j >> 1]));
         __syncwarp();
         // Key lane % 16 of heads lane / 16, + 2, ...: this block's sums over the queries, in their order.
         const int key = f.lane & 15, h0 = f.lane >> 4, j = blk * kFewKeys + key;

@@ -50,7 +50,7 @@ constexpr int kVecPad = 64;           // a partial tile of consecutive positions
 constexpr int kSpan = 1024;           // largest R that the expanded table covers
 constexpr uint32_t kTmemCols = 256;
 
-enum TileKind { kGeneral = 0, kLeft = 1, kRight = 2, kConsecutive = 3, kClamped = 4 };
+enum TileKind { kGeneral = 0, kLeft = 1, kRight = 2, kConsecutive = 3, kClamped = 4, kFarKind = 5 };
 
 __host__ __device__ constexpr int vec_entries(int D, int span) { return 2 * (D + span) + 1 + kVecPad; }
 
@@ -148,18 +148,6 @@ __device__ __forceinline__ void store_row(uint16_t* dst, const uint32_t (&w)[32]
 // factor log2 e goes into the exponent's multiply-add.
 // ---------------------------------------------------------------------------
 
-// A table entry as the kernels keep it: finite values stay within +-2^126, so
-// that a row whose keys all carry the type's lowest value keeps its softmax
-// over them when log2 e multiplies it.
-template <typename T>
-__device__ __forceinline__ uint16_t bias_bits(uint16_t x) {
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        const uint16_t mag = x & 0x7fffu;
-        if (mag > 0x7e80u && mag < 0x7f80u) return static_cast<uint16_t>((x & 0x8000u) | 0x7e80u);
-    }
-    return x;
-}
-
 // What a tile of columns is for the rows of one warp.
 struct TileInfo {
     int lo, hi;   // extremes of the columns' positions
@@ -182,6 +170,17 @@ struct Bias16 {
 template <int NR>
 __device__ __forceinline__ void rows_barrier() {
     asm volatile("bar.sync 1, %0;" ::"n"(NR) : "memory");
+}
+
+// The same, and whether any of the threads has x.
+template <int NR>
+__device__ __forceinline__ bool rows_any(bool x) {
+    int any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any)
+                 : "r"(static_cast<int>(x)), "n"(NR)
+                 : "memory");
+    return any != 0;
 }
 
 // The bucket map as bytes in shared memory (none: an entry outside the table).
@@ -288,9 +287,12 @@ __device__ __forceinline__ int tile_kind(const Bias16& t, int tile) {
     const int4 i = *reinterpret_cast<const int4*>(t.tiles + tile);
     return pos_diff(i.y, t.wlo) <= -t.D ? kLeft : pos_diff(i.x, t.whi) >= t.D ? kRight : i.z;
 }
-// x = x * scale + bias for 32 columns from column c of a tile (not for kLeft, kRight).
-template <typename T>
-__device__ __forceinline__ void bias_add(const Bias16& t, int kind, const int* off, int c, float scale, float (&x)[32]) {
+// x = x * scale + bias for 32 columns from column c of a tile (not for kLeft,
+// kRight).  kFarKind (with FAR), whatever the columns' positions: the largest
+// score of the far rows or columns is taken off, mu or mu_cols (0: not far).
+template <typename T, bool FAR = false>
+__device__ __forceinline__ void bias_add(const Bias16& t, int kind, const int* off, int c, float scale, float (&x)[32],
+                                         const float* mu_cols = nullptr, float mu = 0.f) {
     const uint64_t sc2 = f2(scale, scale);
     const char* row = reinterpret_cast<const char*>(t.vec) + t.row;
     auto at = [&](int o) { return to_float<T>(*reinterpret_cast<const uint16_t*>(row + o)); };
@@ -308,11 +310,19 @@ __device__ __forceinline__ void bias_add(const Bias16& t, int kind, const int* o
             f2_split(f2_fma(f2(x[4 * i], x[4 * i + 1]), sc2, f2(at(o.x), at(o.y))), x[4 * i], x[4 * i + 1]);
             f2_split(f2_fma(f2(x[4 * i + 2], x[4 * i + 3]), sc2, f2(at(o.z), at(o.w))), x[4 * i + 2], x[4 * i + 3]);
         }
-    } else {
+    } else if (!FAR || kind == kClamped) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             const int d = max(-t.D, min(t.D, pos_diff(off[c + i], t.p_row)));
             x[i] = fmaf(x[i], scale, to_float<T>(t.vec[d + t.D]));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const int o = off[c + i];   // of a place past both ends of the map it is that end's
+            const float e = t.near ? at(o) : to_float<T>(t.vec[max(-t.D, min(t.D, pos_diff(o, t.p_row))) + t.D]);
+            const float m = mu_cols != nullptr ? mu_cols[c + i] : mu;
+            x[i] = fminf(fmaf(x[i], scale, e) - m, m != 0.f ? 0.f : INFINITY);
         }
     }
 }
@@ -555,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         Columns<128> cols;
         cols.load(0, s.k_len, key_at);
         bias_map<128>(p, map, p.num_buckets);
-        if (has_entry) s_tab[0][tid] = bias_bits<T>(entry);
+        if (has_entry) s_tab[0][tid] = entry;
         if (tid == p.num_buckets) s_tab[0][tid] = s_tab[1][tid] = 0;
         bias_rows<128>(t, p, pos, valid, span, s_red);
         bias_ids<1, 128>(t, map, ids, p.num_buckets);
@@ -590,19 +600,20 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int j = 0; j < 16; ++j) pk[j] = empty ? 0u : Cvt<T>::pack(v[2 * j] * inv, v[2 * j + 1] * inv);
                 if (valid) store_half_row(dst + hf * 32, pk);
             }
-            if (valid) p.lse[h * p.lse_stride + t_row] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (valid) p.lse[h * p.lse_stride + t_row] = empty ? -INFINITY : fmaf(log2f(l), kLn2, m);
         };
         for (int i = 0; i < nh; ++i) {
             // This head's entries are complete and the last head's no longer read after
             // this barrier; the next head's are filled in behind it.
-            if (i + 1 < nh && has_entry) s_tab[(i + 1) & 1][tid] = bias_bits<T>(__ldg(column + i + 1));
+            if (i + 1 < nh && has_entry) s_tab[(i + 1) & 1][tid] = __ldg(column + i + 1);
             rows_barrier<128>();
             if (i + 1 < nh) {
                 t.vec = vec0 + ((i + 1) & 1) * vec_step;
                 bias_fill<128>(t, ids, s_tab[(i + 1) & 1]);
             }
             t.vec = vec0 + (i & 1) * vec_step;
-            float m_ref = -INFINITY, l0 = 0.f, l1 = 0.f;
+            float m_ref = -INFINITY, neg_ref = 0.f, l0 = 0.f, l1 = 0.f;   // neg_ref: -m_ref in base 2, or 0
+            bool far = false;                                              // some row of the warp is
             for (int tile = 0; tile < nt; ++tile, ++g) {
                 if (tile % kChunkTiles == 0 && (tile > 0 || (i > 0 && nt > kChunkTiles))) {
                     cols.load(tile * kTile, s.k_len, key_at);
@@ -620,10 +631,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                     tmem_ld32(s_buf, x[0]);
                     tmem_ld32(s_buf + 32, x[1]);
                     // Scores in base 2 are x * scale + add; one bias for the whole tile goes into `add`.
-                    float scale = kLog2e, add = 0.f;
-                    if (kind == kLeft || kind == kRight) {
+                    const bool flat = kind == kLeft || kind == kRight;
+                    float scale = kLog2e, add = 0.f, entry = 0.f;
+                    if (flat) {
                         scale = p.scale_log2;
-                        add = to_float<T>(t.vec[kind == kLeft ? 0 : t.last]) * kLog2e;
+                        entry = to_float<T>(t.vec[kind == kLeft ? 0 : t.last]);
+                        add = entry * kLog2e;
                     } else {
                         bias_add<T>(t, kind, off, 0, p.scale, x[0]);
                         bias_add<T>(t, kind, off, 32, p.scale, x[1]);
@@ -645,16 +658,18 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                         mt = fmax3(mt, fmaxf(a, x[hf][15]), fmaxf(c, x[hf][31]));
                     }
-                    mt = fmaf(mt, scale, add);
-                    const bool grow = mt > m_ref + kRescaleThreshold;
+                    if (flat) mt = fmaf(mt, p.scale, entry);
+                    const bool grow = mt > m_ref + kRescaleThreshold * kLn2;
                     if (__any_sync(0xffffffffu, grow)) {
                         float alpha = 1.f;
                         if (grow) {
-                            alpha = mma_attn::fast_exp2(m_ref - mt);
+                            alpha = mma_attn::fast_exp2((m_ref - mt) * kLog2e);
                             l0 *= alpha;
                             l1 *= alpha;
                             m_ref = mt;
+                            neg_ref = -mt * kLog2e;
                         }
+                        far = __any_sync(0xffffffffu, is_far(m_ref));
                         if (tile > 0) {   // O holds the head's products so far
                             confirm_pv(g - 1);
                             fence_after_sync();
@@ -671,22 +686,43 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                     }
                     // A row without a finite score so far has no reference: p = 2^-inf = 0.
-                    const float ref = m_ref == -INFINITY ? add : add - m_ref;
+                    const float ref = add + neg_ref;
                     const uint64_t sc2 = f2(scale, scale), ref2 = f2(ref, ref);
                     uint64_t sum = f2(l0, l1);
+                    if (__builtin_expect(far, false)) {   // (a change of x ahead of one loop for both costs 10 % of the time)
+                        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        uint32_t pk[16];
+                        for (int hf = 0; hf < 2; ++hf) {
+                            uint32_t pk[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float a, c;
-                            f2_split(f2_fma(f2(x[hf][2 * j], x[hf][2 * j + 1]), sc2, ref2), a, c);
-                            a = mma_attn::fast_exp2(a);
-                            c = mma_attn::fast_exp2(c);
-                            sum = f2_add(sum, f2(a, c));
-                            pk[j] = Cvt<T>::pack(a, c);
+                            for (int j = 0; j < 16; ++j) {
+                                float a = x[hf][2 * j], c = x[hf][2 * j + 1];
+                                if (flat) {
+                                    a = fmaf(a, p.scale, entry);
+                                    c = fmaf(c, p.scale, entry);
+                                }
+                                a = mma_attn::fast_exp2((a - mu) * kLog2e);
+                                c = mma_attn::fast_exp2((c - mu) * kLog2e);
+                                sum = f2_add(sum, f2(a, c));
+                                pk[j] = Cvt<T>::pack(a, c);
+                            }
+                            tmem_st16_u(s_buf + hf * 16, pk);
                         }
-                        tmem_st16_u(s_buf + hf * 16, pk);
+                    } else {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                float a, c;
+                                f2_split(f2_fma(f2(x[hf][2 * j], x[hf][2 * j + 1]), sc2, ref2), a, c);
+                                a = mma_attn::fast_exp2(a);
+                                c = mma_attn::fast_exp2(c);
+                                sum = f2_add(sum, f2(a, c));
+                                pk[j] = Cvt<T>::pack(a, c);
+                            }
+                            tmem_st16_u(s_buf + hf * 16, pk);
+                        }
                     }
                     f2_split(sum, l0, l1);
                     tmem_wait_st();
