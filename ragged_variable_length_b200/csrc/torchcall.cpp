@@ -14,6 +14,9 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <cmath>
+
 #include "ragged.h"
 
 namespace {
@@ -83,16 +86,22 @@ struct Scratch {
     }
 };
 
-// The arguments that the three attention operators share.
+// The arguments that the three attention operators share: their tensors, ...
+struct Shared {
+    const Tensor &cu_q, &cu_k, &table, &buckets;
+    const Tensor pos_q, pos_k;
+    explicit Shared(PyObject* const* o)
+        : cu_q(tensor(o[0], "cu_seqlens_q")), cu_k(tensor(o[1], "cu_seqlens_k")), table(tensor(o[4], "table")), buckets(tensor(o[5], "buckets")),
+          pos_q(maybe(o[6], "pos_q")), pos_k(maybe(o[7], "pos_k")) {}
+};
+// ... and the library's view of them, checked.
 struct Problem {
     ragged_bias_attn a;
     Devices dev;
     int64_t Tq, Tk;
 
-    Problem(const Tensor& q, const Tensor& k, const Tensor& v, PyObject* const* o, const Tensor& lse) {
-        const Tensor &cu_q = tensor(o[0], "cu_seqlens_q"), &cu_k = tensor(o[1], "cu_seqlens_k");
-        const Tensor &table = tensor(o[4], "table"), &buckets = tensor(o[5], "buckets");
-        const Tensor pos_q = maybe(o[6], "pos_q"), pos_k = maybe(o[7], "pos_k");
+    Problem(const Tensor& q, const Tensor& k, const Tensor& v, PyObject* const* o, const Shared& in, const Tensor& lse) {
+        const Tensor &cu_q = in.cu_q, &cu_k = in.cu_k, &table = in.table, &buckets = in.buckets, &pos_q = in.pos_q, &pos_k = in.pos_k;
         TORCH_CHECK_VALUE(q.dim() == 3 && k.dim() == 3, "q must be [Tq, H, head_dim], k and v [Tk, Hkv, head_dim]");
         const auto type = q.scalar_type();
         TORCH_CHECK_VALUE(v.sizes() == k.sizes() && k.size(2) == q.size(2) && k.scalar_type() == type &&
@@ -180,11 +189,69 @@ Tensor result(PyObject* o, const Tensor& like, const char* what) {
     return t;
 }
 
-// A result is written while the inputs are still read, and while other results are written.
+// The bytes of a tensor: runs of `len` at base + i * step[0] + j * step[1] + ...
+struct Bytes {
+    int64_t base, len;
+    int dims = 0;
+    int64_t size[8], step[8];   // from the smallest step to the largest
+    bool itself = false;        // runs that overlap one another
+    explicit Bytes(const Tensor& t) : base(reinterpret_cast<int64_t>(t.data_ptr())), len(t.numel() == 0 ? 0 : t.element_size()) {
+        int order[8], n = 0;
+        TORCH_CHECK_VALUE(t.dim() <= 8, "a tensor has ", t.dim(), " dimensions");
+        for (int d = 0; d < t.dim(); ++d) {   // by their strides
+            if (t.size(d) <= 1) continue;
+            int i = n++;
+            for (; i > 0 && t.stride(order[i - 1]) > t.stride(d); --i) order[i] = order[i - 1];
+            order[i] = d;
+        }
+        for (int i = 0; i < n; ++i) {
+            const int64_t s = t.stride(order[i]) * static_cast<int64_t>(t.element_size());
+            itself |= s < extent();
+            if (s == 0) continue;   // the same bytes again
+            if (dims == 0 && s == len) {
+                len *= t.size(order[i]);
+            } else {
+                size[dims] = t.size(order[i]);
+                step[dims++] = s;
+            }
+        }
+    }
+    int64_t extent() const {
+        int64_t e = len;
+        for (int d = 0; d < dims; ++d) e += (size[d] - 1) * step[d];
+        return e;
+    }
+};
+// Whether two tensors share a byte.  `left` bounds the work on layouts that no
+// closed form covers; past it they count as sharing.
+bool share(const Bytes& a, const Bytes& b, int64_t& left) {
+    if (a.len == 0 || b.len == 0 || a.base + a.extent() <= b.base || b.base + b.extent() <= a.base) return false;
+    if (a.dims + b.dims == 0 || --left < 0) return true;
+    if (a.dims <= 1 && b.dims <= 1 && (a.dims == 0 || b.dims == 0 || a.step[0] == b.step[0])) {
+        // Runs i of a and j of b meet where -b.len < distance + (j - i) * step < a.len.
+        const int64_t step = a.dims ? a.step[0] : b.step[0], na = a.dims ? a.size[0] : 1, nb = b.dims ? b.size[0] : 1, d = b.base - a.base;
+        auto floor_div = [](int64_t x, int64_t y) { return x / y - (x % y < 0); };
+        return std::min(nb - 1, floor_div(a.len - 1 - d, step)) >= std::max(1 - na, -floor_div(d + b.len - 1, step));
+    }
+    const bool first = b.dims == 0 || (a.dims > 0 && a.size[a.dims - 1] <= b.size[b.dims - 1]);
+    Bytes one = first ? a : b;
+    const int64_t n = one.size[one.dims - 1], step = one.step[one.dims - 1];
+    --one.dims;
+    for (int64_t i = 0; i < n; ++i, one.base += step)
+        if (share(one, first ? b : a, left)) return true;
+    return false;
+}
+// A result that the caller gave is written while the inputs are still read, and
+// while other results are written: it shares no byte with them or within itself.
 void apart(const Tensor& result, std::initializer_list<const Tensor*> others, const char* what) {
-    for (const Tensor* t : others)
-        TORCH_CHECK_VALUE(result.numel() == 0 || t->numel() == 0 || t->data_ptr() != result.data_ptr(), what,
-                          " must not share its memory with an input or another result");
+    if (result.numel() == 0) return;
+    const Bytes r(result);
+    TORCH_CHECK_VALUE(!r.itself, what, " must not overlap itself");
+    for (const Tensor* t : others) {
+        if (!t->defined()) continue;
+        int64_t left = 1 << 16;
+        TORCH_CHECK_VALUE(!share(r, Bytes(*t), left), what, " must not share its memory with an input or another result");
+    }
 }
 
 // q, k, v, shared..., out, lse -> (out, lse)
@@ -195,9 +262,11 @@ PyObject* bias_fwd(PyObject*, PyObject* const* o, Py_ssize_t n) {
     TORCH_CHECK_VALUE(q.dim() == 3, "q must be [Tq, H, head_dim]");
     const Tensor out = result(o[3 + kShared], q, "out");
     TORCH_CHECK_VALUE(rows_of_heads(out), "out must be [T, H, head_dim] with contiguous heads");
-    apart(out, {&q, &k, &v}, "out");
     const Tensor lse = o[4 + kShared] == Py_None ? empty({q.size(1), q.size(0)}, q, at::kFloat) : tensor(o[4 + kShared], "lse");
-    Problem p(q, k, v, o + 3, lse);
+    const Shared in(o + 3);
+    if (o[3 + kShared] != Py_None) apart(out, {&q, &k, &v, &lse, &in.cu_q, &in.cu_k, &in.table, &in.buckets, &in.pos_q, &in.pos_k}, "out");
+    if (o[4 + kShared] != Py_None) apart(lse, {&q, &k, &v, &in.cu_q, &in.cu_k, &in.table, &in.buckets, &in.pos_q, &in.pos_k}, "lse");
+    Problem p(q, k, v, o + 3, in, lse);
     p.dev.add(out);
     int64_t bytes = 0;
     ragged_status s = g_lib.fwd_workspace(&p.a, &bytes);
@@ -219,16 +288,22 @@ PyObject* bias_bwd(PyObject*, PyObject* const* o, Py_ssize_t n) {
     TORCH_CHECK_VALUE(out.sizes() == q.sizes() && out.scalar_type() == q.scalar_type() && q.dim() == 3 && rows_of_heads(out),
                       "out must be [T, H, head_dim] with contiguous heads");
     TORCH_CHECK_VALUE(dout.sizes() == q.sizes() && dout.scalar_type() == q.scalar_type(), "dout must have the shape and dtype of out");
-    const Tensor& table = tensor(o[6 + 4], "table");
+    const Shared in(o + 6);
+    const Tensor& table = in.table;
     const Tensor dq = result(given[0], q, "dq"), dk = result(given[1], k, "dk"), dv = result(given[2], v, "dv");
     const Tensor dtable = result(given[3], table, "dtable");
     TORCH_CHECK_VALUE(dk.numel() == 0 || dk.strides() == dv.strides(), "dk and dv must have the same strides");
-    apart(dq, {&q, &k, &v, &out, &dout, &dk, &dv}, "dq");
-    apart(dk, {&q, &k, &v, &out, &dout, &dv}, "dk");
-    apart(dv, {&q, &k, &v, &out, &dout}, "dv");
-    apart(dtable, {&table}, "dtable");
+    auto given_apart = [&](int i, const Tensor& d, std::initializer_list<const Tensor*> results, const char* what) {
+        if (given[i] == Py_None) return;
+        apart(d, results, what);
+        apart(d, {&q, &k, &v, &out, &dout, &lse, &table, &in.cu_q, &in.cu_k, &in.buckets, &in.pos_q, &in.pos_k}, what);
+    };
+    given_apart(0, dq, {&dk, &dv, &dtable}, "dq");
+    given_apart(1, dk, {&dv, &dtable}, "dk");
+    given_apart(2, dv, {&dtable}, "dv");
+    given_apart(3, dtable, {}, "dtable");
     TORCH_CHECK_VALUE(dtable.is_contiguous(), "dtable must be contiguous with the shape and dtype of table");
-    Problem p(q, k, v, o + 6, lse);
+    Problem p(q, k, v, o + 6, in, lse);
     p.dev.add(dout);
     p.dev.add(out);
     if (!rows_of_heads(dout) || reinterpret_cast<uintptr_t>(dout.data_ptr()) % 16 != 0 || row_stride(dout) % 8 != 0)
@@ -252,10 +327,17 @@ PyObject* attn_weight(PyObject*, PyObject* const* o, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     arguments(n, 3 + kShared + 2);
     const Tensor &q = tensor(o[0], "q"), &k = tensor(o[1], "k"), &lse = tensor(o[2], "lse");
-    Problem p(q, k, k, o + 3, lse);
+    const Shared in(o + 3);
+    TORCH_CHECK_VALUE(q.dim() == 3 && k.dim() == 3, "q must be [Tq, H, head_dim], k [Tk, Hkv, head_dim]");
     const int64_t H = q.size(1), Tk = k.size(0);
     const Tensor prev = maybe(o[3 + kShared], "prev");
     const Tensor weight = o[4 + kShared] == Py_None ? empty({H, Tk}, k, at::kFloat) : tensor(o[4 + kShared], "weight");
+    if (o[4 + kShared] != Py_None) {
+        const bool in_place = prev.defined() && prev.data_ptr() == weight.data_ptr() && prev.strides() == weight.strides();
+        apart(weight, {&q, &k, &lse, &in.cu_q, &in.cu_k, &in.table, &in.buckets, &in.pos_q, &in.pos_k}, "weight");
+        if (prev.defined() && !in_place) apart(weight, {&prev}, "weight");
+    }
+    Problem p(q, k, k, o + 3, in, lse);
     const int64_t stride = H > 1 ? weight.stride(0) : Tk;
     for (const Tensor* t : {&weight, &prev}) {
         if (!t->defined()) continue;
