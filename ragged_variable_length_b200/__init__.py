@@ -363,11 +363,17 @@ def _on_stream(stream):
 _tc = None
 
 
-def _torchcall():
+def _load_torchcall():
     """The tensor side of the calls below (_torchcall), bound to the loaded library."""
     global _tc
     if _tc is None:
         import importlib
+
+        from . import build
+        path = build.torchcall_path()
+        if os.path.exists(path) and not build.torchcall_is_current(path):
+            raise RuntimeError("the _torchcall extension was built against another torch: build it again with "
+                               "`python -m ragged_variable_length_b200.build`")
         try:
             m = importlib.import_module(__name__ + "._torchcall")
         except ImportError as e:
@@ -394,7 +400,7 @@ def ragged_attn_bias_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_s
         with _on_stream(stream):
             return ragged_attn_bias_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table,
                                         buckets, pos_q, pos_k, scale, out, lse)
-    r = (_tc or _torchcall()).bias_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table, buckets,
+    r = (_tc or _load_torchcall()).bias_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table, buckets,
                                        pos_q, pos_k, scale, out, lse)
     if r.__class__ is int:
         _check(r)
@@ -415,7 +421,7 @@ def ragged_attn_bias_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v
         with _on_stream(stream):
             return ragged_attn_bias_bwd(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                                         max_seqlen_k, table, buckets, pos_q, pos_k, scale, dq, dk, dv, dtable)
-    r = (_tc or _torchcall()).bias_bwd(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+    r = (_tc or _load_torchcall()).bias_bwd(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
                                        table, buckets, pos_q, pos_k, scale, dq, dk, dv, dtable)
     if r.__class__ is int:
         _check(r)
@@ -434,7 +440,7 @@ def ragged_attn_weight(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, cu_s
         with _on_stream(stream):
             return ragged_attn_weight(q, k, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table,
                                       buckets, pos_q, pos_k, scale, prev, weight)
-    r = (_tc or _torchcall()).attn_weight(q, k, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table,
+    r = (_tc or _load_torchcall()).attn_weight(q, k, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table,
                                           buckets, pos_q, pos_k, scale, prev, weight)
     if r.__class__ is int:
         _check(r)
@@ -454,7 +460,7 @@ def ragged_evict(rows: Optional[torch.Tensor], weight: torch.Tensor, cu_seqlens:
     if stream is not None:
         with _on_stream(stream):
             return ragged_evict(rows, weight, cu_seqlens, max_seqlen, budget, sinks, recents, pos, total)
-    r = (_tc or _torchcall()).evict(rows, weight, cu_seqlens, max_seqlen, budget, sinks, recents, pos, total)
+    r = (_tc or _load_torchcall()).evict(rows, weight, cu_seqlens, max_seqlen, budget, sinks, recents, pos, total)
     if r.__class__ is int:
         _check(r)
     return r

@@ -85,6 +85,16 @@ def torchcall_path() -> str:
     return os.path.join(HERE, "_torchcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 
+def torchcall_is_current(path: str) -> bool:
+    """Whether the extension was built against this torch, whose C++ interface it calls (it holds that version as text)."""
+    import torch
+    try:
+        with open(path, "rb") as f:
+            return b"_torchcall for torch " + torch.__version__.encode() + b"\0" in f.read()
+    except OSError:
+        return False
+
+
 def build_torchcall(force: bool = False) -> str:
     """CPython extension with the tensor side of the position-bias and eviction calls (against torch's C++ headers)."""
     import sysconfig
@@ -92,7 +102,8 @@ def build_torchcall(force: bool = False) -> str:
     import torch
     out = torchcall_path()
     deps = [TORCHCALL_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))]
-    if not force and os.path.exists(out) and all(os.path.getmtime(out) >= os.path.getmtime(d) for d in deps):
+    if (not force and os.path.exists(out) and all(os.path.getmtime(out) >= os.path.getmtime(d) for d in deps)
+            and torchcall_is_current(out)):
         return out
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
@@ -100,7 +111,8 @@ def build_torchcall(force: bool = False) -> str:
     headers = [sysconfig.get_paths()["include"], f"{base}/include", f"{base}/include/torch/csrc/api/include",
                f"{cuda}/include"]
     subprocess.run(["g++", "-O2", "-std=c++17", "-Wall", "-Wno-attributes", "-shared", "-fPIC",
-                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                    f'-DRAGGED_TORCH_VERSION="{torch.__version__}"', f"-I{INCLUDE}",
                     *[x for h in headers for x in ("-isystem", h)], TORCHCALL_SRC, "-o", tmp, f"-L{base}/lib",
                     "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], check=True)
     os.replace(tmp, out)

@@ -416,4 +416,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torchcall", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__torchcall(void) { return PyModule_Create(&module); }
+// Of the torch that this was built against; the build and the binding look for it in the file.
+const char kBuiltFor[] = "_torchcall for torch " RAGGED_TORCH_VERSION;
+
+PyMODINIT_FUNC PyInit__torchcall(void) {
+    PyObject* m = PyModule_Create(&module);
+    if (m != nullptr && PyModule_AddStringConstant(m, "built_for", kBuiltFor + sizeof("_torchcall for torch ") - 1) != 0) Py_CLEAR(m);
+    return m;
+}
