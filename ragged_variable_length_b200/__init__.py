@@ -395,7 +395,10 @@ def ragged_attn_bias_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_s
     """Attention of ragged queries q [Tq, H, 64] over ragged keys and values [Tk, Hkv, 64] with the
     learned bias table [num_buckets, H] (bucket of the clamped relative position) -> (out [Tq, H, 64],
     lse float32 [H, Tq]).  f16 / bf16.  For self-attention pass the same cu_seqlens and positions twice;
-    without positions a sequence's queries are its last tokens (one new token against a cache)."""
+    without positions a sequence's queries are its last tokens (one new token against a cache).
+
+    This call and the three below record no autograd graph, and refuse inputs that require a gradient unless
+    grad mode is off, as it is under torch.no_grad() and in a torch.autograd.Function."""
     if stream is not None:
         with _on_stream(stream):
             return ragged_attn_bias_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, table,

@@ -8,6 +8,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/clone.h>
 #include <c10/cuda/CUDAStream.h>
@@ -254,6 +255,14 @@ void apart(const Tensor& result, std::initializer_list<const Tensor*> others, co
     }
 }
 
+// The calls record no graph: results that would silently lose theirs are refused.
+void no_graph(std::initializer_list<const Tensor*> inputs) {
+    if (!at::GradMode::is_enabled()) return;
+    for (const Tensor* t : inputs)
+        TORCH_CHECK_VALUE(!t->defined() || !t->requires_grad(), "an input requires a gradient, and this call records no graph: call it under "
+                          "torch.no_grad(), or in a torch.autograd.Function with ragged_attn_bias_bwd as its backward");
+}
+
 // q, k, v, shared..., out, lse -> (out, lse)
 PyObject* bias_fwd(PyObject*, PyObject* const* o, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -264,6 +273,7 @@ PyObject* bias_fwd(PyObject*, PyObject* const* o, Py_ssize_t n) {
     TORCH_CHECK_VALUE(rows_of_heads(out), "out must be [T, H, head_dim] with contiguous heads");
     const Tensor lse = o[4 + kShared] == Py_None ? empty({q.size(1), q.size(0)}, q, at::kFloat) : tensor(o[4 + kShared], "lse");
     const Shared in(o + 3);
+    no_graph({&q, &k, &v, &in.table});
     if (o[3 + kShared] != Py_None) apart(out, {&q, &k, &v, &lse, &in.cu_q, &in.cu_k, &in.table, &in.buckets, &in.pos_q, &in.pos_k}, "out");
     if (o[4 + kShared] != Py_None) apart(lse, {&q, &k, &v, &in.cu_q, &in.cu_k, &in.table, &in.buckets, &in.pos_q, &in.pos_k}, "lse");
     Problem p(q, k, v, o + 3, in, lse);
@@ -290,6 +300,7 @@ PyObject* bias_bwd(PyObject*, PyObject* const* o, Py_ssize_t n) {
     TORCH_CHECK_VALUE(dout.sizes() == q.sizes() && dout.scalar_type() == q.scalar_type(), "dout must have the shape and dtype of out");
     const Shared in(o + 6);
     const Tensor& table = in.table;
+    no_graph({&dout, &q, &k, &v, &out, &lse, &table});
     const Tensor dq = result(given[0], q, "dq"), dk = result(given[1], k, "dk"), dv = result(given[2], v, "dv");
     const Tensor dtable = result(given[3], table, "dtable");
     TORCH_CHECK_VALUE(dk.numel() == 0 || dk.strides() == dv.strides(), "dk and dv must have the same strides");
@@ -328,6 +339,7 @@ PyObject* attn_weight(PyObject*, PyObject* const* o, Py_ssize_t n) {
     arguments(n, 3 + kShared + 2);
     const Tensor &q = tensor(o[0], "q"), &k = tensor(o[1], "k"), &lse = tensor(o[2], "lse");
     const Shared in(o + 3);
+    no_graph({&q, &k, &lse, &in.table});
     TORCH_CHECK_VALUE(q.dim() == 3 && k.dim() == 3, "q must be [Tq, H, head_dim], k [Tk, Hkv, head_dim]");
     const int64_t H = q.size(1), Tk = k.size(0);
     const Tensor prev = maybe(o[3 + kShared], "prev");
@@ -360,6 +372,7 @@ PyObject* evict(PyObject*, PyObject* const* o, Py_ssize_t n) {
     arguments(n, 9);
     const Tensor rows = maybe(o[0], "rows"), pos = maybe(o[7], "pos");
     const Tensor &weight = tensor(o[1], "weight"), &cu = tensor(o[2], "cu_seqlens"), &budget = tensor(o[4], "budget");
+    no_graph({&rows, &weight});
     TORCH_CHECK_VALUE(weight.scalar_type() == at::kFloat && weight.dim() == 2 && (weight.size(1) <= 1 || weight.stride(1) == 1),
                       "weight must be float32 [H, T] with unit innermost stride");
     const int64_t H = weight.size(0), T = weight.size(1), max_seqlen = integer(o[3]);
