@@ -123,7 +123,7 @@ ragged_status check_workspace(const void* ws, int64_t have, int64_t need) {
     return RAGGED_OK;
 }
 
-DeviceFlags g_bias_fwd_smem[2], g_bias_bwd_q_smem[2], g_bias_bwd_kv_smem[2], g_bias_weight_smem[2];
+DeviceFlags g_bias_fwd_smem[2], g_bias_bwd_q_smem[2][2], g_bias_bwd_kv_smem[2], g_bias_weight_smem[2];
 template <typename T>
 constexpr int kTypeSlot = std::is_same<T, __half>::value ? 0 : 1;
 
@@ -251,7 +251,9 @@ ragged_status launch_bias_fwd(const ragged::bias::Problem& p, uint16_t* out, int
 template <typename T>
 ragged_status launch_bias_bwd(const ragged::bias::Problem& p, ragged::bias::BwdArgs a, cudaStream_t s) {
     using namespace ragged::bias;
-    ragged_status st = ensure_smem(bias_bwd_q_kernel<T>, kBwdQSmemMax, g_bias_bwd_q_smem[kTypeSlot<T>]);
+    const bool one = p.max_k <= kTile;   // every row's keys are in one tile
+    auto q_kernel = one ? bias_bwd_q_kernel<T, true> : bias_bwd_q_kernel<T, false>;
+    ragged_status st = ensure_smem(q_kernel, kBwdQSmemMax, g_bias_bwd_q_smem[kTypeSlot<T>][one]);
     if (st == RAGGED_OK) st = ensure_smem(bias_bwd_kv_kernel<T>, bwd_kv_smem_bytes(kMaxDistance, kSpan), g_bias_bwd_kv_smem[kTypeSlot<T>]);
     if (st != RAGGED_OK) return st;
     const int64_t avg_q = average_length(p.B, p.max_q, p.lse_stride), avg_k = std::max<int64_t>(1, p.max_k * avg_q / p.max_q);
@@ -273,7 +275,7 @@ ragged_status launch_bias_bwd(const ragged::bias::Problem& p, ragged::bias::BwdA
     }
     cfg.gridDim = bias_grid(a.q_tiles, (p.H + a.heads - 1) / a.heads, p.B);
     cfg.dynamicSmemBytes = bwd_q_smem_bytes(p.D, p.num_buckets, a.span);
-    st = cuda_check(cudaLaunchKernelEx(&cfg, bias_bwd_q_kernel<T>, p, a), "query gradient launch");
+    st = cuda_check(cudaLaunchKernelEx(&cfg, q_kernel, p, a), "query gradient launch");
     if (st != RAGGED_OK) return st;
     a.span = bias_span(p.D, bwd_kv_fixed_bytes(), 3);
     a.heads = a.parts > 1 ? 1 : heads_per_cta(p.B * tiles128(avg_k), p.Hkv, (avg_q + kTile - 1) / kTile * p.group, slots);

@@ -10,15 +10,21 @@
 // transposed scores).  Each recomputes S and dP, 7 products instead of 5.  In
 // f16 a small kernel before them reads the size of V (below).
 //
-// delta is formed from O as it was stored, so the half step of O's rounding is
-// in dS, P (dO . err O), and shows in the table's gradient, which sums dS in
-// fp32: 3e-4 of its size in f16, 3e-3 in bf16, against 2e-4 and 2e-3 for sums
-// from an unrounded O, which nobody keeps.
+// delta is formed from O as it was stored, so it is off by dO . err O, which
+// where V lies far from 0 is many times u of dS (values of mean 4 and 4,000
+// keys: the table's gradient off by 190 u of its norm, dQ by 8, dK by 2; u is
+// half a step of the type).  A row's dS add up to 0, so what they add up to is
+// what delta was off by: the query kernel adds them up, hands the exact delta to
+// the key kernel, and takes the difference out of the table's sums of flat
+// tiles, whose probabilities it adds up too (dK 0.6 u, the table 5 u; values of
+// mean 0: 0.6 and 0.4 u).  dQ keeps it: its products are done by then.  Where a
+// row's keys are one tile, delta is sum P dP from the start, and nothing is off.
+// The two sums cost 3 % of the gradients.
 //
 // Measured, both kernels and the sums: 64 sequences of 173 to 403 tokens, 12
-// heads, bf16, positions with gaps: 376 us (memory and products allow 40); 2
-// of 3,279 to 4,099, 8 over 2 heads, f16: 441 us (117); 4 of 79 to 197, 6
-// heads, f16: 29 us.
+// heads, bf16, positions with gaps: 374 us (memory and products allow 40); 2
+// of 3,279 to 4,099, 8 over 2 heads, f16: 457 us (117); 4 of 79 to 197, 6
+// heads, f16: 30 us.
 //
 // Both have eight row warps: two threads share a row, one for each half of a
 // tile's 64 columns (nothing is reduced along a row but the table's sums, which
@@ -163,6 +169,15 @@ __device__ __forceinline__ void probabilities(const Bias16& t, const Problem& p,
     }
 }
 
+__device__ __forceinline__ float sum32(const float (&x)[32]) {
+    uint64_t sum[4];   // chains of their own
+#pragma unroll
+    for (int c = 0; c < 16; ++c) sum[c & 3] = c < 4 ? f2(x[2 * c], x[2 * c + 1]) : f2_add(sum[c & 3], f2(x[2 * c], x[2 * c + 1]));
+    float u, v;
+    f2_split(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), u, v);
+    return u + v;
+}
+
 __host__ __device__ constexpr int bwd_q_fixed_bytes(int num_buckets) {
     return 1024 + kBwdQStages * 2 * kTileBytes + (num_buckets + 1) * 4 * kBwdRows + 4 * kChunk;
 }
@@ -217,7 +232,8 @@ __device__ __forceinline__ int value_exp(const Problem& p, const BwdArgs& a, int
     return top == kNoExp ? 0 : top;
 }
 
-// Query rows: dQ, delta, and each tile's sums for the table's gradient.
+// Query rows: dQ, delta, and each tile's sums for the table's gradient.  ONE:
+// no sequence has more keys than a tile.
 //
 // The table's sums have a column of shared memory per thread, so that no two
 // threads meet and the order is fixed; each element is one read-modify-write
@@ -231,10 +247,10 @@ __device__ __forceinline__ int value_exp(const Problem& p, const BwdArgs& a, int
 // the time of one with A in shared memory, and the room goes to the table's
 // sums.  S of the next tile is computed while dS of this one is, dP of the
 // next one while its probabilities are.
-template <typename T>
+template <typename T, bool ONE>
 __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Problem p, const BwdArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    // kv_full[2], kv_done[2], qd_full, s_full, dp_full, a_full, b_full, dq_full, done
+    // kv_full[2], kv_done[2] from 3, delta_full, qd_full, s_full, dp_full, a_full, b_full, dq_full, done
     constexpr int kBars = 13;
     __shared__ __align__(8) uint64_t s_bar[kBars];
     __shared__ uint16_t s_tab[kMaxBuckets + 1];
@@ -272,12 +288,12 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
     const uint32_t bar0 = smem_addr(&s_bar[0]);
     auto kv_full = [&](uint32_t g) { return bar0 + 8u * (g % kBwdQStages); };
     auto kv_done = [&](uint32_t g) { return bar0 + 8u * (3 + g % kBwdQStages); };
-    const uint32_t qd_full = bar0 + 48, s_full = bar0 + 56, dp_full = bar0 + 64, a_full = bar0 + 72, b_full = bar0 + 80, dq_full = bar0 + 88, done = bar0 + 96;
+    const uint32_t delta_full = bar0 + 40, qd_full = bar0 + 48, s_full = bar0 + 56, dp_full = bar0 + 64, a_full = bar0 + 72, b_full = bar0 + 80, dq_full = bar0 + 88, done = bar0 + 96;
     constexpr uint32_t dp_col = kTile, dq_col = 2 * kTile, q_col = 3 * kTile, do_col = 3 * kTile + 32;
     const Wait wait{&s_fail};
 
     if (warp == kBwdLoadWarp) {
-        if (lane < kBars) mbar_init(bar0 + 8 * lane, lane < 3 ? 32 : lane == 6 || lane == 9 || lane == 10 ? kBwdRows : 1);
+        if (lane < kBars) mbar_init(bar0 + 8 * lane, lane < 3 ? 32 : lane == 5 || lane == 6 || lane == 9 || lane == 10 ? kBwdRows : 1);
         if (lane == 0) s_fail = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         __syncwarp();
@@ -382,7 +398,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
             for (int c = 0; c < 4; ++c) {
                 qw[c] = valid ? __ldg(qp + c) : make_uint4(0, 0, 0, 0);
                 dw[c] = valid ? __ldg(dp + c) : make_uint4(0, 0, 0, 0);
-                ow[c] = valid ? __ldg(op + c) : make_uint4(0, 0, 0, 0);
+                if constexpr (!ONE) ow[c] = valid ? __ldg(op + c) : make_uint4(0, 0, 0, 0);
             }
             if (valid) lse = p.lse[h * p.lse_stride + t_row];
         };
@@ -401,18 +417,28 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
         const uint8_t* id_row = ids + (t.row >> 1);
         bool ok = true;
         uint32_t g = 0;
-        float undo = 1.f, far_left = 0.f, far_right = 0.f;
+        float undo = 1.f, delta = 0.f, far_left = 0.f, far_right = 0.f, p_left = 0.f, p_right = 0.f, near_sum = 0.f;
         // From head i to the next: the table's sums of head i, its dQ once its last product has
         // finished, and the next head's bias and rows.
         auto change = [&](int i, bool more) {
             if (i >= 0) {
+                if (more) {
+                    load_row(h0 + i + 1);
+                    if (has_entry) entry = __ldg(column + i + 1);
+                }
+                if constexpr (!ONE) {   // what delta was short of: dS of a row adds up to 0
+                    s_delta[half][r] = far_left + far_right + near_sum;
+                    rows_barrier<kBwdRows>();
+                    const float sum = s_delta[0][r] + s_delta[1][r];
+                    far_left = fmaf(-sum, p_left, far_left);
+                    far_right = fmaf(-sum, p_right, far_right);
+                    delta = fmaf(sum, undo, delta);
+                }
+                if (half == 0 && valid) a.delta[(h0 + i) * p.lse_stride + t_row] = delta;
                 *reinterpret_cast<float*>(acc_row + ids[0] * (4 * kBwdRows)) += far_left;
                 *reinterpret_cast<float*>(acc_row + ids[t.last] * (4 * kBwdRows)) += far_right;
                 if (half == 0) s_undo[r] = valid ? undo : 0.f;
-                if (more) {
-                    load_row(h0 + i + 1);
-                    if (has_entry) s_tab[tid] = __ldg(column + i + 1);
-                }
+                if (more && has_entry) s_tab[tid] = entry;
                 rows_barrier<kBwdRows>();   // sums complete, the last head's entries no longer read
                 for (int n = warp; n < p.num_buckets; n += 8) {   // each thread's sums, unscaled, in a fixed order
                     float sum = 0.f;
@@ -449,13 +475,16 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
             float d = 0.f, ss = 0.f;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const uint32_t ys[4] = {dw[c].x, dw[c].y, dw[c].z, dw[c].w}, xs[4] = {ow[c].x, ow[c].y, ow[c].z, ow[c].w};
+                const uint32_t ys[4] = {dw[c].x, dw[c].y, dw[c].z, dw[c].w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     w[4 * c + k] = ys[k];
                     const float d0 = to_float<T>(static_cast<uint16_t>(ys[k])), d1 = to_float<T>(static_cast<uint16_t>(ys[k] >> 16));
-                    d = fmaf(to_float<T>(static_cast<uint16_t>(xs[k])), d0, d);
-                    d = fmaf(to_float<T>(static_cast<uint16_t>(xs[k] >> 16)), d1, d);
+                    if constexpr (!ONE) {
+                        const uint32_t xs[4] = {ow[c].x, ow[c].y, ow[c].z, ow[c].w};
+                        d = fmaf(to_float<T>(static_cast<uint16_t>(xs[k])), d0, d);
+                        d = fmaf(to_float<T>(static_cast<uint16_t>(xs[k] >> 16)), d1, d);
+                    }
                     if constexpr (kScaled<T>) ss = fmaf(d0, d0, fmaf(d1, d1, ss));
                 }
             }
@@ -463,7 +492,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
             tmem_wait_st();
             fence_before_sync();
             mbar_arrive(qd_full);
-            s_delta[half][r] = d;
+            if constexpr (!ONE) s_delta[half][r] = d;
             if constexpr (kScaled<T>) s_norm[half][r] = ss;
             rows_barrier<kBwdRows>();   // entries, deltas and cleared sums are there
         };
@@ -471,8 +500,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
         if constexpr (kScaled<T>) wait_for_last();   // the value kernel's exponents
         for (int i = 0; i < nh; ++i) {
             const int h = h0 + i;
-            const float delta = s_delta[0][r] + s_delta[1][r];
-            if (half == 0 && valid) a.delta[h * p.lse_stride + t_row] = delta;
+            if constexpr (!ONE) delta = s_delta[0][r] + s_delta[1][r];
             float rs = 1.f;   // dS is kept times rs
             undo = 1.f;
             if constexpr (kScaled<T>) {
@@ -498,8 +526,9 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                     if (half == 0) a.log_sum[h * p.lse_stride + t_row] = ls;
                 }
             }
-            const uint64_t r2 = f2(rs, rs), nd2 = f2(-delta * rs, -delta * rs);
-            far_left = far_right = 0.f;
+            const uint64_t r2 = f2(rs, rs);
+            uint64_t nd2 = f2(-delta * rs, -delta * rs);
+            far_left = far_right = p_left = p_right = near_sum = 0.f;
             for (int tile = 0; tile < nt; ++tile, ++g) {
                 if (tile % kChunkTiles == 0 && (tile > 0 || (i > 0 && nt > kChunkTiles))) {
                     cols.load(tile * kTile, s.k_len, key_at);
@@ -525,8 +554,31 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                         for (int c = 0; c < 32; ++c)
                             if (c >= left) x[c] = 0.f;
                     }
+                    if constexpr (!ONE) {
+                        if (kind == kLeft) p_left += sum32(x);
+                        else if (kind == kRight) p_right += sum32(x);
+                    }
                 }
                 ok = ok && wait.warp(dp_full, g & 1);
+                if constexpr (ONE) {   // the whole row is here: delta = sum P dP
+                    float sum = 0.f;
+                    if (ok && warp_rows) {
+                        fence_after_sync();
+                        float y[32];
+                        tmem_ld32(t_lane + dp_col + half * 32, y);
+                        uint64_t two = f2(0.f, 0.f);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) two = f2_fma(f2(x[2 * c], x[2 * c + 1]), f2(y[2 * c], y[2 * c + 1]), two);
+                        float u, v;
+                        f2_split(two, u, v);
+                        sum = u + v;
+                    }
+                    s_delta[half][r] = sum;
+                    mbar_arrive(delta_full);
+                    ok = ok && wait.warp(delta_full, i & 1);
+                    delta = s_delta[0][r] + s_delta[1][r];
+                    nd2 = f2(-delta * rs, -delta * rs);
+                }
                 if (ok && warp_rows) {
                     fence_after_sync();
                     float y[32];
@@ -543,15 +595,13 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                 fence_before_sync();
                 mbar_arrive(b_full);
                 if (ok && warp_rows) {   // the table's share, behind the hand-over
-                    if (kind == kLeft || kind == kRight) {
-                        uint64_t sum = f2(x[0], x[1]);
-#pragma unroll
-                        for (int c = 1; c < 16; ++c) sum = f2_add(sum, f2(x[2 * c], x[2 * c + 1]));
-                        float u, v;
-                        f2_split(sum, u, v);
-                        if (kind == kLeft) far_left += u + v;
-                        else far_right += u + v;
+                    const float sum = sum32(x);
+                    if (kind == kLeft) {
+                        far_left += sum;
+                    } else if (kind == kRight) {
+                        far_right += sum;
                     } else {
+                        near_sum += sum;
                         // Addresses first: a load of the next one could not pass a store to the sums.
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
