@@ -419,7 +419,9 @@ RAGGED_API ragged_status ragged_pipeline_graph_destroy(ragged_pipeline_graph *gr
  *                    queries are the last ones: query i at i + L_k - L_q.
  *   lse              device float; lse[h * lse_stride + t].  Written by
  *                    ragged_attn_bias_fwd, read by the others.  lse_stride is
- *                    at least the number of query rows (cu_seqlens_q[B]).
+ *                    at least the number of query rows (cu_seqlens_q[B]); a
+ *                    sequence that ends past it is skipped and
+ *                    RAGGED_DEV_BAD_SEQLENS is set.
  */
 typedef struct ragged_bias_attn {
     const void *q, *k, *v;
@@ -486,7 +488,8 @@ RAGGED_API ragged_status ragged_attn_bias_bwd(const ragged_bias_attn *problem, c
  * over the queries of its sequence, with lse as ragged_attn_bias_fwd wrote it.
  * weight and prev: device float, element [h * weight_stride + key row]; prev
  * may be NULL (0) or weight itself.  weight_stride is at least the number of
- * key rows.
+ * key rows; a sequence whose keys end past it is skipped and
+ * RAGGED_DEV_BAD_SEQLENS is set.
  */
 RAGGED_API ragged_status ragged_attn_weight(const ragged_bias_attn *problem, const float *prev, float *weight,
                                             int64_t weight_stride, void *stream);

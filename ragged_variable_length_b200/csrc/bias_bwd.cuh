@@ -1074,7 +1074,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int nh = min(heads_per_cta, p.H - h0);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Seq s;
-    if (!read_pair(p, b, s) || k0 >= s.k_len) return;
+    if (!read_pair(p, b, s) || k0 >= s.k_len || !keys_held(s, weight_stride)) return;
     if (s.q_len == 0) {   // nothing to add
         for (int i = tid; i < nh * kQTile; i += kThreads) {
             const int r = k0 + i % kQTile;

@@ -53,7 +53,18 @@ struct Seq {
 __device__ __forceinline__ bool read_pair(const Problem& p, int b, Seq& s) {
     bool ok = read_sequence(p.cu_q, b, p.max_q, s.q_start, s.q_len);
     ok &= read_sequence(p.cu_k, b, p.max_k, s.k_start, s.k_len);
+    if (ok && static_cast<int64_t>(s.q_start) + s.q_len > p.lse_stride) {   // rows that lse, and the scratch of its size, do not hold
+        raise_status(RAGGED_DEV_BAD_SEQLENS);
+        ok = false;
+    }
     return ok;
+}
+
+// Whether the sequence's keys lie in rows of `held` elements.
+__device__ __forceinline__ bool keys_held(const Seq& s, int64_t held) {
+    if (static_cast<int64_t>(s.k_start) + s.k_len <= held) return true;
+    raise_status(RAGGED_DEV_BAD_SEQLENS);
+    return false;
 }
 
 template <typename T>

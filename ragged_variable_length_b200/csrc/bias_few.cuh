@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(32 * NW)
     const int splits = gridDim.x, rank = blockIdx.x;
     Few<T, MT, NW, true> f;
     f.z = blockIdx.y;
-    if (!read_pair(p, blockIdx.z, f.s) || f.s.k_len == 0) return;
+    if (!read_pair(p, blockIdx.z, f.s) || f.s.k_len == 0 || !keys_held(f.s, weight_stride)) return;
     const int blocks = (f.s.k_len + kFewKeys - 1) / kFewKeys;
     const int per = (blocks + splits * NW - 1) / (splits * NW);
     const int begin = min(blocks, rank * per * NW), end = min(blocks, (rank + 1) * per * NW);
