@@ -79,8 +79,8 @@ int64_t average_length(int64_t B, int64_t longest, int64_t rows) {
 
 // Parts that a key row's queries are split into, where key tiles and heads
 // alone leave SMs without work and each CTA has many query tiles to walk.  (2
-// sequences of 3,279 to 4,099, 8 over 2 heads: 332 + 5 us for the key rows and
-// the parts' sum, 515 us in one part.)
+// sequences of 3,279 to 4,099, 8 over 2 heads: 223 + 5 us for the key rows and
+// the parts' sum, 341 us in one part, each kernel timed by itself.)
 int64_t bwd_parts(const ragged_bias_attn* a) {
     const int64_t avg_q = average_length(a->B, a->max_seqlen_q, a->lse_stride);
     const int64_t avg_k = std::max<int64_t>(1, a->max_seqlen_k * avg_q / a->max_seqlen_q);
@@ -134,7 +134,9 @@ dim3 bias_grid(int64_t tiles, int heads, int B) {
 // Heads that one CTA walks over: the number with the least time, in units of a
 // tile's, of a grid of `row_tiles` per head over `slots` CTAs at a time.  A CTA's
 // set-up costs about kSetup tiles, a head's start and end kHead; half a wave
-// stands for the uneven end.  (Forward, 64 sequences of 173 to 403 tokens, 12
+// stands for the uneven end.  The costs are the forward kernel's; the gradient
+// kernels' heads cost four times that, and weigh more the more a CTA has of
+// them, which this rule does not see.  (Forward, 64 sequences of 173 to 403 tokens, 12
 // heads: 118, 112, 109, 119, 127, 141 us with 1, 2, 3, 4, 6, 12 heads; 512 of 79
 // to 118, 6 heads: 86, 74, 70, 88, 65 us with 1, 2, 3, 4, 6.)
 int heads_per_cta(int64_t row_tiles, int64_t heads, int64_t col_tiles, int64_t slots) {

@@ -237,9 +237,12 @@ __device__ __forceinline__ int value_exp(const Problem& p, const BwdArgs& a, int
 //
 // The table's sums have a column of shared memory per thread, so that no two
 // threads meet and the order is fixed; each element is one read-modify-write
-// there, after the read of its bucket.  They bound the kernel: 2,470 of a
-// tile's 4,400 cycles where the distances are inside the map, 470 where one sum
-// in a register serves the whole tile.
+// there, after the read of its bucket.  With all places taken a tile costs a CTA
+// 3.1 us where the distances are inside the map, most of it these sums, and 1.8
+// where one sum in a register serves the whole tile; a head costs 11.5 us besides,
+// because its change waits for the products, sums up the table, stores dQ and
+// brings Q and dO before the next head's first product: seven heads of 80 us in
+// all, next to 37 tiles, for 64 sequences of 173 to 403 tokens (238 us).
 // grid (query tiles, groups of heads, B), two CTAs per SM where the table is small.
 //
 // TMEM (256 columns): S, dP (each half replaced in place by its dS), dQ, and
@@ -1026,9 +1029,9 @@ __global__ void __launch_bounds__(256) bias_bwd_parts_kernel(const Problem p, co
 // weight[h, j] = prev[h, j] + sum_i exp(s[i, j] - lse_i): key rows, transposed
 // scores, summed along each thread's row.  grid (key tiles, groups of heads,
 // B), three CTAs per SM; TMEM: two score buffers.  Bound by the row warps'
-// instructions.  512 sequences of 79 to 118 tokens, 6 heads, f16: 60 us, 352 of
-// up to 36, 12 heads: 39, 11 of up to 2,878, 48 heads: 105; with two CTAs and
-// more registers 53, 48 and 120.  The reads alone are 12 us of the first.
+// instructions.  512 sequences of 79 to 118 tokens, 6 heads, f16: 58 us, 352 of
+// up to 36, 12 heads: 37; with two CTAs and more registers (an earlier state,
+// 60 and 39 us with three) 53 and 48.  The reads alone are 12 us of the first.
 // ---------------------------------------------------------------------------
 
 constexpr int kWeightStages = 3;

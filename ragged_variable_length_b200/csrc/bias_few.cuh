@@ -16,7 +16,7 @@
 //
 // Measured: 32 sequences of 4,096 to 8,192 keys, one query, 16 over 4 heads,
 // bf16: 40 us, 5.5 TB/s of keys and values; their weights, with those so far
-// read and written: 38 us.  One sequence of 577, 12 heads, f16: 7.2 and 5.1 us,
+// read and written: 36 us.  One sequence of 577, 12 heads, f16: 7.4 and 5.1 us,
 // a launch and two dependent reads.
 #pragma once
 

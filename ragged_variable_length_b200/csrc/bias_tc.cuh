@@ -344,22 +344,27 @@ __device__ __forceinline__ void bias_add(const Bias16& t, int kind, const int* o
 // sum and O rescaled, only when a tile exceeds it by 2^8.  P is rounded to the
 // 16-bit type of V: the product's operands must have one type, and the
 // rounding (half a step, independent per element) adds about as much to the
-// result as its own final rounding does; the sum that divides is of the
-// unrounded P.
+// result as its own final rounding does (bf16: 0.0023 of the result's norm
+// instead of 0.0017); the sum that divides is of the unrounded P.  A second
+// operand for the residual, as the kernels for few rows have it, costs 23 and
+// 18 % in bf16 (121 instead of 98 us, 680 instead of 576, for the first two
+// shapes below), because the row warps form it.
 //
-// Bound by the row warps' instructions, not by the tensor core or memory: per
-// element one table entry is read from shared memory, and per tile of 128 x 64
-// a CTA takes 2,250 cycles where every distance is past one end of the map
-// (exponentials 900 to 1,300 of them) and more where the entries are gathered.
+// Bound by the latency of the row warps' work, not by the tensor core or memory
+// (issue slots a third busy): per element one table entry is read from shared
+// memory.  With all places taken, a tile of 128 x 64 costs a CTA 1.3 us where
+// every distance is past one end of the map and 1.6 where the entries are
+// gathered, a head 2.3 us besides; the last CTAs of a grid end later than an even
+// split would (four waves: some 20 %).
 // Measured: 64 sequences of 173 to 403 tokens, 12 heads, bf16, positions with
-// gaps: 104 us, the least that memory and products allow is 18; 2 of 4,914 to
-// 8,191, 12 over 4 heads: 580 us, 437 TFLOP/s; 4 of 79 to 118, 6 heads, f16:
+// gaps: 98 us, the least that memory and products allow is 18; 2 of 4,914 to
+// 8,191, 12 over 4 heads: 576 us, 433 TFLOP/s; 4 of 79 to 118, 6 heads, f16:
 // 8.0 us, of which most is the launch and one chain of dependent reads.
 //
-// Tried against this: eight row warps that share each tile (half the columns
-// each): 112 and 651 us for the first two; two groups of row warps on two heads
-// with registers moved between roles: 220 and 1,069 us; waits without the sleep
-// hint: 110 and 573 us.
+// Tried against an earlier state of this (104 and 580 us for the first two): eight
+// row warps that share each tile (half the columns each): 112 and 651 us; two
+// groups of row warps on two heads with registers moved between roles: 220 and
+// 1,069 us; waits without the sleep hint: 110 and 573 us.
 // ---------------------------------------------------------------------------
 
 constexpr int kFwdK = 3, kFwdV = 5;
