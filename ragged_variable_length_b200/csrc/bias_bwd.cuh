@@ -430,11 +430,12 @@ __global__ void __launch_bounds__(kBwdThreads, 2) bias_bwd_q_kernel(const Proble
                     if (has_entry) entry = __ldg(column + i + 1);
                 }
                 if constexpr (!ONE) {   // what delta was short of: dS of a row adds up to 0
+                    if (nt == 1) rows_barrier<kBwdRows>();   // the deltas have been read (else some tile's products waited for that)
                     s_delta[half][r] = far_left + far_right + near_sum;
                     rows_barrier<kBwdRows>();
                     const float sum = s_delta[0][r] + s_delta[1][r];
-                    far_left = fmaf(-sum, p_left, far_left);
-                    far_right = fmaf(-sum, p_right, far_right);
+                    if (p_left != 0.f) far_left = fmaf(-sum, p_left, far_left);   // (a row's NaN keeps to the buckets of its pairs)
+                    if (p_right != 0.f) far_right = fmaf(-sum, p_right, far_right);
                     delta = fmaf(sum, undo, delta);
                 }
                 if (half == 0 && valid) a.delta[(h0 + i) * p.lse_stride + t_row] = delta;

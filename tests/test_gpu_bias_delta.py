@@ -50,3 +50,21 @@ def test_values_far_from_zero(lens, D, H, Hkv, dtype):
         want = good[name][0] + (left if name == "dtable" else 0.0)
         error = ((got[name].double().cpu() - want).norm() / want.norm()).item()
         assert error <= (u + 2.0 ** -12 if name == "dtable" else 2 * u), (name, error / u)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_short_sequences_beside_a_long_one(dtype):
+    """Sequences of one tile in a batch whose bound is longer: the same bits every time, and dk as it is without the rounding
+    of out."""
+    lens = [1 + (29 * i) % 64 for i in range(120)] + [400]
+    s = ref.problem(lens, lens, 4, 2, dtype, 32, 128, layout="rows", extra=0)
+    s["base"]["kv"][:, 1] += 16.0
+    q, k, v, args, where = ref.on_gpu(s)
+    out, lse = rv.ragged_attn_bias_fwd(q, k, v, *args, **where)
+    do = s["dout"].cuda()
+    first = rv.ragged_attn_bias_bwd(do, q, k, v, out, lse, *args, **where)
+    for _ in range(20):
+        for a, b in zip(first, rv.ragged_attn_bias_bwd(do, q, k, v, out, lse, *args, **where)):
+            assert torch.equal(a, b)
+    want = ref.attention(s, s["dout"])["dk"][0]
+    assert ((first[1].double().cpu() - want).norm() / want.norm()).item() <= torch.finfo(dtype).eps
